@@ -1,4 +1,5 @@
-"""Python binding of the GB300 GQA decode library (``include/gqa_decode.h``).
+"""Python binding of the GB300 GQA decode library (``include/gqa_decode.h`` and
+``include/gqa_shared_keys.h``).
 
 Argument marshalling only: every function below turns PyTorch tensors into
 the plain pointers and sizes of the C entry point of the same name and calls
@@ -15,7 +16,7 @@ import re
 import threading
 from typing import Optional
 
-from .build import HEADER, LIB
+from .build import HEADER, LIB, SHARED_KEYS_HEADER
 
 GQA_OK = 0
 GQA_ERR_INVALID_ARG = 1
@@ -100,12 +101,23 @@ def load_library(path: str) -> ctypes.CDLL:
     L.gqa_decode_plan.restype = I
     L.gqa_decode_selftest_timeout.argtypes = [ctypes.c_uint, P]
     L.gqa_decode_selftest_timeout.restype = I
+    L.gqa_cross_workspace_size.argtypes = [D]
+    L.gqa_cross_workspace_size.restype = SZ
+    L.gqa_cross_attn.argtypes = [D, P, P, P, P, P, P, P, SZ, P]
+    L.gqa_cross_attn.restype = I
+    L.gqa_prefix_workspace_size.argtypes = [D, I]
+    L.gqa_prefix_workspace_size.restype = SZ
+    L.gqa_prefix_attn.argtypes = [D, P, P, P, P, I, P, P, P, P, P, P, SZ, P]
+    L.gqa_prefix_attn.restype = I
+    L.gqa_shared_keys_plan.argtypes = [D, I, P, I, ctypes.POINTER(I), ctypes.POINTER(I), ctypes.POINTER(I), P, I64,
+                                       ctypes.POINTER(I64)]
+    L.gqa_shared_keys_plan.restype = I
     return L
 
 
-def header_functions():
-    """Names of the functions ``include/gqa_decode.h`` declares."""
-    with open(HEADER) as f:
+def header_functions(header: str = HEADER):
+    """Names of the functions a header (``include/gqa_decode.h``) declares."""
+    with open(header) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(gqa_[a-z_0-9]+)\s*\(", text)))
@@ -299,3 +311,154 @@ def decode(q, k_cache, v_cache, seqlens, *, num_splits: int = 0, scale: float = 
     gqa_decode_attn(q, k_cache, v_cache, seqlens, out, lse, num_splits, ws, scale=scale, causal=causal,
                     reduction=reduction, stream=stream)
     return out, lse
+
+
+def _check_devices(stream, **tensors):
+    """Every tensor on one CUDA device, which the call then makes current: the
+    C library computes on the current device."""
+    first = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            raise ValueError(f"{name} is on {t.device}, not on {first}")
+    device = getattr(stream, "device", None)
+    if device is not None and device != first:
+        raise ValueError(f"the stream is on {device}, not on {first}")
+    return first
+
+
+def _on_device(device, call):
+    """call() with `device` current."""
+    import torch
+
+    if torch.cuda.current_device() == device.index:
+        return call()
+    with torch.cuda.device(device):
+        return call()
+
+
+def _outputs_ok(q, out, lse, workspace):
+    import torch
+
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous fp32 {tuple(q.shape[:3])} tensor")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
+def _lengths_ok(name, t, n):
+    import torch
+
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous int32")
+
+
+def _bytes_of(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def gqa_cross_workspace_size(q, k, *, out_dtype=None) -> int:
+    """Bytes gqa_cross_attn needs for q [B, nq, Hq, d] against keys [B, S_max, Hkv, d]."""
+    desc = make_desc(q, k, out_dtype=out_dtype)
+    return _on_device(_check_devices(None, q=q, k=k),
+                      lambda: int(lib().gqa_cross_workspace_size(ctypes.byref(desc))))
+
+
+def gqa_cross_attn(q, k, v, kv_lens, out, lse=None, workspace=None, *, scale: float = 0.0, stream=None) -> None:
+    """Cross attention into ``out`` (and ``lse``); see gqa_cross_attn in ``include/gqa_shared_keys.h``."""
+    _inputs_ok(q, k, v, kv_lens)
+    _lengths_ok("kv_lens", kv_lens, q.shape[0])
+    _outputs_ok(q, out, lse, workspace)
+    device = _check_devices(stream, q=q, k=k, v=v, kv_lens=kv_lens, out=out, lse=lse, workspace=workspace)
+    desc = make_desc(q, k, scale=scale, out_dtype=out.dtype)
+    rc = _on_device(device, lambda: lib().gqa_cross_attn(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(out), _ptr(lse), _ptr(workspace),
+        _bytes_of(workspace), _stream(stream)))
+    _check(rc, "gqa_cross_attn")
+
+
+def gqa_prefix_workspace_size(q, k_prefix, k_cache, *, causal: bool = False, out_dtype=None) -> int:
+    """Bytes gqa_prefix_attn needs for a decode step q, k_cache behind k_prefix [max_prefix, Hkv, d]."""
+    desc = make_desc(q, k_cache, causal=causal, out_dtype=out_dtype)
+    return _on_device(_check_devices(None, q=q, k_prefix=k_prefix, k_cache=k_cache), lambda: int(
+        lib().gqa_prefix_workspace_size(ctypes.byref(desc), int(k_prefix.shape[0]))))
+
+
+def gqa_prefix_attn(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens, out, lse=None, workspace=None, *,
+                    scale: float = 0.0, causal: bool = False, stream=None) -> None:
+    """Decode attention behind a shared prefix into ``out`` (and ``lse``); see
+    gqa_prefix_attn in ``include/gqa_shared_keys.h``."""
+    _inputs_ok(q, k_cache, v_cache, seqlens)
+    _inputs_ok(q, k_prefix, v_prefix, prefix_len)
+    if k_prefix.dim() != 3 or k_prefix.shape[1:] != k_cache.shape[2:]:
+        raise ValueError(f"prefix {tuple(k_prefix.shape)} and cache {tuple(k_cache.shape)} disagree")
+    _lengths_ok("seqlens", seqlens, q.shape[0])
+    _lengths_ok("prefix_len", prefix_len, 1)
+    _outputs_ok(q, out, lse, workspace)
+    device = _check_devices(stream, q=q, k_prefix=k_prefix, v_prefix=v_prefix, prefix_len=prefix_len,
+                            k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, out=out, lse=lse, workspace=workspace)
+    desc = make_desc(q, k_cache, scale=scale, causal=causal, out_dtype=out.dtype)
+    rc = _on_device(device, lambda: lib().gqa_prefix_attn(
+        ctypes.byref(desc), _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), int(k_prefix.shape[0]),
+        _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(out), _ptr(lse), _ptr(workspace), _bytes_of(workspace),
+        _stream(stream)))
+    _check(rc, "gqa_prefix_attn")
+
+
+def _allocate(q, out_dtype, workspace_bytes, stream):
+    """out, lse and a workspace of the call's own stream, so that the caching
+    allocator hands none of them on while that stream still uses it."""
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(q.device)
+    elif not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        ws = torch.empty(workspace_bytes, dtype=torch.uint8, device=q.device) if workspace_bytes else None
+    return out, lse, ws
+
+
+def cross_attention(q, k, v, kv_lens, *, scale: float = 0.0, out_dtype=None, stream=None):
+    """Allocates out / lse / workspace with torch and calls gqa_cross_attn."""
+    out, lse, ws = _allocate(q, out_dtype, gqa_cross_workspace_size(q, k, out_dtype=out_dtype), stream)
+    gqa_cross_attn(q, k, v, kv_lens, out, lse, ws, scale=scale, stream=stream)
+    return out, lse
+
+
+def prefix_decode(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens, *, scale: float = 0.0,
+                  causal: bool = False, out_dtype=None, stream=None):
+    """Allocates out / lse / workspace with torch and calls gqa_prefix_attn."""
+    ws_bytes = gqa_prefix_workspace_size(q, k_prefix, k_cache, causal=causal, out_dtype=out_dtype)
+    out, lse, ws = _allocate(q, out_dtype, ws_bytes, stream)
+    gqa_prefix_attn(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens, out, lse, ws, scale=scale,
+                    causal=causal, stream=stream)
+    return out, lse
+
+
+def gqa_shared_keys_plan(desc: gqa_desc_t, kv_lens_host, every_piece: bool = False, sm_count: int = 0):
+    """The tiled kernel's decomposition as (num_ctas, group_tokens, num_pieces, items int32 [n, 8])."""
+    import numpy as np
+
+    sl = np.ascontiguousarray(np.asarray(kv_lens_host, dtype=np.int32))
+    nc, gt, pieces, n = ctypes.c_int(), ctypes.c_int(), ctypes.c_int(), ctypes.c_int64()
+
+    def call(items, cap):
+        _check(lib().gqa_shared_keys_plan(ctypes.byref(desc), int(every_piece), sl.ctypes.data, int(sm_count),
+                                          ctypes.byref(nc), ctypes.byref(gt), ctypes.byref(pieces),
+                                          None if items is None else items.ctypes.data, cap, ctypes.byref(n)),
+               "gqa_shared_keys_plan")
+
+    call(None, 0)
+    items = np.zeros((n.value, 8), dtype=np.int32)
+    call(items, n.value)
+    return nc.value, gt.value, pieces.value, items

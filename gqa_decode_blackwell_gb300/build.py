@@ -1,7 +1,7 @@
 """Builds the sm_103a shared library in-tree with nvcc.
 
-The library is a plain C-ABI ``.so`` (see ``include/gqa_decode.h``); nothing
-here links against PyTorch.
+The library is a plain C-ABI ``.so`` (see ``include/gqa_decode.h`` and
+``include/gqa_shared_keys.h``); nothing here links against PyTorch.
 """
 from __future__ import annotations
 
@@ -13,6 +13,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 HEADER = os.path.join(ROOT, "include", "gqa_decode.h")
+SHARED_KEYS_HEADER = os.path.join(ROOT, "include", "gqa_shared_keys.h")
 LIB = os.path.join(PKG, "libgqa_decode_sm103.so")
 # The same library with device-side bounds checks (-DGQA_DEBUG): every
 # global write of the decode kernel is checked against its buffer and
@@ -34,7 +35,8 @@ def _nvcc() -> str:
 
 
 def sources():
-    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))] + [HEADER]
+    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))] + [
+        HEADER, SHARED_KEYS_HEADER]
 
 
 def up_to_date(out: str = LIB) -> bool:
@@ -44,14 +46,19 @@ def up_to_date(out: str = LIB) -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
-# Translation units: the host side (C ABI, planning, combine kernel) and one
-# unit per head_dim and merge mode holding that combination's decode kernels,
-# compiled in parallel and linked into one shared library.
+# Translation units: the host sides (C ABI, planning, merge kernels) of the two
+# headers, one unit per head_dim and merge mode holding that combination's
+# decode kernels and one per head_dim with its rows kernels, compiled in
+# parallel and linked into one shared library.
 INSTANCES = [(hd, cl) for hd in (64, 128, 256) for cl in (0, 1)]
 
 
 def _units(build_dir: str):
-    units = [(os.path.join(CSRC, "gqa_decode.cu"), [], os.path.join(build_dir, "gqa_decode.o"))]
+    units = [(os.path.join(CSRC, f"{name}.cu"), [], os.path.join(build_dir, f"{name}.o"))
+             for name in ("gqa_decode", "gqa_shared_keys")]
+    for hd in (64, 128, 256):
+        units.append((os.path.join(CSRC, "rows_instances.cu"), [f"-DGQA_INST_HD={hd}"],
+                      os.path.join(build_dir, f"rows_{hd}.o")))
     for hd, cl in INSTANCES:
         units.append((os.path.join(CSRC, "decode_instances.cu"), [f"-DGQA_INST_HD={hd}", f"-DGQA_INST_CLUSTER={cl}"],
                       os.path.join(build_dir, f"decode_{hd}_{cl}.o")))

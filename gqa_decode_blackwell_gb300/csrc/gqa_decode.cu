@@ -14,6 +14,7 @@
 #include "combine_kernel.cuh"
 #include "decode_kernel.cuh"
 #include "decode_launch.h"
+#include "host.h"
 #include "plan.cuh"
 
 namespace gqa {
@@ -24,21 +25,9 @@ namespace gqa {
 __device__ unsigned int g_gqa_error_bits = 0;
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-constexpr size_t kWsAlign = 256;
-
-struct DeviceState {
-  int sm_count = 0;
-  unsigned attr_done = 0;          // one bit per kernel instantiation
-  unsigned int* err_word = nullptr;  // device address of g_gqa_error_bits
-};
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -67,9 +56,6 @@ unsigned long long wait_timeout_ns() {
   }
   return 1000000000ull;  // one second: decode launches take microseconds
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 gqa_status_t current_device(int* dev, DeviceState** st) {
   if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return GQA_ERR_CUDA;
@@ -100,7 +86,7 @@ gqa_status_t error_word(DeviceState* st, unsigned int** out) {
 }
 
 #ifdef GQA_TRACE
-unsigned long long* g_trace_buf = nullptr;  // attached by gqa_trace_attach (trace builds)
+static unsigned long long* g_trace_buf = nullptr;  // attached by gqa_trace_attach (trace builds)
 #endif
 
 // Sets the dynamic shared memory limit of a kernel once per device.
@@ -113,7 +99,7 @@ gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int
   return GQA_OK;
 }
 
-gqa_status_t check_desc(const gqa_desc_t* d) {
+gqa_status_t check_desc_any_rows(const gqa_desc_t* d) {
   if (d == nullptr) return GQA_ERR_INVALID_ARG;
   if (d->batch < 0 || d->q_tokens < 1 || d->q_heads < 1 || d->kv_heads < 1 || d->max_seqlen < 1)
     return GQA_ERR_INVALID_ARG;
@@ -127,20 +113,18 @@ gqa_status_t check_desc(const gqa_desc_t* d) {
   if (d->reduction != GQA_REDUCE_AUTO && d->reduction != GQA_REDUCE_COMBINE && d->reduction != GQA_REDUCE_CLUSTER)
     return GQA_ERR_INVALID_ARG;
   if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return GQA_ERR_UNSUPPORTED;
-  const long long g = d->q_heads / d->kv_heads;
-  if (static_cast<long long>(d->q_tokens) * g > GQA_MAX_QROWS) return GQA_ERR_UNSUPPORTED;
   if (d->q_heads > 65535 || d->max_seqlen > (1 << 30)) return GQA_ERR_UNSUPPORTED;
   return GQA_OK;
 }
 
-struct HostPlan {
-  PlanParams pp;
-  int num_slots;      // partial slots per row (0: the decode writes final outputs only)
-  bool combine;       // a combine launch follows
-  bool use_n_pieces;  // combine reads per-pair piece counts (balanced plan)
-  int cluster_k;      // > 1: the k splits of a pair form a cluster and merge in it
-  gqa_status_t status;  // GQA_ERR_UNSUPPORTED: an in-cluster merge was asked for and cannot be done
-};
+gqa_status_t check_desc(const gqa_desc_t* d) {
+  const gqa_status_t rc = check_desc_any_rows(d);
+  if (rc != GQA_OK) return rc;
+  const long long g = d->q_heads / d->kv_heads;
+  return static_cast<long long>(d->q_tokens) * g > GQA_MAX_QROWS ? GQA_ERR_UNSUPPORTED : GQA_OK;
+}
+
+namespace {
 
 // Largest power of two <= x, for 1 <= x (capped at kMaxClusterK).
 int pow2_floor_k(long long x) {
@@ -216,6 +200,8 @@ int cluster_splits(const gqa_desc_t* d, int num_splits, int sm, bool force_parti
   if (forced) return (pow2 && num_splits <= kMaxClusterK) ? num_splits : -1;
   return (num_splits == 2 && pairs * 2 >= 128) ? 2 : 0;
 }
+
+}  // namespace
 
 HostPlan make_plan(const gqa_desc_t* d, int num_splits, int sm, bool force_partial) {
   HostPlan hp;
@@ -293,6 +279,8 @@ HostPlan make_plan(const gqa_desc_t* d, int num_splits, int sm, bool force_parti
   hp.use_n_pieces = false;
   return hp;
 }
+
+namespace {
 
 struct WsLayout {
   size_t o_off, lse_off, np_off, total;
@@ -401,6 +389,8 @@ gqa_status_t encode_maps_uncached(const gqa_desc_t* d, const void* q, const void
   return GQA_OK;
 }
 
+}  // namespace
+
 cudaLaunchAttribute pdl_attr(bool on) {
   cudaLaunchAttribute a;
   std::memset(&a, 0, sizeof a);
@@ -409,7 +399,7 @@ cudaLaunchAttribute pdl_attr(bool on) {
   return a;
 }
 
-KernelRef decode_kernel_ref(int head_dim, int np, bool f16, bool cluster) {
+static KernelRef decode_kernel_ref(int head_dim, int np, bool f16, bool cluster) {
   if (head_dim == 64) return cluster ? decode_kernel_ref_64_1(np, f16) : decode_kernel_ref_64_0(np, f16);
   if (head_dim == 256) return cluster ? decode_kernel_ref_256_1(np, f16) : decode_kernel_ref_256_0(np, f16);
   return cluster ? decode_kernel_ref_128_1(np, f16) : decode_kernel_ref_128_0(np, f16);
@@ -451,7 +441,7 @@ gqa_status_t launch_decode(DeviceState* st, DecodeParams& p, bool in_f16, cudaSt
   return GQA_OK;
 }
 
-gqa_status_t launch_combine(const CombineParams& c, int head_dim, cudaStream_t s) {
+static gqa_status_t launch_combine(const CombineParams& c, int head_dim, cudaStream_t s) {
   if (c.rows == 0) return GQA_OK;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
@@ -478,9 +468,9 @@ gqa_status_t check_inputs(const void* q, const void* k, const void* v, const int
 
 // Common front half of gqa_decode_attn / gqa_decode_splitkv.
 gqa_status_t prepare_decode(const gqa_desc_t* d, const void* q, const void* k, const void* v,
-                            const int32_t* seqlens, const HostPlan& hp, DecodeParams* p) {
+                            const int32_t* seqlens, const HostPlan& hp, DecodeParams* p, bool keep_maps) {
   std::memset(p, 0, sizeof *p);
-  gqa_status_t rc = encode_maps(d, q, k, v, p);
+  gqa_status_t rc = keep_maps ? encode_maps(d, q, k, v, p) : encode_maps_uncached(d, q, k, v, p);
   if (rc != GQA_OK) return rc;
   p->seqlens = seqlens;
   p->plan = hp.pp;
@@ -497,6 +487,8 @@ gqa_status_t prepare_decode(const gqa_desc_t* d, const void* q, const void* k, c
   p->timeout_ns = wait_timeout_ns();
   return GQA_OK;
 }
+
+namespace {
 
 __global__ void selftest_wait_kernel(unsigned long long timeout_ns) {
   __shared__ uint64_t bar;

@@ -1,0 +1,62 @@
+// What the host side of gqa_decode.cu shares with that of gqa_shared_keys.cu:
+// device state, argument checks, tensor-map encoding, split plans and the
+// decode kernel's launch.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/gqa_decode.h"
+#include "decode_kernel.cuh"
+#include "plan.cuh"
+
+namespace gqa {
+
+constexpr int kMaxDevices = 64;
+constexpr size_t kWsAlign = 256;
+
+struct DeviceState {
+  int sm_count = 0;
+  unsigned attr_done = 0;            // one bit per kernel instantiation (decode: 0..23, rows: 24..29)
+  unsigned int* err_word = nullptr;  // device address of the library's error word
+};
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct HostPlan {
+  PlanParams pp;
+  int num_slots;      // partial slots per row (0: the decode writes final outputs only)
+  bool combine;       // a combine launch follows
+  bool use_n_pieces;  // combine reads per-pair piece counts (balanced plan)
+  int cluster_k;      // > 1: the k splits of a pair form a cluster and merge in it
+  gqa_status_t status;  // GQA_ERR_UNSUPPORTED: an in-cluster merge was asked for and cannot be done
+};
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+EncodeTiledFn encode_fn();
+bool env_flag(const char* name);
+unsigned long long wait_timeout_ns();
+gqa_status_t current_device(int* dev, DeviceState** st);
+gqa_status_t error_word(DeviceState* st, unsigned int** out);
+gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int bytes);
+cudaLaunchAttribute pdl_attr(bool on);
+
+// A description for any number of query rows, and one the decode kernel can
+// serve (at most GQA_MAX_QROWS per KV head).
+gqa_status_t check_desc_any_rows(const gqa_desc_t* d);
+gqa_status_t check_desc(const gqa_desc_t* d);
+gqa_status_t check_inputs(const void* q, const void* k, const void* v, const int32_t* seqlens);
+HostPlan make_plan(const gqa_desc_t* d, int num_splits, int sm, bool force_partial);
+// Everything of a decode launch but its outputs.  keep_maps: the tensor maps
+// are kept for a later call on the same buffers.
+gqa_status_t prepare_decode(const gqa_desc_t* d, const void* q, const void* k, const void* v,
+                            const int32_t* seqlens, const HostPlan& hp, DecodeParams* p, bool keep_maps = true);
+gqa_status_t launch_decode(DeviceState* st, DecodeParams& p, bool in_f16, cudaStream_t s);
+
+}  // namespace gqa

@@ -1,0 +1,628 @@
+// Attention of many query rows over one range of keys, for sm_103a (TMA +
+// tcgen05 + TMEM).
+//
+// The decode kernel (decode_kernel.cuh) serves at most 32 query rows per KV
+// head and puts key positions along the MMA's M dimension.  Here the rows are
+// many -- a prompt's tokens against an encoder's states, or every sequence of
+// a batch against a prefix they share -- and fill M themselves.  Per tile of
+// 128 rows and block of 128 keys of one (batch, KV head) pair:
+//
+//     S[128 x 128] = Q_tile[128 x d] K_blk[128 x d]^T       (TMEM, fp32)
+//     P            = exp2(S * scale*log2e - m)              (online softmax)
+//     O[128 x d]  += P[128 x 128] V_blk[128 x d]            (TMEM, fp32)
+//
+// A tile's rows are the G query heads of T = 128 / G consecutive query tokens
+// (row t*G + g), so one TMA box brings them and the heads of a KV head share
+// its keys.  Rows past T*G, and tokens past the last one, hold zeros and are
+// never written out.
+//
+// Warps: 4 softmax warps per tile, then one TMA producer and one MMA issuer.
+// A row of S is one TMEM lane, so one softmax thread holds a whole row: its
+// max and sum need no exchange, P goes back into the TMEM columns of its S
+// (16-bit, the value MMA's A operand) and never passes through shared memory.
+//   head_dim 64, 128: two tiles (256 rows) share each K/V block; one tile's
+//     softmax runs under the other's MMAs (QK of its next block, PV of this).
+//   head_dim 256: O takes half of TMEM, so there is one tile, with two S
+//     slots: the next block's QK runs under this block's softmax.  K and V
+//     blocks are two ring tiles each, their 128-element d-halves.
+//
+// The running max is only replaced when it grows by more than 8 (log2 units),
+// as in the decode kernel; a warp whose rows need it rescales its own lanes
+// of O, after the value MMA of the block before has landed.
+//
+// Work: the (batch, KV head, tile) triples are cut by plan.cuh's balanced
+// partition, triples in the place of (batch, KV head) pairs.  A triple that
+// is cut leaves fp32 partials (normalised O_s, lse_s) for rows_merge.cuh.
+//
+// Every wait is bounded, as in the decode kernel.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "decode_kernel.cuh"
+#include "plan.cuh"
+#include "rows_ptx.cuh"
+
+namespace gqa {
+
+constexpr int kTileRows = 128;  // query rows of a tile (the MMA M dimension)
+
+struct RowsParams {
+  CUtensorMap tm_q;     // q [B, nq, Hq, d], box {64, G, T, 1}
+  CUtensorMap tm_k;     // k [B, S_max, Hkv, d], box {64, 1, 128, 1}
+  CUtensorMap tm_v;     // v, same
+  const int32_t* lens;  // [B] keys of each batch entry
+  void* out;            // [B, nq, Hq, d] bf16, fp16 or fp32: the rows of uncut triples
+  float* lse;           // [B, nq, Hq] or null
+  float* o_part;        // [pieces][tiles per triple][128][d]
+  float* lse_part;      // [pieces][tiles per triple][128]
+  int2* rec;            // what was cut, for the merge (see below)
+  PlanParams plan;      // kv_heads: Hkv * groups, h' = h * groups + (tile group)
+  int nq, Hq, G, groups;
+  int tokens;           // T: query tokens of a tile
+  int out_dtype;
+  int out_v32;          // out is 32-byte aligned
+  // 0: an uncut triple's rows go to out / lse; piece indexes are 2 * CTA,
+  //    + 1 for the triple's first piece; rec[CTA] = {triple, pieces} of the
+  //    cut triple that begins in this CTA (at most one), or {-1, 0}.
+  // 1: every triple leaves partials; piece index triple + CTA, which no two
+  //    pieces share as both grow along the plan; rec[triple] = {first piece
+  //    index, pieces}, 0 pieces when it has no keys.
+  int all_partial;
+  float scale_log2;
+  unsigned long long timeout_ns;
+  unsigned int* err_word;
+  // byte extents of the buffers the kernel writes, checked by -DGQA_DEBUG builds
+  unsigned long long out_bytes, lse_bytes, o_part_bytes, lse_part_bytes, rec_bytes;
+};
+
+template <int HEAD_DIM>
+struct RowsCfg {
+  static constexpr int kTiles = HEAD_DIM == 256 ? 1 : 2;  // row tiles of a CTA
+  static constexpr int kChunks = HEAD_DIM / 64;           // 128-byte swizzle atoms along d
+  static constexpr int kTileDim = HEAD_DIM < 128 ? HEAD_DIM : 128;
+  static constexpr int kTileChunks = kTileDim / 64;
+  static constexpr int kTilesPerBlock = HEAD_DIM / kTileDim;  // ring tiles of a K or V block
+  static constexpr int kStageBytes = kBlockN * kTileDim * 2;
+  static constexpr int kQTileBytes = kTileRows * HEAD_DIM * 2;
+  static constexpr int kQBytes = kTiles * kQTileBytes;
+  static constexpr int kStagesK = HEAD_DIM == 64 ? 4 : 2;
+  static constexpr int kStagesV = kStagesK;
+  static constexpr int kSoftmaxWarps = 4 * kTiles;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+  static constexpr int kRingBytes = (kStagesK + kStagesV) * kStageBytes;
+  static constexpr int kMiscBytes = 512 + 4 * kMaxSmemB + 4 * (kMaxSmemB + 1) + 60;
+  static constexpr int kSmemBytes = 1024 + kQBytes + kRingBytes + kMiscBytes;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kOCol = 256;  // after the two S slots of 128 columns
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory over budget");
+  static_assert(kOCol + kTiles * HEAD_DIM <= kTmemCols, "TMEM column plan");
+  static_assert(kStagesK % kTilesPerBlock == 0, "rings of whole blocks");
+};
+
+// IN_F16: q, k, v (and P) are fp16; otherwise bf16.
+template <int HEAD_DIM, bool IN_F16>
+__global__ void __launch_bounds__(RowsCfg<HEAD_DIM>::kThreads, 1)
+gqa_rows_kernel(const __grid_constant__ RowsParams p) {
+  using Cfg = RowsCfg<HEAD_DIM>;
+  constexpr int NT = Cfg::kTiles, KCH = Cfg::kChunks, TCH = Cfg::kTileChunks, TPB = Cfg::kTilesPerBlock;
+  constexpr uint32_t NSK = Cfg::kStagesK, NSV = Cfg::kStagesV;
+  constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;
+  uint8_t* kring = qbuf + Cfg::kQBytes;
+  uint8_t* vring = kring + NSK * Cfg::kStageBytes;
+  uint8_t* misc = vring + NSV * Cfg::kStageBytes;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(misc);
+  int32_t* s_len = reinterpret_cast<int32_t*>(misc + 512);
+  int32_t* s_pre = s_len + kMaxSmemB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pre + kMaxSmemB + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const uint32_t bar_base = ptx::smem_u32(bar);
+  auto BAR = [&](int i) -> uint32_t { return bar_base + 8u * static_cast<uint32_t>(i); };
+  // The S, P and O barriers are indexed by S slot: the tile, or (one tile) the
+  // block's parity.  A parity wait is sound only while the phase before the
+  // awaited one is known to be complete; with one tile, QK(g) is issued ahead
+  // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
+  constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
+                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + 1, S_FULL = Q_EMPTY + 1, P_FULL = S_FULL + 2,
+                O_FULL = P_FULL + 2, DRAIN = O_FULL + 2;
+  static_assert(DRAIN < 64, "barrier words");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PlanParams plan = p.plan;
+  const int B = plan.batch;
+
+  // ---------------------------------------------------------------- set-up
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < NSK; ++i) {
+      ptx::mbar_init(BAR(K_FULL + i), 1);
+      ptx::mbar_init(BAR(K_EMPTY + i), 1);
+    }
+    for (uint32_t i = 0; i < NSV; ++i) {
+      ptx::mbar_init(BAR(V_FULL + i), 1);
+      ptx::mbar_init(BAR(V_EMPTY + i), 1);
+    }
+    ptx::mbar_init(BAR(Q_FULL), 1);
+    ptx::mbar_init(BAR(Q_EMPTY), 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(BAR(S_FULL + i), 1);
+      ptx::mbar_init(BAR(P_FULL + i), 4);  // one arrival per softmax warp of the tile
+      ptx::mbar_init(BAR(O_FULL + i), 1);
+    }
+    ptx::mbar_init(BAR(DRAIN), 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tensormap(&p.tm_q);
+    ptx::prefetch_tensormap(&p.tm_k);
+    ptx::prefetch_tensormap(&p.tm_v);
+  }
+  __syncwarp();
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), Cfg::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  // Rows past T*G of each 64-element chunk of Q: TMA never writes them.
+  {
+    const int used = p.tokens * p.G;
+    for (int i = threadIdx.x; i < NT * KCH * kTileRows; i += Cfg::kThreads) {
+      if (i % kTileRows < used) continue;
+      uint4* row = reinterpret_cast<uint4*>(qbuf + i * 128);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+    }
+    ptx::fence_proxy_async_smem();
+  }
+  // Lengths may be produced, and outputs still read, by the previous kernel.
+  ptx::griddep_wait();
+  // The next launch may set itself up; it waits for this grid before it
+  // reads or writes anything this grid touches.
+  ptx::griddep_launch_dependents();
+  if (plan.mode == PLAN_BALANCED && warp == 0) {
+    int run = 0;
+    for (int base = 0; base < B; base += 32) {
+      const int i = base + lane;
+      int nb = 0;
+      if (i < B) {
+        const int raw = p.lens[i], L = clamp_len(raw, plan.max_seqlen);
+        if (raw != L) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
+        s_len[i] = L;
+        nb = pair_units(num_blocks(L), plan.item_units);
+      }
+      int incl = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (i < B) s_pre[i] = run + incl - nb;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s_pre[B] = run;
+  } else if (plan.mode != PLAN_BALANCED && blockIdx.x == 0) {
+    // lengths too many to stage: each item reads its own; one CTA flags the bad ones
+    for (int i = threadIdx.x; i < B; i += Cfg::kThreads)
+      if (p.lens[i] != clamp_len(p.lens[i], plan.max_seqlen)) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  WorkIter iter;
+  iter.init_warp(plan, p.lens, s_len, s_pre, blockIdx.x, lane);
+  WorkItem it;
+  auto head_of = [&](const WorkItem& w) { return w.h / p.groups; };
+  auto token_of = [&](const WorkItem& w) { return (w.h % p.groups) * (NT * p.tokens); };  // its first query token
+  // row tiles of an item that hold any token (at least one)
+  auto tiles_of = [&](const WorkItem& w) { return NT == 2 && token_of(w) + p.tokens < p.nq ? 2 : 1; };
+
+  if (warp == kProducerWarp) {
+    // ============================================================= producer
+    if (lane == 0) {
+      uint32_t tk = 0, tv = 0, items = 0;  // ring tiles and items loaded
+      bool ok = true;
+      auto load_block = [&](bool is_v, const WorkItem& w, int blk) -> bool {
+        const int h = head_of(w);
+#pragma unroll
+        for (int hf = 0; hf < TPB; ++hf) {
+          const uint32_t n = is_v ? tv : tk, ns = is_v ? NSV : NSK, stage = n % ns;
+          const uint32_t full = BAR((is_v ? V_FULL : K_FULL) + static_cast<int>(stage));
+          const uint32_t empty = BAR((is_v ? V_EMPTY : K_EMPTY) + static_cast<int>(stage));
+          // the first pass over a ring needs no wait
+          if (n >= ns && !ptx::mbar_wait_bounded(empty, ((n / ns) & 1u) ^ 1u, abort_flag, p.timeout_ns)) return false;
+          ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
+          detail::check_coord(p.err_word, w.b >= 0 && w.b < B && h >= 0 && h * p.groups < plan.kv_heads && blk >= 0 &&
+                                              blk * kBlockN < plan.max_seqlen);
+          uint8_t* dst = (is_v ? vring : kring) + stage * Cfg::kStageBytes;
+#pragma unroll
+          for (int kc = 0; kc < TCH; ++kc)
+            ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &p.tm_v : &p.tm_k, full, (hf * TCH + kc) * 64, h,
+                             blk * kBlockN, w.b);
+          if (is_v) ++tv; else ++tk;
+        }
+        return true;
+      };
+      while (ok && iter.next(it)) {
+        if (it.blk_begin >= it.blk_end) continue;
+        if (items >= 1 && !ptx::mbar_wait_bounded(BAR(Q_EMPTY), (items & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const int nt = tiles_of(it), tok0 = token_of(it), h = head_of(it);
+        ptx::mbar_arrive_expect_tx(BAR(Q_FULL), static_cast<uint32_t>(nt * KCH * p.tokens * p.G * 128));
+        for (int t = 0; t < nt; ++t)
+#pragma unroll
+          for (int kc = 0; kc < KCH; ++kc)
+            ptx::tma_load_4d(ptx::smem_u32(qbuf + t * Cfg::kQTileBytes + kc * 16384), &p.tm_q, BAR(Q_FULL), kc * 64,
+                             h * p.G, tok0 + t * p.tokens, it.b);
+        ++items;
+        // K0, then V(i), K(i+1) in the order the MMAs take them
+        ok = load_block(false, it, it.blk_begin);
+        for (int blk = it.blk_begin; blk < it.blk_end && ok; ++blk) {
+          if (blk + 1 < it.blk_end) ok = load_block(false, it, blk + 1);
+          if (ok) ok = load_block(true, it, blk);
+        }
+      }
+      if (!ok) {
+        detail::set_error(p.err_word, kErrTimeout, abort_flag);
+        // let the copies already issued land before the CTA exits
+        for (uint32_t u = tk > NSK ? tk - NSK : 0u; u < tk; ++u)
+          ptx::mbar_wait_bounded(BAR(K_FULL + static_cast<int>(u % NSK)), (u / NSK) & 1u, nullptr, p.timeout_ns);
+        for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
+          ptx::mbar_wait_bounded(BAR(V_FULL + static_cast<int>(u % NSV)), (u / NSV) & 1u, nullptr, p.timeout_ns);
+        if (items > 0) ptx::mbar_wait_bounded(BAR(Q_FULL), (items - 1) & 1u, nullptr, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // =========================================================== MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = ptx::idesc_f16_f32(128, kBlockN, 0, 0, !IN_F16);
+      constexpr uint32_t idesc_pv = ptx::idesc_f16_f32(128, Cfg::kTileDim, 0, 1, !IN_F16);
+      const uint64_t q_desc = ptx::smem_desc_sw128(ptx::smem_u32(qbuf), 16, 1024);
+      const uint64_t k_desc = ptx::smem_desc_sw128(ptx::smem_u32(kring), 16, 1024);
+      // V as the MN-major B operand: 64-element chunks of d 16 KB apart, 8 keys 1 KB
+      const uint64_t v_desc = ptx::smem_desc_sw128(ptx::smem_u32(vring), 16384, 1024);
+      bool ok = true;
+      uint32_t u = 0;            // K/V blocks
+      uint32_t items = 0;
+      uint32_t g[2] = {0u, 0u};  // blocks of each tile
+      auto wait = [&](int i, uint32_t parity) {
+        if (ok) ok = ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns);
+        return ok;
+      };
+      // The tiles of K block u2, each waited for; S slot `slot` of tile t
+      auto qk = [&](int t, uint32_t u2, uint32_t slot, bool wait_k) {
+#pragma unroll
+        for (int hf = 0; hf < TPB; ++hf) {
+          const uint32_t n = u2 * TPB + hf, stage = n % NSK;
+          if (wait_k && !wait(K_FULL + static_cast<int>(stage), n / NSK)) return;
+          ptx::tc_fence_after();
+          const uint64_t qd = q_desc + static_cast<uint64_t>((t * Cfg::kQTileBytes) >> 4);
+          const uint64_t kd = k_desc + static_cast<uint64_t>((stage * Cfg::kStageBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < Cfg::kTileDim / 16; ++kk) {
+            const int k = hf * (Cfg::kTileDim / 16) + kk;
+            ptx::mma_f16_ss(tmem_base + slot * kBlockN, qd + static_cast<uint32_t>((k >> 2) * 1024 + (k & 3) * 2),
+                            kd + static_cast<uint32_t>((kk >> 2) * 1024 + (kk & 3) * 2), idesc_qk, k > 0 ? 1u : 0u);
+          }
+        }
+        ptx::mma_commit(BAR(S_FULL + static_cast<int>(slot)));
+      };
+      auto pv = [&](int t, uint32_t u2, uint32_t slot, bool first, bool wait_v) {
+#pragma unroll
+        for (int hf = 0; hf < TPB; ++hf) {
+          const uint32_t n = u2 * TPB + hf, stage = n % NSV;
+          if (wait_v && !wait(V_FULL + static_cast<int>(stage), n / NSV)) return;
+          ptx::tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint64_t>((stage * Cfg::kStageBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kBlockN / 16; ++kk)
+            ptx::mma_f16_ts(tmem_base + Cfg::kOCol + t * HEAD_DIM + hf * Cfg::kTileDim,
+                            tmem_base + slot * kBlockN + kk * 8, vd + static_cast<uint32_t>(kk * (2048 >> 4)),
+                            idesc_pv, (kk > 0 || !first) ? 1u : 0u);
+        }
+        ptx::mma_commit(BAR(O_FULL + static_cast<int>(slot)));
+      };
+      auto release = [&](int ring_empty, uint32_t u2, uint32_t ns) {  // the ring tiles of block u2
+#pragma unroll
+        for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit(BAR(ring_empty + static_cast<int>((u2 * TPB + hf) % ns)));
+      };
+      while (ok && iter.next(it)) {
+        const int n = it.blk_end - it.blk_begin;
+        if (n <= 0) continue;
+        const int nt = tiles_of(it);
+        if (!wait(Q_FULL, items)) break;
+        if constexpr (NT == 2) {
+          // S slot t holds S and P of tile t.  The MMAs run in issue order, so
+          // QK(t, i+1) may overwrite P(t, i) once PV(t, i) is issued.
+          for (int t = 0; t < nt && ok; ++t) qk(t, u, static_cast<uint32_t>(t), t == 0);
+          if (!ok) break;
+          release(K_EMPTY, u, NSK);
+          if (n == 1) ptx::mma_commit(BAR(Q_EMPTY));
+          for (int i = 0; i < n && ok; ++i, ++u) {
+            const bool more = i + 1 < n;
+            for (int t = 0; t < nt; ++t) {
+              if (!wait(P_FULL + t, g[t])) break;
+              ++g[t];
+              pv(t, u, static_cast<uint32_t>(t), i == 0, t == 0);
+              if (more && ok) qk(t, u + 1, static_cast<uint32_t>(t), t == 0);
+              if (!ok) break;
+            }
+            if (!ok) break;
+            release(V_EMPTY, u, NSV);
+            if (more) release(K_EMPTY, u + 1, NSK);
+            if (i + 2 == n) ptx::mma_commit(BAR(Q_EMPTY));
+          }
+        } else {
+          // S slot g % 2 holds S and P of block g; QK(i+1) is issued before
+          // PV(i), over P(i-1), whose PV is issued already.
+          qk(0, u, u & 1u, true);
+          if (!ok) break;
+          release(K_EMPTY, u, NSK);
+          if (n == 1) ptx::mma_commit(BAR(Q_EMPTY));
+          for (int i = 0; i < n && ok; ++i, ++u) {
+            if (i + 1 < n) {
+              qk(0, u + 1, (u + 1) & 1u, true);
+              if (!ok) break;
+              release(K_EMPTY, u + 1, NSK);
+              if (i + 2 == n) ptx::mma_commit(BAR(Q_EMPTY));
+            }
+            if (!wait(P_FULL + static_cast<int>(u & 1u), u >> 1)) break;
+            pv(0, u, u & 1u, i == 0, true);
+            if (!ok) break;
+            release(V_EMPTY, u, NSV);
+          }
+        }
+        ++items;
+      }
+      if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
+      // every MMA has completed before TMEM is released
+      ptx::mma_commit(BAR(DRAIN));
+      ptx::mbar_wait_bounded(BAR(DRAIN), 0, nullptr, p.timeout_ns);
+    }
+    __syncwarp();
+  } else {
+    // ======================================================== softmax warps
+    const int t = warp >> 2;                        // this warp's row tile
+    const int r = (warp & 3) * 32 + lane;           // its TMEM lane: a row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t o_addr = tmem_base + lanes + Cfg::kOCol + static_cast<uint32_t>(t * HEAD_DIM);
+    const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+    const uint64_t scale2 = ptx::pack_f32x2(p.scale_log2, p.scale_log2);
+    uint32_t g = 0;  // blocks of this tile
+    bool ok = true;
+    int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
+    auto pack16 = [](float lo, float hi) -> uint32_t {
+      if constexpr (IN_F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+      }
+    };
+    auto wait = [&](int i, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns));
+      return ok;
+    };
+
+    auto wait_pv = [&](uint32_t blk_g) {  // the value MMA of this tile's block blk_g has landed
+      return NT == 2 ? wait(O_FULL + t, blk_g) : wait(O_FULL + static_cast<int>(blk_g & 1u), blk_g >> 1);
+    };
+
+    while (ok && iter.next(it)) {
+      const int tok = token_of(it) + t * p.tokens + r_tok, h = head_of(it);
+      const long long triple = static_cast<long long>(it.b) * plan.kv_heads + it.h;
+      const bool partial = p.all_partial != 0 || it.slot >= 0;
+      const int n_pieces = it.blk_begin < it.blk_end ? it.n_pieces : 0;
+      if (it.first_piece && partial) {
+        if (p.all_partial != 0) {
+          if (threadIdx.x == 0 && detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + triple, sizeof(int2)))
+            p.rec[triple] = make_int2(static_cast<int>(triple) + static_cast<int>(blockIdx.x), n_pieces);
+        } else {
+          cut = make_int2(static_cast<int>(triple), n_pieces);
+        }
+      }
+      if (t >= tiles_of(it)) continue;
+      const bool row_valid = r_tok < p.tokens && tok < p.nq;
+      const long long row = (static_cast<long long>(it.b) * p.nq + tok) * p.Hq + h * p.G + r_head;
+
+      float nm = kNoMax, l = 0.f;  // -max (log2 units; kNoMax while it is -inf) and the sum of this row
+      for (int blk = it.blk_begin; blk < it.blk_end; ++blk, ++g) {
+        const uint32_t slot = NT == 2 ? static_cast<uint32_t>(t) : (g & 1u);
+        const uint32_t s_addr = tmem_base + lanes + slot * kBlockN;
+        const bool first = blk == it.blk_begin;
+        if (!wait(S_FULL + static_cast<int>(slot), NT == 2 ? g : g >> 1)) break;
+        ptx::tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, x + 32 * c);
+        ptx::tmem_wait_ld();
+
+        const int tail = it.L - blk * kBlockN;  // keys of this block
+        if (tail < kBlockN) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) x[j] = j < tail ? x[j] : 0xff800000u;  // -inf
+          // V rows past the end hold whatever the buffer holds there; zero
+          // them (up to the capacity, past which TMA wrote zeros) so that
+          // 0 * garbage cannot reach O.  The first tile's warps do it, before
+          // their P lets the issuer start on this V.  The parity wait is
+          // sound: S(g) complete means that PV(g-1) is issued and V(g-1) has
+          // landed (one tile: PV(g-1) is waited for).
+          const int cap = plan.max_seqlen - blk * kBlockN;
+          if (t == 0 && cap > tail) {
+            if constexpr (NT == 1) {
+              if (g >= 1 && !wait_pv(g - 1)) break;
+            }
+#pragma unroll
+            for (int hf = 0; hf < TPB; ++hf) {
+              const uint32_t n = g * TPB + hf, stage = n % NSV;
+              if (!wait(V_FULL + static_cast<int>(stage), n / NSV)) break;
+              if (r >= tail && r < cap) {
+#pragma unroll
+                for (int kc = 0; kc < TCH; ++kc) {
+                  uint4* z = reinterpret_cast<uint4*>(vring + stage * Cfg::kStageBytes + kc * 16384 + r * 128);
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) z[c] = make_uint4(0, 0, 0, 0);
+                }
+              }
+            }
+            if (!ok) break;
+            ptx::fence_proxy_async_smem();
+          }
+        }
+
+        float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3])};
+#pragma unroll
+        for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+        const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;  // the scale is positive
+        if (first) {
+          nm = m_blk == -INFINITY ? kNoMax : -m_blk;
+        } else if (__any_sync(0xffffffffu, m_blk + nm > kRescaleThreshold)) {
+          // O may be rescaled once the value MMA of the block before has landed
+          if (!wait_pv(g - 1)) break;
+          ptx::tc_fence_after();
+          const float m_old = nm == kNoMax ? -INFINITY : -nm;
+          const float m_new = fmaxf(m_old, m_blk);
+          const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2_approx(m_old - m_new);
+          nm = m_new == -INFINITY ? kNoMax : -m_new;
+          l *= alpha;
+#pragma unroll
+          for (int c = 0; c < HEAD_DIM / 16; ++c) {
+            float o[16];
+            ptx::tmem_ld_32x32b_x16(o_addr + 16 * c, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] *= alpha;
+            ptx::tmem_st_32x32b_x16(o_addr + 16 * c, o);
+          }
+          ptx::tmem_wait_st();
+        }
+
+        // P, in place of the scores: 16-bit, two to a column
+        const uint64_t nm2 = ptx::pack_f32x2(nm, nm);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int k = 64 * c + 2 * j;
+            float a, b;
+            ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale2,
+                                             nm2), a, b);
+            a = ptx::ex2_approx(a);
+            b = ptx::ex2_approx(b);
+            x[k] = __float_as_uint(a);
+            x[k + 1] = __float_as_uint(b);
+            w[j] = pack16(a, b);
+          }
+          ptx::tmem_st_32x32b_x32(s_addr + 32 * c, w);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + static_cast<int>(slot)));
+
+        // the sum, from the unrounded p, under the value MMA
+        uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          s2[j & 3] = ptx::add_f32x2(s2[j & 3], ptx::pack_f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])));
+        float a, b;
+        ptx::unpack_f32x2(ptx::add_f32x2(ptx::add_f32x2(s2[0], s2[1]), ptx::add_f32x2(s2[2], s2[3])), a, b);
+        l += a + b;
+      }
+      if (!ok) break;
+
+      // ------------------------------------------------------------ epilogue
+      const bool empty = it.blk_begin >= it.blk_end;
+      if (empty && partial) continue;  // 0 pieces: the merge reads nothing of this triple
+      if (!empty) {
+        if (!wait_pv(g - 1)) break;
+        ptx::tc_fence_after();
+      }
+      const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // a row that saw only -inf scores: 0; NaN stays NaN
+      const float lse = l > 0.f || l != l ? 0.69314718055994531f * (__log2f(l) - nm) : -INFINITY;
+      const long long piece = p.all_partial != 0 ? triple + blockIdx.x
+                                                 : 2ll * blockIdx.x + (it.first_piece ? 1 : 0);
+      const long long prow = (piece * NT + t) * kTileRows + r;
+      const bool out16 = !partial && p.out_dtype != kOutF32;
+      uint8_t* dst;
+      bool store;
+      if (partial) {
+        dst = reinterpret_cast<uint8_t*>(p.o_part + prow * HEAD_DIM);
+        store = row_valid && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
+        if (row_valid && detail::write_ok(p.err_word, p.lse_part, p.lse_part_bytes, p.lse_part + prow, 4ull))
+          p.lse_part[prow] = lse;
+      } else {
+        dst = static_cast<uint8_t*>(p.out) + row * (HEAD_DIM * (out16 ? 2 : 4));
+        store = row_valid &&
+                detail::write_ok(p.err_word, p.out, p.out_bytes, dst, HEAD_DIM * (out16 ? 2ull : 4ull));
+        if (row_valid && p.lse != nullptr && detail::write_ok(p.err_word, p.lse, p.lse_bytes, p.lse + row, 4ull))
+          p.lse[row] = lse;
+      }
+      const bool v32 = partial || p.out_v32 != 0;
+      auto put = [&](uint8_t* to, const uint32_t (&v)[8]) {
+        if (v32) {
+          ptx::st_global_v8(to, v);
+        } else {
+          reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+      };
+#pragma unroll
+      for (int c = 0; c < HEAD_DIM / 32; ++c) {
+        uint32_t o[32];
+        if (!empty) {
+          ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+          ptx::tmem_wait_ld();
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = empty ? 0u : __float_as_uint(inv == 0.f ? 0.f : __uint_as_float(o[j]) * inv);
+        if (store) {
+          if (out16) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = pack16(__uint_as_float(o[16 * q + 2 * j]), __uint_as_float(o[16 * q + 2 * j + 1]));
+              put(dst + 64 * c + 32 * q, v);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = o[8 * q + j];
+              put(dst + 128 * c + 32 * q, v);
+            }
+          }
+        }
+        __syncwarp();  // the next TMEM load is the whole warp's
+      }
+    }
+    if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
+    // after a timeout too, so that the merge never reads what an earlier call left
+    if (threadIdx.x == 0 && p.all_partial == 0 && p.rec != nullptr &&
+        detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + blockIdx.x, sizeof(int2)))
+      p.rec[blockIdx.x] = cut;
+  }
+
+  // ---------------------------------------------------------------- teardown
+  ptx::tc_fence_before();
+  __syncwarp();
+  __syncthreads();  // every role is done with TMEM and shared memory
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace gqa
