@@ -9,6 +9,7 @@ struct KernelRef {
   const void* fn;  // the __global__ function, for cudaLaunchKernelExC / cudaFuncSetAttribute
   int smem_bytes;  // dynamic shared memory it is launched with
   int threads;     // CTA size
+  int regs = 0;    // registers per thread it must be launched with (0: any)
 };
 
 // np: padded head columns (16 or 32); f16: fp16 inputs (else bf16).

@@ -89,10 +89,15 @@ gqa_status_t error_word(DeviceState* st, unsigned int** out) {
 static unsigned long long* g_trace_buf = nullptr;  // attached by gqa_trace_attach (trace builds)
 #endif
 
-// Sets the dynamic shared memory limit of a kernel once per device.
-gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int bytes) {
+// Sets the dynamic shared memory limit of a kernel once per device, and checks
+// that it was compiled to the register count (0: any) its warps share out.
+gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int bytes, int regs) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (st->attr_done & (1u << bit)) return GQA_OK;
+  if (regs != 0) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs != regs) return GQA_ERR_CUDA;
+  }
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GQA_ERR_CUDA;
   st->attr_done |= 1u << bit;

@@ -162,7 +162,7 @@ gqa_status_t launch_rows(DeviceState* st, const gqa_desc_t* d, const RowsPlan& r
                           : d->head_dim == 256 ? rows_kernel_ref_256(f16)
                                                : rows_kernel_ref_128(f16);
   const unsigned bit = 24u + (d->head_dim == 64 ? 0u : d->head_dim == 128 ? 2u : 4u) + (f16 ? 1u : 0u);
-  if ((rc = ensure_smem_attr(st, bit, k_ref.fn, k_ref.smem_bytes)) != GQA_OK) return rc;
+  if ((rc = ensure_smem_attr(st, bit, k_ref.fn, k_ref.smem_bytes, k_ref.regs)) != GQA_OK) return rc;
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);

@@ -44,7 +44,7 @@ bool env_flag(const char* name);
 unsigned long long wait_timeout_ns();
 gqa_status_t current_device(int* dev, DeviceState** st);
 gqa_status_t error_word(DeviceState* st, unsigned int** out);
-gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int bytes);
+gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int bytes, int regs = 0);
 cudaLaunchAttribute pdl_attr(bool on);
 
 // A description for any number of query rows, and one the decode kernel can

@@ -16,7 +16,7 @@ KernelRef GQA_ROWS_REF_NAME(GQA_INST_HD)(bool f16) {
   using Cfg = RowsCfg<GQA_INST_HD>;
   const void* fn = f16 ? reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, true>)
                        : reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, false>);
-  return KernelRef{fn, Cfg::kSmemBytes, Cfg::kThreads};
+  return KernelRef{fn, Cfg::kSmemBytes, Cfg::kThreads, Cfg::kMoveRegs ? Cfg::kLaunchRegs : 0};
 }
 
 }  // namespace gqa

@@ -16,7 +16,9 @@
 // its keys.  Rows past T*G, and tokens past the last one, hold zeros and are
 // never written out.
 //
-// Warps: 4 softmax warps per tile, then one TMA producer and one MMA issuer.
+// Warps: 4 softmax warps per tile, then one TMA producer, one MMA issuer and
+// one that walks the plan and hands the others their items through a ring in
+// shared memory (so that none of them keeps the plan's state in registers).
 // A row of S is one TMEM lane, so one softmax thread holds a whole row: its
 // max and sum need no exchange, P goes back into the TMEM columns of its S
 // (16-bit, the value MMA's A operand) and never passes through shared memory.
@@ -78,6 +80,18 @@ struct RowsParams {
   unsigned long long out_bytes, lse_bytes, o_part_bytes, lse_part_bytes, rec_bytes;
 };
 
+// One item of a CTA: a range of key blocks of one triple.
+struct RowsItem {
+  int b, h;
+  int tok0;               // the first query token of its tiles
+  int blk_begin, blk_end; // blk_begin < 0: no further item
+  int L;                  // keys of batch entry b
+  int piece;              // where its partials go; -1: final output
+  int unused;
+};
+constexpr int kItemRing = 4;
+constexpr uint32_t kPlanSuspendNs = 1000;  // the plan walker is ahead: its waits may sleep
+
 template <int HEAD_DIM>
 struct RowsCfg {
   static constexpr int kTiles = HEAD_DIM == 256 ? 1 : 2;  // row tiles of a CTA
@@ -91,9 +105,17 @@ struct RowsCfg {
   static constexpr int kStagesK = HEAD_DIM == 64 ? 4 : 2;
   static constexpr int kStagesV = kStagesK;
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+  // Two tiles: three warpgroups (softmax, softmax, and the other roles with an
+  // idle warp), so that registers can move from the third to the softmax
+  // warps, which hold a row of 128 scores each: 384 threads x 168 at launch =
+  // 256 x 208 + 128 x 88.  One tile: 224 threads have registers enough.
+  static constexpr bool kMoveRegs = kTiles == 2;
+  static constexpr int kThreads = kMoveRegs ? 384 : 224;
+  static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kControlRegs = 88;
+  static_assert(256 * kSoftmaxRegs + 128 * kControlRegs <= 384 * kLaunchRegs, "more registers than the launch has");
   static constexpr int kRingBytes = (kStagesK + kStagesV) * kStageBytes;
-  static constexpr int kMiscBytes = 512 + 4 * kMaxSmemB + 4 * (kMaxSmemB + 1) + 60;
+  static constexpr int kItemBytes = kItemRing * static_cast<int>(sizeof(RowsItem));
+  static constexpr int kMiscBytes = 512 + kItemBytes + 4 * kMaxSmemB + 4 * (kMaxSmemB + 1) + 60;
   static constexpr int kSmemBytes = 1024 + kQBytes + kRingBytes + kMiscBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 256;  // after the two S slots of 128 columns
@@ -109,7 +131,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   using Cfg = RowsCfg<HEAD_DIM>;
   constexpr int NT = Cfg::kTiles, KCH = Cfg::kChunks, TCH = Cfg::kTileChunks, TPB = Cfg::kTilesPerBlock;
   constexpr uint32_t NSK = Cfg::kStagesK, NSV = Cfg::kStagesV;
-  constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1;
+  constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1, kPlanWarp = kProducerWarp + 2;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -118,7 +140,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   uint8_t* vring = kring + NSK * Cfg::kStageBytes;
   uint8_t* misc = vring + NSV * Cfg::kStageBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(misc);
-  int32_t* s_len = reinterpret_cast<int32_t*>(misc + 512);
+  RowsItem* items_ring = reinterpret_cast<RowsItem*>(misc + 512);
+  int32_t* s_len = reinterpret_cast<int32_t*>(misc + 512 + Cfg::kItemBytes);
   int32_t* s_pre = s_len + kMaxSmemB;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pre + kMaxSmemB + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -131,8 +154,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
                 Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + 1, S_FULL = Q_EMPTY + 1, P_FULL = S_FULL + 2,
-                O_FULL = P_FULL + 2, DRAIN = O_FULL + 2;
-  static_assert(DRAIN < 64, "barrier words");
+                O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing;
+  static_assert(ITEM_EMPTY + kItemRing <= 64, "barrier words");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PlanParams plan = p.plan;
@@ -156,6 +179,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       ptx::mbar_init(BAR(O_FULL + i), 1);
     }
     ptx::mbar_init(BAR(DRAIN), 1);
+    for (int i = 0; i < kItemRing; ++i) {
+      ptx::mbar_init(BAR(ITEM_FULL + i), 1);
+      ptx::mbar_init(BAR(ITEM_EMPTY + i), Cfg::kSoftmaxWarps + 2);  // softmax warps, producer, issuer
+    }
     *abort_flag = 0;
     ptx::fence_barrier_init();
     ptx::prefetch_tensormap(&p.tm_q);
@@ -214,21 +241,32 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  WorkIter iter;
-  iter.init_warp(plan, p.lens, s_len, s_pre, blockIdx.x, lane);
-  WorkItem it;
-  auto head_of = [&](const WorkItem& w) { return w.h / p.groups; };
-  auto token_of = [&](const WorkItem& w) { return (w.h % p.groups) * (NT * p.tokens); };  // its first query token
+  // The next item of this role (one thread, or a whole warp): waits for it,
+  // copies it, releases its place.  False at the end of the work, or, with
+  // ok = false, when the wait ran out.
+  uint32_t n_items = 0;
+  auto next_item = [&](RowsItem& it, bool& ok, bool whole_warp) -> bool {
+    const int i = static_cast<int>(n_items % kItemRing);
+    ok = ok && ptx::mbar_wait_bounded(BAR(ITEM_FULL + i), (n_items / kItemRing) & 1u, abort_flag, p.timeout_ns);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it = items_ring[i];
+    if (whole_warp) __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(BAR(ITEM_EMPTY + i));
+    ++n_items;
+    return it.blk_begin >= 0;
+  };
   // row tiles of an item that hold any token (at least one)
-  auto tiles_of = [&](const WorkItem& w) { return NT == 2 && token_of(w) + p.tokens < p.nq ? 2 : 1; };
+  auto tiles_of = [&](const RowsItem& w) { return NT == 2 && w.tok0 + p.tokens < p.nq ? 2 : 1; };
 
+  if (warp >= kProducerWarp) {
+  if constexpr (Cfg::kMoveRegs) ptx::regs_dec<Cfg::kControlRegs>();
   if (warp == kProducerWarp) {
     // ============================================================= producer
     if (lane == 0) {
       uint32_t tk = 0, tv = 0, items = 0;  // ring tiles and items loaded
       bool ok = true;
-      auto load_block = [&](bool is_v, const WorkItem& w, int blk) -> bool {
-        const int h = head_of(w);
+      auto load_block = [&](bool is_v, const RowsItem& w, int blk) -> bool {
 #pragma unroll
         for (int hf = 0; hf < TPB; ++hf) {
           const uint32_t n = is_v ? tv : tk, ns = is_v ? NSV : NSK, stage = n % ns;
@@ -237,30 +275,31 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           // the first pass over a ring needs no wait
           if (n >= ns && !ptx::mbar_wait_bounded(empty, ((n / ns) & 1u) ^ 1u, abort_flag, p.timeout_ns)) return false;
           ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
-          detail::check_coord(p.err_word, w.b >= 0 && w.b < B && h >= 0 && h * p.groups < plan.kv_heads && blk >= 0 &&
+          detail::check_coord(p.err_word, w.b >= 0 && w.b < B && w.h >= 0 && w.h * p.groups < plan.kv_heads && blk >= 0 &&
                                               blk * kBlockN < plan.max_seqlen);
           uint8_t* dst = (is_v ? vring : kring) + stage * Cfg::kStageBytes;
 #pragma unroll
           for (int kc = 0; kc < TCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &p.tm_v : &p.tm_k, full, (hf * TCH + kc) * 64, h,
+            ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &p.tm_v : &p.tm_k, full, (hf * TCH + kc) * 64, w.h,
                              blk * kBlockN, w.b);
           if (is_v) ++tv; else ++tk;
         }
         return true;
       };
-      while (ok && iter.next(it)) {
+      RowsItem it;
+      while (next_item(it, ok, false)) {
         if (it.blk_begin >= it.blk_end) continue;
         if (items >= 1 && !ptx::mbar_wait_bounded(BAR(Q_EMPTY), (items & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
           ok = false;
           break;
         }
-        const int nt = tiles_of(it), tok0 = token_of(it), h = head_of(it);
+        const int nt = tiles_of(it);
         ptx::mbar_arrive_expect_tx(BAR(Q_FULL), static_cast<uint32_t>(nt * KCH * p.tokens * p.G * 128));
         for (int t = 0; t < nt; ++t)
 #pragma unroll
           for (int kc = 0; kc < KCH; ++kc)
             ptx::tma_load_4d(ptx::smem_u32(qbuf + t * Cfg::kQTileBytes + kc * 16384), &p.tm_q, BAR(Q_FULL), kc * 64,
-                             h * p.G, tok0 + t * p.tokens, it.b);
+                             it.h * p.G, it.tok0 + t * p.tokens, it.b);
         ++items;
         // K0, then V(i), K(i+1) in the order the MMAs take them
         ok = load_block(false, it, it.blk_begin);
@@ -268,6 +307,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           if (blk + 1 < it.blk_end) ok = load_block(false, it, blk + 1);
           if (ok) ok = load_block(true, it, blk);
         }
+        if (!ok) break;
       }
       if (!ok) {
         detail::set_error(p.err_word, kErrTimeout, abort_flag);
@@ -334,7 +374,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
 #pragma unroll
         for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit(BAR(ring_empty + static_cast<int>((u2 * TPB + hf) % ns)));
       };
-      while (ok && iter.next(it)) {
+      RowsItem it;
+      while (next_item(it, ok, false)) {
         const int n = it.blk_end - it.blk_begin;
         if (n <= 0) continue;
         const int nt = tiles_of(it);
@@ -388,17 +429,66 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       ptx::mbar_wait_bounded(BAR(DRAIN), 0, nullptr, p.timeout_ns);
     }
     __syncwarp();
+  } else if (warp == kPlanWarp) {
+    // ========================================================== plan walker
+    WorkIter iter;
+    iter.init_warp(plan, p.lens, s_len, s_pre, blockIdx.x, lane);
+    if (lane == 0) {
+      bool ok = true;
+      int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
+      for (uint32_t n = 0; ok; ++n) {
+        WorkItem w;
+        const bool more = iter.next(w);
+        RowsItem it;
+        it.blk_begin = -1;
+        it.blk_end = -1;
+        if (more) {
+          const int triple = w.b * plan.kv_heads + w.h;
+          const bool partial = p.all_partial != 0 || w.slot >= 0;
+          const int n_pieces = w.blk_begin < w.blk_end ? w.n_pieces : 0;
+          it.b = w.b;
+          it.h = w.h / p.groups;
+          it.tok0 = (w.h - it.h * p.groups) * (NT * p.tokens);
+          it.blk_begin = w.blk_begin;
+          it.blk_end = w.blk_end;
+          it.L = w.L;
+          it.piece = !partial            ? -1
+                     : p.all_partial != 0 ? triple + static_cast<int>(blockIdx.x)
+                                          : 2 * static_cast<int>(blockIdx.x) + (w.first_piece ? 1 : 0);
+          if (w.first_piece && partial) {
+            if (p.all_partial == 0)
+              cut = make_int2(triple, n_pieces);
+            else if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + triple, sizeof(int2)))
+              p.rec[triple] = make_int2(it.piece, n_pieces);
+          }
+        }
+        const int i = static_cast<int>(n % kItemRing);
+        if (n >= kItemRing)
+          ok = ptx::mbar_wait_bounded(BAR(ITEM_EMPTY + i), ((n / kItemRing) & 1u) ^ 1u, abort_flag, p.timeout_ns,
+                                      kPlanSuspendNs);
+        if (!ok) break;
+        items_ring[i] = it;
+        ptx::mbar_arrive(BAR(ITEM_FULL + i));
+        if (!more) break;
+      }
+      if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
+      // after a timeout too, so that the merge never reads what an earlier call left
+      if (p.all_partial == 0 && p.rec != nullptr &&
+          detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + blockIdx.x, sizeof(int2)))
+        p.rec[blockIdx.x] = cut;
+    }
+    __syncwarp();
+  }
   } else {
     // ======================================================== softmax warps
+    if constexpr (Cfg::kMoveRegs) ptx::regs_inc<Cfg::kSoftmaxRegs>();
     const int t = warp >> 2;                        // this warp's row tile
     const int r = (warp & 3) * 32 + lane;           // its TMEM lane: a row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t o_addr = tmem_base + lanes + Cfg::kOCol + static_cast<uint32_t>(t * HEAD_DIM);
-    const int r_tok = r / p.G, r_head = r - r_tok * p.G;
     const uint64_t scale2 = ptx::pack_f32x2(p.scale_log2, p.scale_log2);
     uint32_t g = 0;  // blocks of this tile
     bool ok = true;
-    int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
     auto pack16 = [](float lo, float hi) -> uint32_t {
       if constexpr (IN_F16) {
         const __half2 v = __floats2half2_rn(lo, hi);
@@ -417,23 +507,9 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       return NT == 2 ? wait(O_FULL + t, blk_g) : wait(O_FULL + static_cast<int>(blk_g & 1u), blk_g >> 1);
     };
 
-    while (ok && iter.next(it)) {
-      const int tok = token_of(it) + t * p.tokens + r_tok, h = head_of(it);
-      const long long triple = static_cast<long long>(it.b) * plan.kv_heads + it.h;
-      const bool partial = p.all_partial != 0 || it.slot >= 0;
-      const int n_pieces = it.blk_begin < it.blk_end ? it.n_pieces : 0;
-      if (it.first_piece && partial) {
-        if (p.all_partial != 0) {
-          if (threadIdx.x == 0 && detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + triple, sizeof(int2)))
-            p.rec[triple] = make_int2(static_cast<int>(triple) + static_cast<int>(blockIdx.x), n_pieces);
-        } else {
-          cut = make_int2(static_cast<int>(triple), n_pieces);
-        }
-      }
+    RowsItem it;
+    while (next_item(it, ok, true)) {
       if (t >= tiles_of(it)) continue;
-      const bool row_valid = r_tok < p.tokens && tok < p.nq;
-      const long long row = (static_cast<long long>(it.b) * p.nq + tok) * p.Hq + h * p.G + r_head;
-
       float nm = kNoMax, l = 0.f;  // -max (log2 units; kNoMax while it is -inf) and the sum of this row
       for (int blk = it.blk_begin; blk < it.blk_end; ++blk, ++g) {
         const uint32_t slot = NT == 2 ? static_cast<uint32_t>(t) : (g & 1u);
@@ -509,11 +585,11 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         // P, in place of the scores: 16-bit, two to a column
         const uint64_t nm2 = ptx::pack_f32x2(nm, nm);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int k = 64 * c + 2 * j;
+          for (int j = 0; j < 16; ++j) {
+            const int k = 32 * c + 2 * j;
             float a, b;
             ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale2,
                                              nm2), a, b);
@@ -523,7 +599,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             x[k + 1] = __float_as_uint(b);
             w[j] = pack16(a, b);
           }
-          ptx::tmem_st_32x32b_x32(s_addr + 32 * c, w);
+          ptx::tmem_st_32x32b_x16u(s_addr + 16 * c, w);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -542,17 +618,18 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       if (!ok) break;
 
       // ------------------------------------------------------------ epilogue
-      const bool empty = it.blk_begin >= it.blk_end;
+      const bool empty = it.blk_begin >= it.blk_end, partial = it.piece >= 0;
       if (empty && partial) continue;  // 0 pieces: the merge reads nothing of this triple
       if (!empty) {
         if (!wait_pv(g - 1)) break;
         ptx::tc_fence_after();
       }
+      const int r_tok = r / p.G, tok = it.tok0 + t * p.tokens + r_tok;
+      const bool row_valid = r_tok < p.tokens && tok < p.nq;
+      const long long row = (static_cast<long long>(it.b) * p.nq + tok) * p.Hq + it.h * p.G + (r - r_tok * p.G);
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // a row that saw only -inf scores: 0; NaN stays NaN
       const float lse = l > 0.f || l != l ? 0.69314718055994531f * (__log2f(l) - nm) : -INFINITY;
-      const long long piece = p.all_partial != 0 ? triple + blockIdx.x
-                                                 : 2ll * blockIdx.x + (it.first_piece ? 1 : 0);
-      const long long prow = (piece * NT + t) * kTileRows + r;
+      const long long prow = (static_cast<long long>(it.piece) * NT + t) * kTileRows + r;
       const bool out16 = !partial && p.out_dtype != kOutF32;
       uint8_t* dst;
       bool store;
@@ -609,10 +686,6 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       }
     }
     if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
-    // after a timeout too, so that the merge never reads what an earlier call left
-    if (threadIdx.x == 0 && p.all_partial == 0 && p.rec != nullptr &&
-        detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + blockIdx.x, sizeof(int2)))
-      p.rec[blockIdx.x] = cut;
   }
 
   // ---------------------------------------------------------------- teardown
