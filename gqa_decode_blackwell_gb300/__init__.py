@@ -109,7 +109,7 @@ def load_library(path: str) -> ctypes.CDLL:
     L.gqa_prefix_workspace_size.restype = SZ
     L.gqa_prefix_attn.argtypes = [D, P, P, P, P, I, P, P, P, P, P, P, SZ, P]
     L.gqa_prefix_attn.restype = I
-    L.gqa_shared_keys_plan.argtypes = [D, I, P, I, ctypes.POINTER(I), ctypes.POINTER(I), ctypes.POINTER(I), P, I64,
+    L.gqa_shared_keys_plan.argtypes = [D, I, I, P, I, ctypes.POINTER(I), ctypes.POINTER(I), P, P, I64,
                                        ctypes.POINTER(I64)]
     L.gqa_shared_keys_plan.restype = I
     return L
@@ -445,20 +445,23 @@ def prefix_decode(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens, 
     return out, lse
 
 
-def gqa_shared_keys_plan(desc: gqa_desc_t, kv_lens_host, every_piece: bool = False, sm_count: int = 0):
-    """The tiled kernel's decomposition as (num_ctas, group_tokens, num_pieces, items int32 [n, 8])."""
+def gqa_shared_keys_plan(desc: gqa_desc_t, kv_lens_host, prefix_len: int = 0, max_prefix: int = 0,
+                         sm_count: int = 0):
+    """The tiled kernel's decomposition as (num_ctas, every_piece, info int32 [2, 4], items int32 [n, 9]);
+    see gqa_shared_keys_plan in ``include/gqa_shared_keys.h``."""
     import numpy as np
 
     sl = np.ascontiguousarray(np.asarray(kv_lens_host, dtype=np.int32))
-    nc, gt, pieces, n = ctypes.c_int(), ctypes.c_int(), ctypes.c_int(), ctypes.c_int64()
+    nc, every, n = ctypes.c_int(), ctypes.c_int(), ctypes.c_int64()
+    info = np.zeros((2, 4), dtype=np.int32)
 
     def call(items, cap):
-        _check(lib().gqa_shared_keys_plan(ctypes.byref(desc), int(every_piece), sl.ctypes.data, int(sm_count),
-                                          ctypes.byref(nc), ctypes.byref(gt), ctypes.byref(pieces),
+        _check(lib().gqa_shared_keys_plan(ctypes.byref(desc), int(prefix_len), int(max_prefix), sl.ctypes.data,
+                                          int(sm_count), ctypes.byref(nc), ctypes.byref(every), info.ctypes.data,
                                           None if items is None else items.ctypes.data, cap, ctypes.byref(n)),
                "gqa_shared_keys_plan")
 
     call(None, 0)
-    items = np.zeros((n.value, 8), dtype=np.int32)
+    items = np.zeros((n.value, 9), dtype=np.int32)
     call(items, n.value)
-    return nc.value, gt.value, pieces.value, items
+    return nc.value, bool(every.value), info, items

@@ -131,6 +131,15 @@ gqa_status_t check_desc(const gqa_desc_t* d) {
 
 namespace {
 
+struct HostPlan {
+  PlanParams pp;
+  int num_slots;      // partial slots per row (0: the decode writes final outputs only)
+  bool combine;       // a combine launch follows
+  bool use_n_pieces;  // combine reads per-pair piece counts (balanced plan)
+  int cluster_k;      // > 1: the k splits of a pair form a cluster and merge in it
+  gqa_status_t status;  // GQA_ERR_UNSUPPORTED: an in-cluster merge was asked for and cannot be done
+};
+
 // Largest power of two <= x, for 1 <= x (capped at kMaxClusterK).
 int pow2_floor_k(long long x) {
   int k = 1;
@@ -205,8 +214,6 @@ int cluster_splits(const gqa_desc_t* d, int num_splits, int sm, bool force_parti
   if (forced) return (pow2 && num_splits <= kMaxClusterK) ? num_splits : -1;
   return (num_splits == 2 && pairs * 2 >= 128) ? 2 : 0;
 }
-
-}  // namespace
 
 HostPlan make_plan(const gqa_desc_t* d, int num_splits, int sm, bool force_partial) {
   HostPlan hp;
@@ -284,8 +291,6 @@ HostPlan make_plan(const gqa_desc_t* d, int num_splits, int sm, bool force_parti
   hp.use_n_pieces = false;
   return hp;
 }
-
-namespace {
 
 struct WsLayout {
   size_t o_off, lse_off, np_off, total;
@@ -404,7 +409,9 @@ cudaLaunchAttribute pdl_attr(bool on) {
   return a;
 }
 
-static KernelRef decode_kernel_ref(int head_dim, int np, bool f16, bool cluster) {
+namespace {
+
+KernelRef decode_kernel_ref(int head_dim, int np, bool f16, bool cluster) {
   if (head_dim == 64) return cluster ? decode_kernel_ref_64_1(np, f16) : decode_kernel_ref_64_0(np, f16);
   if (head_dim == 256) return cluster ? decode_kernel_ref_256_1(np, f16) : decode_kernel_ref_256_0(np, f16);
   return cluster ? decode_kernel_ref_128_1(np, f16) : decode_kernel_ref_128_0(np, f16);
@@ -446,7 +453,7 @@ gqa_status_t launch_decode(DeviceState* st, DecodeParams& p, bool in_f16, cudaSt
   return GQA_OK;
 }
 
-static gqa_status_t launch_combine(const CombineParams& c, int head_dim, cudaStream_t s) {
+gqa_status_t launch_combine(const CombineParams& c, int head_dim, cudaStream_t s) {
   if (c.rows == 0) return GQA_OK;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
@@ -465,17 +472,21 @@ static gqa_status_t launch_combine(const CombineParams& c, int head_dim, cudaStr
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
+}  // namespace
+
 gqa_status_t check_inputs(const void* q, const void* k, const void* v, const int32_t* seqlens) {
   if (q == nullptr || k == nullptr || v == nullptr || seqlens == nullptr) return GQA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(seqlens, 4)) return GQA_ERR_INVALID_ARG;
   return GQA_OK;
 }
 
+namespace {
+
 // Common front half of gqa_decode_attn / gqa_decode_splitkv.
 gqa_status_t prepare_decode(const gqa_desc_t* d, const void* q, const void* k, const void* v,
-                            const int32_t* seqlens, const HostPlan& hp, DecodeParams* p, bool keep_maps) {
+                            const int32_t* seqlens, const HostPlan& hp, DecodeParams* p) {
   std::memset(p, 0, sizeof *p);
-  gqa_status_t rc = keep_maps ? encode_maps(d, q, k, v, p) : encode_maps_uncached(d, q, k, v, p);
+  gqa_status_t rc = encode_maps(d, q, k, v, p);
   if (rc != GQA_OK) return rc;
   p->seqlens = seqlens;
   p->plan = hp.pp;
@@ -492,8 +503,6 @@ gqa_status_t prepare_decode(const gqa_desc_t* d, const void* q, const void* k, c
   p->timeout_ns = wait_timeout_ns();
   return GQA_OK;
 }
-
-namespace {
 
 __global__ void selftest_wait_kernel(unsigned long long timeout_ns) {
   __shared__ uint64_t bar;

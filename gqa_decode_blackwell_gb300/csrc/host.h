@@ -1,6 +1,5 @@
 // What the host side of gqa_decode.cu shares with that of gqa_shared_keys.cu:
-// device state, argument checks, tensor-map encoding, split plans and the
-// decode kernel's launch.
+// device state, argument checks and the encoder of tensor maps.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -9,8 +8,6 @@
 #include <cstdint>
 
 #include "../../include/gqa_decode.h"
-#include "decode_kernel.cuh"
-#include "plan.cuh"
 
 namespace gqa {
 
@@ -26,15 +23,6 @@ struct DeviceState {
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-struct HostPlan {
-  PlanParams pp;
-  int num_slots;      // partial slots per row (0: the decode writes final outputs only)
-  bool combine;       // a combine launch follows
-  bool use_n_pieces;  // combine reads per-pair piece counts (balanced plan)
-  int cluster_k;      // > 1: the k splits of a pair form a cluster and merge in it
-  gqa_status_t status;  // GQA_ERR_UNSUPPORTED: an in-cluster merge was asked for and cannot be done
-};
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -52,11 +40,5 @@ cudaLaunchAttribute pdl_attr(bool on);
 gqa_status_t check_desc_any_rows(const gqa_desc_t* d);
 gqa_status_t check_desc(const gqa_desc_t* d);
 gqa_status_t check_inputs(const void* q, const void* k, const void* v, const int32_t* seqlens);
-HostPlan make_plan(const gqa_desc_t* d, int num_splits, int sm, bool force_partial);
-// Everything of a decode launch but its outputs.  keep_maps: the tensor maps
-// are kept for a later call on the same buffers.
-gqa_status_t prepare_decode(const gqa_desc_t* d, const void* q, const void* k, const void* v,
-                            const int32_t* seqlens, const HostPlan& hp, DecodeParams* p, bool keep_maps = true);
-gqa_status_t launch_decode(DeviceState* st, DecodeParams& p, bool in_f16, cudaStream_t s);
 
 }  // namespace gqa

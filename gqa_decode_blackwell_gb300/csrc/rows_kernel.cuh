@@ -22,19 +22,24 @@
 // A row of S is one TMEM lane, so one softmax thread holds a whole row: its
 // max and sum need no exchange, P goes back into the TMEM columns of its S
 // (16-bit, the value MMA's A operand) and never passes through shared memory.
-//   head_dim 64, 128: two tiles (256 rows) share each K/V block; one tile's
-//     softmax runs under the other's MMAs (QK of its next block, PV of this).
+//   head_dim 64, 128: two tiles; one's softmax runs under the other's MMAs.
+//     They are 256 rows that share each K/V block, or, where 128 rows hold
+//     all the query rows there are, the same rows with the key blocks dealt to
+//     them in turn ("split keys"): each then leaves a partial of its own.
 //   head_dim 256: O takes half of TMEM, so there is one tile, with two S
 //     slots: the next block's QK runs under this block's softmax.  K and V
 //     blocks are two ring tiles each, their 128-element d-halves.
 //
 // The running max is only replaced when it grows by more than 8 (log2 units),
 // as in the decode kernel; a warp whose rows need it rescales its own lanes
-// of O, after the value MMA of the block before has landed.
+// of O, after the value MMA of the block before has landed.  Warps whose rows
+// all lie past the tile's last one only keep step.
 //
-// Work: the (batch, KV head, tile) triples are cut by plan.cuh's balanced
-// partition, triples in the place of (batch, KV head) pairs.  A triple that
-// is cut leaves fp32 partials (normalised O_s, lse_s) for rows_merge.cuh.
+// Work: rows_plan.cuh.  A launch has one section of batch entries (cross
+// attention), or two: a prefix that a batch shares, all its rows as one
+// entry, and the sequences' own keys.  Triples that are cut, or all of them
+// (every_piece), leave fp32 partials (normalised O_s, lse_s) for
+// rows_merge.cuh.
 //
 // Every wait is bounded, as in the decode kernel.
 #pragma once
@@ -44,35 +49,44 @@
 #include <cuda_fp16.h>
 
 #include "decode_kernel.cuh"
-#include "plan.cuh"
+#include "rows_plan.cuh"
 #include "rows_ptx.cuh"
 
 namespace gqa {
 
 constexpr int kTileRows = 128;  // query rows of a tile (the MMA M dimension)
 
-struct RowsParams {
-  CUtensorMap tm_q;     // q [B, nq, Hq, d], box {64, G, T, 1}
+struct RowsSection {
+  CUtensorMap tm_q;     // q [B, nq, Hq, d], box {64, G, tokens, 1}
   CUtensorMap tm_k;     // k [B, S_max, Hkv, d], box {64, 1, 128, 1}
   CUtensorMap tm_v;     // v, same
-  const int32_t* lens;  // [B] keys of each batch entry
+  const int32_t* lens;  // [B] keys of each entry
+  long long part_row;   // first of the section's partial rows
+  long long rec;        // first of its records (every_piece)
+  int nq;               // query tokens of an entry
+  int tokens;           // query tokens of a tile: at most 128 / G
+  int groups;           // tile groups of an entry: triples are h * groups + group
+  int split_keys;       // both tiles hold the same rows
+  int causal;           // token t sees keys j <= L - nq + t
+  int triples;          // of the section
+};
+
+struct RowsParams {
+  RowsSection s[2];
+  RowsPlan plan;
   void* out;            // [B, nq, Hq, d] bf16, fp16 or fp32: the rows of uncut triples
   float* lse;           // [B, nq, Hq] or null
-  float* o_part;        // [pieces][tiles per triple][128][d]
-  float* lse_part;      // [pieces][tiles per triple][128]
-  int2* rec;            // what was cut, for the merge (see below)
-  PlanParams plan;      // kv_heads: Hkv * groups, h' = h * groups + (tile group)
-  int nq, Hq, G, groups;
-  int tokens;           // T: query tokens of a tile
+  float* o_part;        // partial rows of d; a piece of a section holds kTiles * tokens * G of them, tile by tile
+  float* lse_part;      // one per partial row
+  // every_piece: rec[triple] = {first piece, pieces} (0 pieces: no keys), the
+  // pieces consecutive.  Else rec[CTA] = {triple, pieces} of the cut triple
+  // that begins in this CTA (at most one), or {-1, 0}; its pieces are
+  // 2 * CTA + 1 and then 2 * c of the CTAs c that follow.
+  int2* rec;
+  int Hq, G;
   int out_dtype;
   int out_v32;          // out is 32-byte aligned
-  // 0: an uncut triple's rows go to out / lse; piece indexes are 2 * CTA,
-  //    + 1 for the triple's first piece; rec[CTA] = {triple, pieces} of the
-  //    cut triple that begins in this CTA (at most one), or {-1, 0}.
-  // 1: every triple leaves partials; piece index triple + CTA, which no two
-  //    pieces share as both grow along the plan; rec[triple] = {first piece
-  //    index, pieces}, 0 pieces when it has no keys.
-  int all_partial;
+  int every_piece;      // every triple leaves partials, none writes out / lse
   float scale_log2;
   unsigned long long timeout_ns;
   unsigned int* err_word;
@@ -82,14 +96,14 @@ struct RowsParams {
 
 // One item of a CTA: a range of key blocks of one triple.
 struct RowsItem {
-  int b, h;
+  int section, b, h;
   int tok0;               // the first query token of its tiles
   int blk_begin, blk_end; // blk_begin < 0: no further item
-  int L;                  // keys of batch entry b
+  int L;                  // keys of entry b
   int piece;              // where its partials go; -1: final output
-  int unused;
 };
 constexpr int kItemRing = 4;
+constexpr uint64_t kBlockNs = 20000;       // far more than a key block of an item takes
 constexpr uint32_t kPlanSuspendNs = 1000;  // the plan walker is ahead: its waits may sleep
 
 template <int HEAD_DIM>
@@ -100,7 +114,7 @@ struct RowsCfg {
   static constexpr int kTileChunks = kTileDim / 64;
   static constexpr int kTilesPerBlock = HEAD_DIM / kTileDim;  // ring tiles of a K or V block
   static constexpr int kStageBytes = kBlockN * kTileDim * 2;
-  static constexpr int kQTileBytes = kTileRows * HEAD_DIM * 2;
+  static constexpr int kQTileBytes = kTileRows * HEAD_DIM * 2;  // one of kTiles Q slots, taken in turn
   static constexpr int kQBytes = kTiles * kQTileBytes;
   static constexpr int kStagesK = HEAD_DIM == 64 ? 4 : 2;
   static constexpr int kStagesV = kStagesK;
@@ -115,7 +129,8 @@ struct RowsCfg {
   static_assert(256 * kSoftmaxRegs + 128 * kControlRegs <= 384 * kLaunchRegs, "more registers than the launch has");
   static constexpr int kRingBytes = (kStagesK + kStagesV) * kStageBytes;
   static constexpr int kItemBytes = kItemRing * static_cast<int>(sizeof(RowsItem));
-  static constexpr int kMiscBytes = 512 + kItemBytes + 4 * kMaxSmemB + 4 * (kMaxSmemB + 1) + 60;
+  static constexpr int kPlanBytes = 8 * (kMaxRowsEntries + 1) + 4 * kMaxRowsEntries;
+  static constexpr int kMiscBytes = 512 + kItemBytes + kPlanBytes + 16;
   static constexpr int kSmemBytes = 1024 + kQBytes + kRingBytes + kMiscBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 256;  // after the two S slots of 128 columns
@@ -141,9 +156,9 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   uint8_t* misc = vring + NSV * Cfg::kStageBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(misc);
   RowsItem* items_ring = reinterpret_cast<RowsItem*>(misc + 512);
-  int32_t* s_len = reinterpret_cast<int32_t*>(misc + 512 + Cfg::kItemBytes);
-  int32_t* s_pre = s_len + kMaxSmemB;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pre + kMaxSmemB + 1);
+  long long* s_pre = reinterpret_cast<long long*>(misc + 512 + Cfg::kItemBytes);
+  int32_t* s_len = reinterpret_cast<int32_t*>(s_pre + kMaxRowsEntries + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_len + kMaxRowsEntries);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t bar_base = ptx::smem_u32(bar);
@@ -153,13 +168,13 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // awaited one is known to be complete; with one tile, QK(g) is issued ahead
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
-                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + 1, S_FULL = Q_EMPTY + 1, P_FULL = S_FULL + 2,
+                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NT, S_FULL = Q_EMPTY + NT, P_FULL = S_FULL + 2,
                 O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing;
   static_assert(ITEM_EMPTY + kItemRing <= 64, "barrier words");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PlanParams plan = p.plan;
-  const int B = plan.batch;
+  // (a shuffle tells the compiler that it is the same in all the warp)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int n0 = p.plan.s[0].batch, n_entries = n0 + p.plan.s[1].batch;
 
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
@@ -171,8 +186,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       ptx::mbar_init(BAR(V_FULL + i), 1);
       ptx::mbar_init(BAR(V_EMPTY + i), 1);
     }
-    ptx::mbar_init(BAR(Q_FULL), 1);
-    ptx::mbar_init(BAR(Q_EMPTY), 1);
+    for (int i = 0; i < NT; ++i) {
+      ptx::mbar_init(BAR(Q_FULL + i), 1);
+      ptx::mbar_init(BAR(Q_EMPTY + i), 1);
+    }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(BAR(S_FULL + i), 1);
       ptx::mbar_init(BAR(P_FULL + i), 4);  // one arrival per softmax warp of the tile
@@ -185,56 +202,34 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
-    ptx::prefetch_tensormap(&p.tm_q);
-    ptx::prefetch_tensormap(&p.tm_k);
-    ptx::prefetch_tensormap(&p.tm_v);
+    for (int i = 0; i < 2; ++i) {
+      if (p.plan.s[i].batch == 0) continue;
+      ptx::prefetch_tensormap(&p.s[i].tm_q);
+      ptx::prefetch_tensormap(&p.s[i].tm_k);
+      ptx::prefetch_tensormap(&p.s[i].tm_v);
+    }
   }
   __syncwarp();
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), Cfg::kTmemCols);
     ptx::tmem_relinquish();
   }
-  // Rows past T*G of each 64-element chunk of Q: TMA never writes them.
-  {
-    const int used = p.tokens * p.G;
-    for (int i = threadIdx.x; i < NT * KCH * kTileRows; i += Cfg::kThreads) {
-      if (i % kTileRows < used) continue;
-      uint4* row = reinterpret_cast<uint4*>(qbuf + i * 128);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
-    }
-    ptx::fence_proxy_async_smem();
-  }
+  // Q rows that no TMA box writes (past tokens * G) stay zero or become an
+  // earlier item's: rows of S that no one reads.
+  for (int i = threadIdx.x; i < Cfg::kQBytes / 16; i += Cfg::kThreads)
+    reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
   // Lengths may be produced, and outputs still read, by the previous kernel.
   ptx::griddep_wait();
   // The next launch may set itself up; it waits for this grid before it
   // reads or writes anything this grid touches.
   ptx::griddep_launch_dependents();
-  if (plan.mode == PLAN_BALANCED && warp == 0) {
-    int run = 0;
-    for (int base = 0; base < B; base += 32) {
-      const int i = base + lane;
-      int nb = 0;
-      if (i < B) {
-        const int raw = p.lens[i], L = clamp_len(raw, plan.max_seqlen);
-        if (raw != L) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
-        s_len[i] = L;
-        nb = pair_units(num_blocks(L), plan.item_units);
-      }
-      int incl = nb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (i < B) s_pre[i] = run + incl - nb;
-      run += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) s_pre[B] = run;
-  } else if (plan.mode != PLAN_BALANCED && blockIdx.x == 0) {
-    // lengths too many to stage: each item reads its own; one CTA flags the bad ones
-    for (int i = threadIdx.x; i < B; i += Cfg::kThreads)
-      if (p.lens[i] != clamp_len(p.lens[i], plan.max_seqlen)) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
+  for (int i = threadIdx.x; i < n_entries; i += Cfg::kThreads) {
+    const int sec = i < n0 ? 0 : 1;
+    const int raw = p.s[sec].lens[i - (sec ? n0 : 0)], L = clamp_len(raw, p.plan.s[sec].max_len);
+    if (p.plan.dealt == 0) s_len[i] = L;
+    if (raw != L && blockIdx.x == 0) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
+    if (p.plan.dealt != 0 && blockIdx.x != 0) break;  // only flagged, by one CTA
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -256,17 +251,21 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     ++n_items;
     return it.blk_begin >= 0;
   };
-  // row tiles of an item that hold any token (at least one)
-  auto tiles_of = [&](const RowsItem& w) { return NT == 2 && w.tok0 + p.tokens < p.nq ? 2 : 1; };
+  // Q slots of an item: its row tiles that hold any token (at least one)
+  auto slots_of = [&](const RowsItem& w) {
+    const RowsSection& s = p.s[w.section];
+    return NT == 2 && s.split_keys == 0 && w.tok0 + s.tokens < s.nq ? 2 : 1;
+  };
 
   if (warp >= kProducerWarp) {
   if constexpr (Cfg::kMoveRegs) ptx::regs_dec<Cfg::kControlRegs>();
   if (warp == kProducerWarp) {
     // ============================================================= producer
     if (lane == 0) {
-      uint32_t tk = 0, tv = 0, items = 0;  // ring tiles and items loaded
+      uint32_t tk = 0, tv = 0, tq = 0;  // ring tiles and Q slots loaded
       bool ok = true;
       auto load_block = [&](bool is_v, const RowsItem& w, int blk) -> bool {
+        const RowsSection& s = p.s[w.section];
 #pragma unroll
         for (int hf = 0; hf < TPB; ++hf) {
           const uint32_t n = is_v ? tv : tk, ns = is_v ? NSV : NSK, stage = n % ns;
@@ -275,13 +274,14 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           // the first pass over a ring needs no wait
           if (n >= ns && !ptx::mbar_wait_bounded(empty, ((n / ns) & 1u) ^ 1u, abort_flag, p.timeout_ns)) return false;
           ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
-          detail::check_coord(p.err_word, w.b >= 0 && w.b < B && w.h >= 0 && w.h * p.groups < plan.kv_heads && blk >= 0 &&
-                                              blk * kBlockN < plan.max_seqlen);
+          detail::check_coord(p.err_word, w.b >= 0 && w.b < p.plan.s[w.section].batch && w.h >= 0 &&
+                                              (w.h + 1) * p.G <= p.Hq && blk >= 0 &&
+                                              blk * kBlockN < p.plan.s[w.section].max_len);
           uint8_t* dst = (is_v ? vring : kring) + stage * Cfg::kStageBytes;
 #pragma unroll
           for (int kc = 0; kc < TCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &p.tm_v : &p.tm_k, full, (hf * TCH + kc) * 64, w.h,
-                             blk * kBlockN, w.b);
+            ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &s.tm_v : &s.tm_k, full, (hf * TCH + kc) * 64,
+                             w.h, blk * kBlockN, w.b);
           if (is_v) ++tv; else ++tk;
         }
         return true;
@@ -289,20 +289,22 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       RowsItem it;
       while (next_item(it, ok, false)) {
         if (it.blk_begin >= it.blk_end) continue;
-        if (items >= 1 && !ptx::mbar_wait_bounded(BAR(Q_EMPTY), (items & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
-          ok = false;
-          break;
-        }
-        const int nt = tiles_of(it);
-        ptx::mbar_arrive_expect_tx(BAR(Q_FULL), static_cast<uint32_t>(nt * KCH * p.tokens * p.G * 128));
-        for (int t = 0; t < nt; ++t)
+        const RowsSection& s = p.s[it.section];
+        const int nt = slots_of(it);
+        for (int t = 0; t < nt; ++t, ++tq) {
+          const int slot = static_cast<int>(tq % NT);
+          if (tq >= NT && !ptx::mbar_wait_bounded(BAR(Q_EMPTY + slot), ((tq / NT) & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx(BAR(Q_FULL + slot), static_cast<uint32_t>(KCH * s.tokens * p.G * 128));
 #pragma unroll
           for (int kc = 0; kc < KCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(qbuf + t * Cfg::kQTileBytes + kc * 16384), &p.tm_q, BAR(Q_FULL), kc * 64,
-                             it.h * p.G, it.tok0 + t * p.tokens, it.b);
-        ++items;
-        // K0, then V(i), K(i+1) in the order the MMAs take them
-        ok = load_block(false, it, it.blk_begin);
+            ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384), &s.tm_q, BAR(Q_FULL + slot),
+                             kc * 64, it.h * p.G, it.tok0 + t * s.tokens, it.b);
+        }
+        // K0, then K(i+1), V(i): at most one block of K ahead of its V
+        if (ok) ok = load_block(false, it, it.blk_begin);
         for (int blk = it.blk_begin; blk < it.blk_end && ok; ++blk) {
           if (blk + 1 < it.blk_end) ok = load_block(false, it, blk + 1);
           if (ok) ok = load_block(true, it, blk);
@@ -316,156 +318,185 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           ptx::mbar_wait_bounded(BAR(K_FULL + static_cast<int>(u % NSK)), (u / NSK) & 1u, nullptr, p.timeout_ns);
         for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
           ptx::mbar_wait_bounded(BAR(V_FULL + static_cast<int>(u % NSV)), (u / NSV) & 1u, nullptr, p.timeout_ns);
-        if (items > 0) ptx::mbar_wait_bounded(BAR(Q_FULL), (items - 1) & 1u, nullptr, p.timeout_ns);
+        for (uint32_t u = tq > NT ? tq - NT : 0u; u < tq; ++u)
+          ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(u % NT)), (u / NT) & 1u, nullptr, p.timeout_ns);
       }
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // =========================================================== MMA issuer
-    if (lane == 0) {
+    // The whole warp walks the items, converged, and one elected thread issues.
+    {
       constexpr uint32_t idesc_qk = ptx::idesc_f16_f32(128, kBlockN, 0, 0, !IN_F16);
       constexpr uint32_t idesc_pv = ptx::idesc_f16_f32(128, Cfg::kTileDim, 0, 1, !IN_F16);
       const uint64_t q_desc = ptx::smem_desc_sw128(ptx::smem_u32(qbuf), 16, 1024);
       const uint64_t k_desc = ptx::smem_desc_sw128(ptx::smem_u32(kring), 16, 1024);
       // V as the MN-major B operand: 64-element chunks of d 16 KB apart, 8 keys 1 KB
       const uint64_t v_desc = ptx::smem_desc_sw128(ptx::smem_u32(vring), 16384, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc),
+                     v_lo = static_cast<uint32_t>(v_desc);
+      const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32), k_hi = static_cast<uint32_t>(k_desc >> 32),
+                     v_hi = static_cast<uint32_t>(v_desc >> 32);
+      const uint32_t leader = ptx::elect_one();
       bool ok = true;
       uint32_t u = 0;            // K/V blocks
-      uint32_t items = 0;
-      uint32_t g[2] = {0u, 0u};  // blocks of each tile
+      uint32_t uq = 0;           // Q slots
+      uint32_t g[2] = {0u, 0u};  // value MMAs of each S slot
       auto wait = [&](int i, uint32_t parity) {
-        if (ok) ok = ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns);
-        return ok;
-      };
-      // The tiles of K block u2, each waited for; S slot `slot` of tile t
-      auto qk = [&](int t, uint32_t u2, uint32_t slot, bool wait_k) {
-#pragma unroll
-        for (int hf = 0; hf < TPB; ++hf) {
-          const uint32_t n = u2 * TPB + hf, stage = n % NSK;
-          if (wait_k && !wait(K_FULL + static_cast<int>(stage), n / NSK)) return;
-          ptx::tc_fence_after();
-          const uint64_t qd = q_desc + static_cast<uint64_t>((t * Cfg::kQTileBytes) >> 4);
-          const uint64_t kd = k_desc + static_cast<uint64_t>((stage * Cfg::kStageBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < Cfg::kTileDim / 16; ++kk) {
-            const int k = hf * (Cfg::kTileDim / 16) + kk;
-            ptx::mma_f16_ss(tmem_base + slot * kBlockN, qd + static_cast<uint32_t>((k >> 2) * 1024 + (k & 3) * 2),
-                            kd + static_cast<uint32_t>((kk >> 2) * 1024 + (kk & 3) * 2), idesc_qk, k > 0 ? 1u : 0u);
-          }
-        }
-        ptx::mma_commit(BAR(S_FULL + static_cast<int>(slot)));
-      };
-      auto pv = [&](int t, uint32_t u2, uint32_t slot, bool first, bool wait_v) {
-#pragma unroll
-        for (int hf = 0; hf < TPB; ++hf) {
-          const uint32_t n = u2 * TPB + hf, stage = n % NSV;
-          if (wait_v && !wait(V_FULL + static_cast<int>(stage), n / NSV)) return;
-          ptx::tc_fence_after();
-          const uint64_t vd = v_desc + static_cast<uint64_t>((stage * Cfg::kStageBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kBlockN / 16; ++kk)
-            ptx::mma_f16_ts(tmem_base + Cfg::kOCol + t * HEAD_DIM + hf * Cfg::kTileDim,
-                            tmem_base + slot * kBlockN + kk * 8, vd + static_cast<uint32_t>(kk * (2048 >> 4)),
-                            idesc_pv, (kk > 0 || !first) ? 1u : 0u);
-        }
-        ptx::mma_commit(BAR(O_FULL + static_cast<int>(slot)));
-      };
-      auto release = [&](int ring_empty, uint32_t u2, uint32_t ns) {  // the ring tiles of block u2
-#pragma unroll
-        for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit(BAR(ring_empty + static_cast<int>((u2 * TPB + hf) % ns)));
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns));
       };
       RowsItem it;
-      while (next_item(it, ok, false)) {
-        const int n = it.blk_end - it.blk_begin;
+      while (next_item(it, ok, true)) {
+        const int n = __shfl_sync(0xffffffffu, it.blk_end - it.blk_begin, 0);
         if (n <= 0) continue;
-        const int nt = tiles_of(it);
-        if (!wait(Q_FULL, items)) break;
-        if constexpr (NT == 2) {
-          // S slot t holds S and P of tile t.  The MMAs run in issue order, so
-          // QK(t, i+1) may overwrite P(t, i) once PV(t, i) is issued.
-          for (int t = 0; t < nt && ok; ++t) qk(t, u, static_cast<uint32_t>(t), t == 0);
-          if (!ok) break;
-          release(K_EMPTY, u, NSK);
-          if (n == 1) ptx::mma_commit(BAR(Q_EMPTY));
-          for (int i = 0; i < n && ok; ++i, ++u) {
-            const bool more = i + 1 < n;
-            for (int t = 0; t < nt; ++t) {
-              if (!wait(P_FULL + t, g[t])) break;
-              ++g[t];
-              pv(t, u, static_cast<uint32_t>(t), i == 0, t == 0);
-              if (more && ok) qk(t, u + 1, static_cast<uint32_t>(t), t == 0);
-              if (!ok) break;
+        const int nt = __shfl_sync(0xffffffffu, slots_of(it), 0);
+        for (int t = 0; t < nt; ++t) wait(Q_FULL + static_cast<int>((uq + t) % NT), (uq + t) / NT);
+        // The item's steps j, each a QK and a PV of one block: with two tiles
+        // of rows, tile j % 2 and block j / 2; with split keys, tile j % 2 and
+        // block j; with one tile, block j (in S slot j % 2 where two are free).
+        // S slot t holds S and P of tile t, and the MMAs run in issue order:
+        // a step's QK may overwrite the P of the step `ahead` before it once
+        // that one's PV is issued.  With one tile and two slots QK(j+1) goes
+        // first, over P(j-1), whose PV is issued already.
+        const bool two = nt == 2;
+        const int steps = two ? 2 * n : n;
+        const int ahead = NT == 1 ? 1 : (two || __shfl_sync(0xffffffffu, p.s[it.section].split_keys, 0) != 0 ? 2 : 1);
+        auto slot_of = [&](int j) -> uint32_t {
+          return NT == 1 ? (u + static_cast<uint32_t>(j)) & 1u : (ahead == 2 ? static_cast<uint32_t>(j) & 1u : 0u);
+        };
+        auto block_of = [&](int j) -> uint32_t { return u + static_cast<uint32_t>(two ? j >> 1 : j); };
+        auto qk = [&](int j) {
+          const uint32_t slot = slot_of(j), blk = block_of(j), qs = (uq + (two ? slot : 0u)) % NT;
+#pragma unroll
+          for (int hf = 0; hf < TPB; ++hf) {
+            const uint32_t m = blk * TPB + hf, stage = m % NSK;
+            if (!two || slot == 0u) wait(K_FULL + static_cast<int>(stage), m / NSK);
+            if (!ok) return;
+            ptx::tc_fence_after();
+            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4), kd = k_lo + ((stage * Cfg::kStageBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < Cfg::kTileDim / 16; ++kk) {
+              const int k = hf * (Cfg::kTileDim / 16) + kk;
+              ptx::mma_f16_ss_elect(leader, tmem_base + slot * kBlockN, qd + (k >> 2) * 1024 + (k & 3) * 2, q_hi,
+                                    kd + (kk >> 2) * 1024 + (kk & 3) * 2, k_hi, idesc_qk, k > 0 ? 1u : 0u);
             }
-            if (!ok) break;
-            release(V_EMPTY, u, NSV);
-            if (more) release(K_EMPTY, u + 1, NSK);
-            if (i + 2 == n) ptx::mma_commit(BAR(Q_EMPTY));
           }
-        } else {
-          // S slot g % 2 holds S and P of block g; QK(i+1) is issued before
-          // PV(i), over P(i-1), whose PV is issued already.
-          qk(0, u, u & 1u, true);
-          if (!ok) break;
-          release(K_EMPTY, u, NSK);
-          if (n == 1) ptx::mma_commit(BAR(Q_EMPTY));
-          for (int i = 0; i < n && ok; ++i, ++u) {
-            if (i + 1 < n) {
-              qk(0, u + 1, (u + 1) & 1u, true);
-              if (!ok) break;
-              release(K_EMPTY, u + 1, NSK);
-              if (i + 2 == n) ptx::mma_commit(BAR(Q_EMPTY));
-            }
-            if (!wait(P_FULL + static_cast<int>(u & 1u), u >> 1)) break;
-            pv(0, u, u & 1u, i == 0, true);
-            if (!ok) break;
-            release(V_EMPTY, u, NSV);
+          ptx::mma_commit_elect(leader, BAR(S_FULL + static_cast<int>(slot)));
+          if (!two || slot == 1u) {  // the block's last use
+#pragma unroll
+            for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>((blk * TPB + hf) % NSK)));
+          }
+          if (j + 1 == steps)
+            for (int t = 0; t < nt; ++t) ptx::mma_commit_elect(leader, BAR(Q_EMPTY + static_cast<int>((uq + t) % NT)));
+        };
+        auto pv = [&](int j) {
+          const uint32_t slot = slot_of(j), blk = block_of(j);
+          const uint32_t o_tmem = tmem_base + Cfg::kOCol + (NT == 1 ? 0u : slot * HEAD_DIM);
+          wait(P_FULL + static_cast<int>(slot), g[slot]);
+          ++g[slot];
+          const bool first = j < (NT == 1 ? 1 : ahead);
+#pragma unroll
+          for (int hf = 0; hf < TPB; ++hf) {
+            const uint32_t m = blk * TPB + hf, stage = m % NSV;
+            if (!two || slot == 0u) wait(V_FULL + static_cast<int>(stage), m / NSV);
+            if (!ok) return;
+            ptx::tc_fence_after();
+            const uint32_t vd = v_lo + ((stage * Cfg::kStageBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kBlockN / 16; ++kk)
+              ptx::mma_f16_ts_elect(leader, o_tmem + hf * Cfg::kTileDim, tmem_base + slot * kBlockN + kk * 8,
+                                    vd + kk * (2048 >> 4), v_hi, idesc_pv, (kk > 0 || !first) ? 1u : 0u);
+          }
+          ptx::mma_commit_elect(leader, BAR(O_FULL + static_cast<int>(slot)));
+          if (!two || slot == 1u) {
+#pragma unroll
+            for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit_elect(leader, BAR(V_EMPTY + static_cast<int>((blk * TPB + hf) % NSV)));
+          }
+        };
+#pragma unroll 1
+        for (int j = -ahead; j < steps && ok; ++j) {
+          if constexpr (NT == 1) {
+            if (j + 1 < steps) qk(j + 1);
+            if (j >= 0 && ok) pv(j);
+          } else {
+            if (j >= 0) pv(j);
+            if (ok && j + ahead < steps) qk(j + ahead);
           }
         }
-        ++items;
+        u += static_cast<uint32_t>(n);
+        uq += static_cast<uint32_t>(nt);
       }
-      if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
+      if (!ok && lane == 0) detail::set_error(p.err_word, kErrTimeout, abort_flag);
       // every MMA has completed before TMEM is released
-      ptx::mma_commit(BAR(DRAIN));
+      ptx::mma_commit_elect(leader, BAR(DRAIN));
       ptx::mbar_wait_bounded(BAR(DRAIN), 0, nullptr, p.timeout_ns);
     }
     __syncwarp();
   } else if (warp == kPlanWarp) {
     // ========================================================== plan walker
-    WorkIter iter;
-    iter.init_warp(plan, p.lens, s_len, s_pre, blockIdx.x, lane);
+    if (p.plan.dealt == 0) {
+      // exclusive prefix sums of the entries' units
+      long long run = 0;
+      for (int base = 0; base < n_entries; base += 32) {
+        const int i = base + lane;
+        long long units = 0;
+        if (i < n_entries) {
+          const RowsPlanSection& s = p.plan.s[i < n0 ? 0 : 1];
+          units = static_cast<long long>(s.heads) * rows_units(s, s_len[i]);
+        }
+        long long incl = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (i < n_entries) s_pre[i] = run + incl - units;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) s_pre[n_entries] = run;
+      __syncwarp();
+    }
     if (lane == 0) {
       bool ok = true;
       int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
+      int longest = 0;              // blocks of the longest item so far
+      RowsPlanIter iter;
+      iter.init(p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
       for (uint32_t n = 0; ok; ++n) {
-        WorkItem w;
+        RowsWork w;
         const bool more = iter.next(w);
         RowsItem it;
         it.blk_begin = -1;
         it.blk_end = -1;
         if (more) {
-          const int triple = w.b * plan.kv_heads + w.h;
-          const bool partial = p.all_partial != 0 || w.slot >= 0;
+          const RowsSection& s = p.s[w.section];
+          const int triple = w.b * p.plan.s[w.section].heads + w.hh;
+          const bool partial = p.every_piece != 0 || w.n_pieces > 1;
           const int n_pieces = w.blk_begin < w.blk_end ? w.n_pieces : 0;
+          it.section = w.section;
           it.b = w.b;
-          it.h = w.h / p.groups;
-          it.tok0 = (w.h - it.h * p.groups) * (NT * p.tokens);
+          it.h = w.hh / s.groups;
+          it.tok0 = (w.hh - it.h * s.groups) * (NT * s.tokens);
           it.blk_begin = w.blk_begin;
           it.blk_end = w.blk_end;
           it.L = w.L;
-          it.piece = !partial            ? -1
-                     : p.all_partial != 0 ? triple + static_cast<int>(blockIdx.x)
-                                          : 2 * static_cast<int>(blockIdx.x) + (w.first_piece ? 1 : 0);
+          it.piece = partial ? rows_piece(p.every_piece != 0, p.plan.dealt != 0, triple, static_cast<int>(blockIdx.x),
+                                          w.first_piece != 0)
+                             : -1;
           if (w.first_piece && partial) {
-            if (p.all_partial == 0)
+            if (p.every_piece == 0)
               cut = make_int2(triple, n_pieces);
-            else if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + triple, sizeof(int2)))
-              p.rec[triple] = make_int2(it.piece, n_pieces);
+            else if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + s.rec + triple, sizeof(int2)))
+              p.rec[s.rec + triple] = make_int2(it.piece, n_pieces);
           }
         }
         const int i = static_cast<int>(n % kItemRing);
+        // as long as the items in the ring may take
         if (n >= kItemRing)
-          ok = ptx::mbar_wait_bounded(BAR(ITEM_EMPTY + i), ((n / kItemRing) & 1u) ^ 1u, abort_flag, p.timeout_ns,
+          ok = ptx::mbar_wait_bounded(BAR(ITEM_EMPTY + i), ((n / kItemRing) & 1u) ^ 1u, abort_flag,
+                                      p.timeout_ns + static_cast<uint64_t>(longest) * kItemRing * kBlockNs,
                                       kPlanSuspendNs);
+        if (it.blk_end - it.blk_begin > longest) longest = it.blk_end - it.blk_begin;
         if (!ok) break;
         items_ring[i] = it;
         ptx::mbar_arrive(BAR(ITEM_FULL + i));
@@ -473,7 +504,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       }
       if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
       // after a timeout too, so that the merge never reads what an earlier call left
-      if (p.all_partial == 0 && p.rec != nullptr &&
+      if (p.every_piece == 0 && p.rec != nullptr &&
           detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + blockIdx.x, sizeof(int2)))
         p.rec[blockIdx.x] = cut;
     }
@@ -488,6 +519,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     const uint32_t o_addr = tmem_base + lanes + Cfg::kOCol + static_cast<uint32_t>(t * HEAD_DIM);
     const uint64_t scale2 = ptx::pack_f32x2(p.scale_log2, p.scale_log2);
     uint32_t g = 0;  // blocks of this tile
+    uint32_t u = 0;  // K/V blocks of the items before
     bool ok = true;
     auto pack16 = [](float lo, float hi) -> uint32_t {
       if constexpr (IN_F16) {
@@ -509,37 +541,42 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
 
     RowsItem it;
     while (next_item(it, ok, true)) {
-      if (t >= tiles_of(it)) continue;
+      const int n_blk = it.blk_end - it.blk_begin;
+      const uint32_t u0 = u;
+      u += static_cast<uint32_t>(n_blk);
+      const bool split_keys = NT == 2 && p.s[it.section].split_keys != 0;
+      if (!split_keys && t >= slots_of(it)) continue;
+      const int rows = p.s[it.section].tokens * p.G;   // of a tile
+      const bool active = (warp & 3) * 32 < rows;      // this warp holds any of them
+      // the last key this row sees is L - 1, or (causal) L - nq + its token
+      const int causal_cut = p.s[it.section].causal != 0 ? p.s[it.section].nq - 1 : 0;
+      const int sees = it.L - causal_cut + (causal_cut != 0 ? it.tok0 + r / p.G : 0);
+      const int step = split_keys ? 2 : 1, i0 = split_keys ? t : 0;
+
       float nm = kNoMax, l = 0.f;  // -max (log2 units; kNoMax while it is -inf) and the sum of this row
-      for (int blk = it.blk_begin; blk < it.blk_end; ++blk, ++g) {
+      for (int i = i0; i < n_blk; i += step, ++g) {
+        const int blk = it.blk_begin + i;
         const uint32_t slot = NT == 2 ? static_cast<uint32_t>(t) : (g & 1u);
         const uint32_t s_addr = tmem_base + lanes + slot * kBlockN;
-        const bool first = blk == it.blk_begin;
+        const bool first = i == i0;
         if (!wait(S_FULL + static_cast<int>(slot), NT == 2 ? g : g >> 1)) break;
-        ptx::tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, x + 32 * c);
-        ptx::tmem_wait_ld();
-
         const int tail = it.L - blk * kBlockN;  // keys of this block
         if (tail < kBlockN) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j) x[j] = j < tail ? x[j] : 0xff800000u;  // -inf
           // V rows past the end hold whatever the buffer holds there; zero
           // them (up to the capacity, past which TMA wrote zeros) so that
-          // 0 * garbage cannot reach O.  The first tile's warps do it, before
-          // their P lets the issuer start on this V.  The parity wait is
-          // sound: S(g) complete means that PV(g-1) is issued and V(g-1) has
-          // landed (one tile: PV(g-1) is waited for).
-          const int cap = plan.max_seqlen - blk * kBlockN;
-          if (t == 0 && cap > tail) {
+          // 0 * garbage cannot reach O.  One tile's warps do it, before their
+          // P lets the issuer start on this V.  The parity wait is sound: a
+          // complete S says that every PV issued before it has landed, among
+          // them the one that read the stage's V before (one tile: that is
+          // PV(g-1), issued after this S, and waited for).
+          const int cap = p.plan.s[it.section].max_len - blk * kBlockN;
+          if ((t == 0 || split_keys) && cap > tail) {
             if constexpr (NT == 1) {
               if (g >= 1 && !wait_pv(g - 1)) break;
             }
 #pragma unroll
             for (int hf = 0; hf < TPB; ++hf) {
-              const uint32_t n = g * TPB + hf, stage = n % NSV;
+              const uint32_t n = (u0 + static_cast<uint32_t>(i)) * TPB + hf, stage = n % NSV;
               if (!wait(V_FULL + static_cast<int>(stage), n / NSV)) break;
               if (r >= tail && r < cap) {
 #pragma unroll
@@ -554,10 +591,32 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             ptx::fence_proxy_async_smem();
           }
         }
+        if (!active) {  // no row of this warp is read: whatever its lanes hold may stand for P
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + static_cast<int>(slot)));
+          continue;
+        }
+        ptx::tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, x + 32 * c);
+        ptx::tmem_wait_ld();
+
+        if ((blk + 1) * kBlockN > it.L - causal_cut) {
+          const int seen = sees - blk * kBlockN < tail ? sees - blk * kBlockN : tail;
+#pragma unroll
+          for (int j = 0; j < 128; ++j) x[j] = j < seen ? x[j] : 0xff800000u;  // -inf
+        }
 
         float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3])};
 #pragma unroll
-        for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+        for (int j = 4; j < 124; j += 8) {
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2)
+            mx[i2] = ptx::max3(mx[i2], __uint_as_float(x[j + 2 * i2]), __uint_as_float(x[j + 2 * i2 + 1]));
+        }
+        mx[0] = ptx::max3(mx[0], __uint_as_float(x[124]), __uint_as_float(x[125]));
+        mx[1] = ptx::max3(mx[1], __uint_as_float(x[126]), __uint_as_float(x[127]));
         const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;  // the scale is positive
         if (first) {
           nm = m_blk == -INFINITY ? kNoMax : -m_blk;
@@ -593,12 +652,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             float a, b;
             ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale2,
                                              nm2), a, b);
-            a = ptx::ex2_approx(a);
-            b = ptx::ex2_approx(b);
-            x[k] = __float_as_uint(a);
-            x[k + 1] = __float_as_uint(b);
-            w[j] = pack16(a, b);
+            x[k] = __float_as_uint(ptx::ex2_in_order(a));
+            x[k + 1] = __float_as_uint(ptx::ex2_in_order(b));
           }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = pack16(__uint_as_float(x[32 * c + 2 * j]), __uint_as_float(x[32 * c + 2 * j + 1]));
           ptx::tmem_st_32x32b_x16u(s_addr + 16 * c, w);
         }
         ptx::tmem_wait_st();
@@ -618,24 +677,27 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       if (!ok) break;
 
       // ------------------------------------------------------------ epilogue
-      const bool empty = it.blk_begin >= it.blk_end, partial = it.piece >= 0;
-      if (empty && partial) continue;  // 0 pieces: the merge reads nothing of this triple
+      const bool partial = it.piece >= 0;
+      if (n_blk == 0 && partial) continue;  // 0 pieces: the merge reads nothing of this triple
+      const bool empty = i0 >= n_blk;       // this tile had no key
+      if (!active) continue;
       if (!empty) {
         if (!wait_pv(g - 1)) break;
         ptx::tc_fence_after();
       }
-      const int r_tok = r / p.G, tok = it.tok0 + t * p.tokens + r_tok;
-      const bool row_valid = r_tok < p.tokens && tok < p.nq;
-      const long long row = (static_cast<long long>(it.b) * p.nq + tok) * p.Hq + it.h * p.G + (r - r_tok * p.G);
+      const RowsSection& sec = p.s[it.section];
+      const int r_tok = r / p.G, tok = it.tok0 + (split_keys ? 0 : t * sec.tokens) + r_tok;
+      const bool row_valid = r_tok < sec.tokens && tok < sec.nq;
+      const long long row = (static_cast<long long>(it.b) * sec.nq + tok) * p.Hq + it.h * p.G + (r - r_tok * p.G);
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // a row that saw only -inf scores: 0; NaN stays NaN
       const float lse = l > 0.f || l != l ? 0.69314718055994531f * (__log2f(l) - nm) : -INFINITY;
-      const long long prow = (static_cast<long long>(it.piece) * NT + t) * kTileRows + r;
+      const long long prow = sec.part_row + (static_cast<long long>(it.piece) * NT + t) * rows + r;
       const bool out16 = !partial && p.out_dtype != kOutF32;
       uint8_t* dst;
       bool store;
       if (partial) {
         dst = reinterpret_cast<uint8_t*>(p.o_part + prow * HEAD_DIM);
-        store = row_valid && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
+        store = row_valid && !empty && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
         if (row_valid && detail::write_ok(p.err_word, p.lse_part, p.lse_part_bytes, p.lse_part + prow, 4ull))
           p.lse_part[prow] = lse;
       } else {

@@ -6,7 +6,9 @@
 //
 // over normalised fp32 partials, pieces with lse_s = -inf skipped (their rows
 // are never read), in a fixed order: the result is bit-identical from run to
-// run.  One warp per row; a lane owns HEAD_DIM / 32 consecutive elements.
+// run.  A lane owns HEAD_DIM / 32 consecutive elements of a row; a row
+// is one warp's, or (WARPS = 4, launches of few rows) its pieces are dealt to
+// four warps and their sums joined through shared memory.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -17,92 +19,69 @@
 
 namespace gqa {
 
-constexpr int kMergeThreads = 128;  // four rows
+constexpr int kMergeThreads = 128;
 
-// Partials [slots][rows][d] as the decode kernel leaves them: n_pieces (one
-// 16-byte record per (batch, KV head) pair, or null) says how many slots hold
-// pieces of the pair's rows, else all of them do.
-struct DecodePartials {
-  const float* o;
-  const float* lse;
-  const int32_t* n_pieces;
-  int slots;
+struct RowsMergeSection {
+  long long part_row;  // as in RowsSection
+  long long rec;
+  int nq, tokens, groups, split_keys;
+  int pieces;          // pieces its part of o_part holds: records that name others are ignored
 };
 
 struct RowsMergeParams {
-  // the rows kernel's partials and records
   const float* o_part;
   const float* lse_part;
   const int2* rec;
-  int pieces;               // partial tiles o_part holds: records that name others are ignored
-  int tiles, tokens;        // row tiles per triple, tokens per tile
-  int groups, kv_heads;     // tile groups; KV heads
+  int n_sections;
+  RowsMergeSection s[2];
   void* out;
   float* lse;
   int out_dtype;
-  int batch, nq, Hq, G;
-  // the shared prefix only
-  int prefix_in_rows;       // the prefix's partials are the rows kernel's (else `prefix`)
-  DecodePartials prefix, own;
+  int batch, nq, Hq, G, kv_heads;
+  int tiles;           // row tiles of a triple
 };
 
 namespace detail {
 
-// A run of partial rows: row `first`, then n - 1 more from `next` in steps of `stride`.
+// n partial rows: `first`, then from `next` on in steps of `stride`.
 struct PieceRun {
-  const float* o;
-  const float* lse;
   long long first, next, stride;
   int n;
   __device__ __forceinline__ long long at(int j) const { return j == 0 ? first : next + (j - 1) * stride; }
 };
 
-__device__ __forceinline__ PieceRun decode_run(const DecodePartials& d, long long rows, long long row, long long pair) {
-  PieceRun r;
-  r.o = d.o;
-  r.lse = d.lse;
-  r.first = row;
-  r.next = row + rows;
-  r.stride = rows;
-  r.n = d.slots;
-  if (d.n_pieces != nullptr) {
-    const int n = d.n_pieces[pair * 4];
-    r.n = n < d.slots ? n : d.slots;
-  }
-  return r;
+__device__ __forceinline__ float max_or_nan(float a, float b) {  // a NaN piece makes the row NaN
+  return a != a || b != b ? NAN : fmaxf(a, b);
 }
 
-template <int HEAD_DIM, int RUNS>
-__device__ __forceinline__ void merge_row(const PieceRun (&runs)[RUNS], void* out, float* lse, int out_dtype,
+// Merges runs[0 .. n_runs) into row `row`.  With WARPS > 1 the CTA's warps
+// share the row, and every thread of the CTA must call it.
+template <int HEAD_DIM, int WARPS>
+__device__ __forceinline__ void merge_row(const float* __restrict__ o_part, const float* __restrict__ lse_part,
+                                          const PieceRun (&runs)[2], int n_runs, void* out, float* lse, int out_dtype,
                                           long long row) {
   constexpr int VEC = HEAD_DIM / 32;
+  constexpr int kBatch = 32 / VEC;  // partial rows in flight
   constexpr float kLog2e = 1.4426950408889634f;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = WARPS > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
   float M = -INFINITY;
+  for (int i = 0; i < n_runs; ++i)
+    for (int j = lane; j < runs[i].n; j += 32) M = max_or_nan(M, lse_part[runs[i].at(j)]);
 #pragma unroll
-  for (int i = 0; i < RUNS; ++i)
-    for (int j = lane; j < runs[i].n; j += 32) {
-      const float v = runs[i].lse[runs[i].at(j)];
-      M = v != v || M != M ? NAN : fmaxf(M, v);  // a NaN piece makes the row NaN, not disappear
-    }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const float v = __shfl_xor_sync(0xffffffffu, M, o);
-    M = v != v || M != M ? NAN : fmaxf(M, v);
-  }
+  for (int o = 16; o >= 1; o >>= 1) M = max_or_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-  float W = 0.f;
+  float W = 0.f;  // the weights of this lane's pieces
   if (M != -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < RUNS; ++i) {
-      for (int j0 = 0; j0 < runs[i].n; j0 += 32) {
-        const float l = j0 + lane < runs[i].n ? runs[i].lse[runs[i].at(j0 + lane)] : -INFINITY;
+    for (int i = 0; i < n_runs; ++i) {
+      // this warp's pieces: warp, warp + WARPS, ...; 32 of them at a time
+      for (int j0 = warp; j0 < runs[i].n; j0 += 32 * WARPS) {
+        const int mine = j0 + lane * WARPS;
+        const float l = mine < runs[i].n ? lse_part[runs[i].at(mine)] : -INFINITY;
         const float w = l == -INFINITY ? 0.f : ptx::ex2_approx((l - M) * kLog2e);
         W += w;
-        const int cnt = runs[i].n - j0 < 32 ? runs[i].n - j0 : 32;
-        constexpr int kBatch = VEC <= 4 ? 4 : 2;  // partial rows in flight
+        const int left = (runs[i].n - j0 + WARPS - 1) / WARPS, cnt = left < 32 ? left : 32;
         for (int j = 0; j < cnt; j += kBatch) {
           float v[kBatch][VEC], wb[kBatch];
 #pragma unroll
@@ -110,7 +89,7 @@ __device__ __forceinline__ void merge_row(const PieceRun (&runs)[RUNS], void* ou
             const float ws = __shfl_sync(0xffffffffu, w, (j + q) & 31);
             wb[q] = j + q < cnt ? ws : 0.f;
             if (wb[q] != 0.f) {
-              load_vec<VEC>(runs[i].o + runs[i].at(j0 + j + q) * HEAD_DIM + lane * VEC, v[q]);
+              load_vec<VEC>(o_part + runs[i].at(j0 + (j + q) * WARPS) * HEAD_DIM + lane * VEC, v[q]);
             } else {
 #pragma unroll
               for (int e = 0; e < VEC; ++e) v[q][e] = 0.f;
@@ -127,6 +106,26 @@ __device__ __forceinline__ void merge_row(const PieceRun (&runs)[RUNS], void* ou
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+  }
+  if constexpr (WARPS > 1) {
+    __shared__ float s_acc[WARPS][HEAD_DIM];
+    __shared__ float s_w[WARPS];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s_acc[warp][lane * VEC + i] = acc[i];
+    if (lane == 0) s_w[warp] = W;
+    __syncthreads();
+    if (warp != 0) return;
+    W = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      W += s_w[k];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += s_acc[k][lane * VEC + i];
+    }
+  }
+  if (M != -INFINITY) {
     const float inv = 1.0f / W;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] *= inv;
@@ -163,64 +162,65 @@ __device__ __forceinline__ void merge_row(const PieceRun (&runs)[RUNS], void* ou
 
 }  // namespace detail
 
-// The cut triples of a rows-kernel launch: blockIdx.x is the CTA of that
+// The cut triples of a launch of one section: blockIdx.x is the CTA of that
 // launch in which a cut triple may begin, blockIdx.y a group of its rows.
 template <int HEAD_DIM>
 __global__ void __launch_bounds__(kMergeThreads)
 gqa_rows_merge_kernel(const RowsMergeParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  const RowsMergeSection& s = p.s[0];
   const int2 rec = p.rec[blockIdx.x];
-  if (rec.x < 0 || rec.y <= 0 || 2 * (static_cast<int>(blockIdx.x) + rec.y) > p.pieces) return;
-  const int r = static_cast<int>(blockIdx.y) * (kMergeThreads / 32) + (threadIdx.x >> 5);  // row of the triple's tiles
-  const int t = r / kTileRows, rt = r - t * kTileRows;
-  const int per_batch = p.kv_heads * p.groups;
+  if (rec.x < 0 || rec.y <= 0 || 2 * (static_cast<int>(blockIdx.x) + rec.y) > s.pieces) return;
+  const int rows = s.tokens * p.G;  // of a tile
+  const int i = static_cast<int>(blockIdx.y) * (kMergeThreads / 32) + (threadIdx.x >> 5);  // row of the triple's tiles
+  const int t = i / rows, r = i - t * rows;
+  const int per_batch = p.kv_heads * s.groups;
   const int b = rec.x / per_batch, hg = rec.x - b * per_batch;
-  const int h = hg / p.groups, grp = hg - h * p.groups;
-  const int tok = (grp * p.tiles + t) * p.tokens + rt / p.G;
-  if (t >= p.tiles || rt >= p.tokens * p.G || tok >= p.nq) return;
-  const long long tile_rows = static_cast<long long>(p.tiles) * kTileRows;
-  detail::PieceRun run[1];
-  run[0].o = p.o_part;
-  run[0].lse = p.lse_part;
-  run[0].first = (2ll * blockIdx.x + 1) * tile_rows + r;
-  run[0].next = 2ll * (blockIdx.x + 1) * tile_rows + r;
-  run[0].stride = 2ll * tile_rows;
+  const int h = hg / s.groups, grp = hg - h * s.groups;
+  const int tok = (grp * p.tiles + t) * s.tokens + r / p.G;
+  if (t >= p.tiles || tok >= s.nq) return;
+  const long long piece_rows = static_cast<long long>(p.tiles) * rows;
+  detail::PieceRun run[2];
+  run[0].first = (2ll * blockIdx.x + 1) * piece_rows + i;
+  run[0].next = 2ll * (blockIdx.x + 1) * piece_rows + i;
+  run[0].stride = 2ll * piece_rows;
   run[0].n = rec.y;
-  const long long row = (static_cast<long long>(b) * p.nq + tok) * p.Hq + h * p.G + rt % p.G;
-  detail::merge_row<HEAD_DIM>(run, p.out, p.lse, p.out_dtype, row);
+  const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + r % p.G;
+  detail::merge_row<HEAD_DIM, 1>(p.o_part, p.lse_part, run, 1, p.out, p.lse, p.out_dtype, row);
 }
 
-// Every row of a batch: the shared prefix's pieces, then its own keys'.
-template <int HEAD_DIM>
+// Every row of a batch, from the pieces of one or two sections: its own keys
+// (the last section), and before them the prefix, whose one entry holds all
+// the batch's tokens.
+template <int HEAD_DIM, int WARPS>
 __global__ void __launch_bounds__(kMergeThreads)
-gqa_prefix_merge_kernel(const RowsMergeParams p) {
+gqa_pieces_merge_kernel(const RowsMergeParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long rows = static_cast<long long>(p.batch) * p.nq * p.Hq;
-  const long long row = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const long long row = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32 / WARPS) +
+                        (WARPS > 1 ? 0 : static_cast<int>(threadIdx.x >> 5));
   if (row >= rows) return;
-  const long long tok = row / p.Hq;  // b * nq + t: the token among the prefix's rows
-  const int hq = static_cast<int>(row - tok * p.Hq), h = hq / p.G;
+  const long long bt = row / p.Hq;  // b * nq + t
+  const int hq = static_cast<int>(row - bt * p.Hq), h = hq / p.G;
   detail::PieceRun run[2];
-  if (p.prefix_in_rows != 0) {
-    const long long per_triple = static_cast<long long>(p.tiles) * p.tokens;
-    const long long grp = tok / per_triple;
-    const int in_triple = static_cast<int>(tok - grp * per_triple);
-    const int t = in_triple / p.tokens, rt = (in_triple - t * p.tokens) * p.G + (hq - h * p.G);
-    const int2 rec = p.rec[static_cast<long long>(h) * p.groups + grp];
-    const long long tile_rows = static_cast<long long>(p.tiles) * kTileRows;
-    run[0].o = p.o_part;
-    run[0].lse = p.lse_part;
-    run[0].first = rec.x * tile_rows + t * kTileRows + rt;
-    run[0].next = run[0].first + tile_rows;
-    run[0].stride = tile_rows;
-    run[0].n = rec.x >= 0 && rec.y > 0 && rec.x <= p.pieces - rec.y ? rec.y : 0;
-  } else {
-    run[0] = detail::decode_run(p.prefix, rows, row, h);
+  for (int i = 0; i < p.n_sections; ++i) {
+    const RowsMergeSection& s = p.s[i];
+    const long long b = bt / s.nq;  // the section's entry, and the token within it
+    const int tok = static_cast<int>(bt - b * s.nq);
+    const int per_group = (s.split_keys ? 1 : p.tiles) * s.tokens;
+    const int grp = tok / per_group, in_group = tok - grp * per_group;
+    const int t = in_group / s.tokens, r = (in_group - t * s.tokens) * p.G + (hq - h * p.G);
+    const int2 rec = p.rec[s.rec + (b * p.kv_heads + h) * s.groups + grp];
+    const long long tile_rows = static_cast<long long>(s.tokens) * p.G;
+    run[i].first = s.part_row + (static_cast<long long>(rec.x) * p.tiles + t) * tile_rows + r;
+    run[i].stride = s.split_keys ? tile_rows : p.tiles * tile_rows;
+    run[i].next = run[i].first + run[i].stride;
+    const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
+    run[i].n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
   }
-  run[1] = detail::decode_run(p.own, rows, row, (tok / p.nq) * p.kv_heads + h);
-  detail::merge_row<HEAD_DIM>(run, p.out, p.lse, p.out_dtype, row);
+  detail::merge_row<HEAD_DIM, WARPS>(p.o_part, p.lse_part, run, p.n_sections, p.out, p.lse, p.out_dtype, row);
 }
 
 }  // namespace gqa

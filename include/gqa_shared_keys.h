@@ -85,18 +85,24 @@ gqa_status_t gqa_prefix_attn(const gqa_desc_t* desc, const void* q, const void* 
 
 /*
  * Host-side view of the tiled kernel's work decomposition, for inspection and
- * testing (the counterpart of gqa_decode_plan).  A triple is a (batch entry,
- * KV head, tile group) with tile groups of *group_tokens query tokens;
- * every_piece: nonzero for the plan of a shared prefix (batch 1, all its rows;
- * every triple leaves partials), 0 for cross attention.  kv_lens_host: int32
- * [B] in host memory; sm_count: SMs to plan for (0: those of the current
- * device).  Fills *num_ctas, *num_pieces (partial tiles the workspace holds)
- * and, if `items` is not NULL, up to max_items records of 8 int32 each -- cta,
- * b, h, tile group, blk_begin, blk_end, piece (-1 = final output), n_pieces --
- * in the order each CTA processes them; the total count goes to *num_items.
+ * testing (the counterpart of gqa_decode_plan).  max_prefix = 0: the launch of
+ * gqa_cross_attn(desc) with more than GQA_MAX_QROWS rows per KV head, one
+ * section of batch entries; else that of gqa_prefix_attn, section 0 the prefix
+ * (one entry, prefix_len keys), section 1 the sequences' own keys.  A triple
+ * is an (entry, KV head, tile group).  kv_lens_host: int32 [B] in host memory;
+ * sm_count: SMs to plan for (0: those of the current device).  Fills
+ *   *num_ctas, *every_piece (whether every triple leaves partials),
+ *   info     per section: query tokens of a tile, tile groups, whether both
+ *            tiles hold the same rows with the keys in turn, pieces its part
+ *            of the workspace holds (8 int in all)
+ *   items    (if not NULL) up to max_items records of 9 int32 each: cta,
+ *            section, b, h, tile group, blk_begin, blk_end, piece (-1 = final
+ *            output), n_pieces, in the order each CTA processes them
+ *   *num_items  their total count
+ * sm_count and lengths as gqa_decode_plan; any output but items may be NULL.
  */
-gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int every_piece, const int32_t* kv_lens_host, int sm_count,
-                                  int* num_ctas, int* group_tokens, int* num_pieces, int32_t* items,
+gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int max_prefix, const int32_t* kv_lens_host,
+                                  int sm_count, int* num_ctas, int* every_piece, int* info, int32_t* items,
                                   int64_t max_items, int64_t* num_items);
 
 #ifdef __cplusplus

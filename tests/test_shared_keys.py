@@ -134,7 +134,7 @@ def test_header_is_plain_c_and_exported(tmp_path):
     src.write_text('#include "gqa_shared_keys.h"\nint main(void) {\n  gqa_desc_t d = {0};\n  int64_t n = 0;\n'
                    "  (void)gqa_cross_attn(&d, 0, 0, 0, 0, 0, 0, 0, gqa_cross_workspace_size(&d), 0);\n"
                    "  (void)gqa_prefix_attn(&d, 0, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, gqa_prefix_workspace_size(&d, 1), 0);\n"
-                   "  return (int)gqa_shared_keys_plan(&d, 0, 0, 1, 0, 0, 0, 0, 0, &n) == GQA_OK;\n}\n")
+                   "  return (int)gqa_shared_keys_plan(&d, 0, 0, 0, 1, 0, 0, 0, 0, 0, &n) == GQA_OK;\n}\n")
     subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror", "-I",
                     os.path.join(gbuild.ROOT, "include"), str(src), gbuild.LIB, "-o", str(tmp_path / "use")],
                    check=True)
@@ -161,24 +161,34 @@ def test_python_checks_tensors():
 
 
 # ---------------------------------------------------------------------- plan
-def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, every_piece):
+def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix=None):
+    """prefix: (length, capacity) of a shared prefix."""
+    P, room = prefix or (0, 0)
     desc = _desc(batch=len(lens), q_tokens=nq, q_heads=Hq, kv_heads=Hkv, head_dim=d, max_seqlen=s_max)
-    ctas, group_tokens, pieces, items = g.gqa_shared_keys_plan(desc, lens, every_piece, sm)
+    ctas, every, info, items = g.gqa_shared_keys_plan(desc, lens, P, room, sm)
     assert 1 <= ctas <= sm
-    G = Hq // Hkv
-    assert group_tokens == (1 if d == 256 else 2) * (128 // G)
-    groups = -(-nq // group_tokens)
+    G, tiles = Hq // Hkv, 1 if d == 256 else 2
+    sections = [([P], nq * len(lens), room), (lens, nq, s_max)] if prefix else [(lens, nq, s_max)]
+    assert every == (bool(prefix) or nq <= 128 // G)
     by_triple, used, load = {}, set(), {}
-    for cta, b, h, grp, lo, hi, piece, n in items.tolist():
+    for cta, sec, b, h, grp, lo, hi, piece, n in items.tolist():
+        tokens, groups, split, pieces = info[sec].tolist()
         assert 0 <= cta < ctas and 0 <= h < Hkv and 0 <= grp < groups
-        by_triple.setdefault((b, h, grp), []).append((lo, hi, piece, n, cta))
+        by_triple.setdefault((sec, b, h, grp), []).append((lo, hi, piece, n, cta))
         load[cta] = load.get(cta, 0) + hi - lo
-        if piece >= 0:
-            assert piece < pieces and piece not in used, "two pieces share a place"
-            used.add(piece)
-    assert len(by_triple) == len(lens) * Hkv * groups
-    for (b, h, grp), its in by_triple.items():
-        blocks = (min(max(lens[b], 0), s_max) + 127) // 128
+        if piece >= 0 and n:
+            assert piece < pieces and (sec, piece) not in used, "two pieces share a place"
+            used.add((sec, piece))
+    total = 0
+    for sec, (sec_lens, tokens_in, cap) in enumerate(sections):
+        tokens, groups, split, _ = info[sec].tolist()
+        assert tokens == min(tokens_in, 128 // G) and split == (tiles == 2 and tokens_in <= 128 // G)
+        assert groups == -(-tokens_in // (tokens * (1 if split else tiles)))
+        total += len(sec_lens) * Hkv * groups
+    assert len(by_triple) == total
+    for (sec, b, h, grp), its in by_triple.items():
+        sec_lens, _, cap = sections[sec]
+        blocks = (min(max(sec_lens[b], 0), cap) + 127) // 128
         if blocks == 0:
             assert len(its) == 1 and its[0][0] == its[0][1] and its[0][3] == 0
             continue
@@ -186,7 +196,7 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, every_piece):
         assert all(lo < hi and n == len(its) for lo, hi, _, n, _ in its)
         first, ctas_of = its[0][2], [x[4] for x in its]
         assert ctas_of == list(range(ctas_of[0], ctas_of[0] + len(its)))
-        if every_piece:    # consecutive places from the first
+        if every:          # consecutive places from the first
             assert [x[2] for x in its] == list(range(first, first + len(its)))
         elif len(its) == 1:
             assert first == -1
@@ -199,13 +209,21 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, every_piece):
 @pytest.mark.parametrize("lens,nq,Hq,Hkv,d,s_max", [
     ([4096] * 4, 2048, 32, 8, 128, 4096), ([1, 0, 129, 1000, 128], 77, 12, 12, 64, 1023), ([0, 0], 50, 8, 1, 64, 512),
     ([131072], 64, 64, 8, 128, 131072), ([5001, 4000], 333, 16, 2, 256, 5001), ([700], 33, 3, 1, 128, 700),
-    ([-5, 9999, 300], 100, 24, 8, 128, 600), ([1], 1, 128, 1, 64, 1), ([300] * 600, 40, 4, 4, 64, 300)])
+    ([-5, 9999, 300], 100, 24, 8, 128, 600), ([1], 1, 128, 1, 64, 1), ([300] * 1100, 40, 4, 4, 64, 300),
+    ([0, 0, 5, 0, 0, 700, 0], 200, 4, 2, 128, 700), ([100, 90], 129, 2, 2, 64, 128)])
 def test_plan_covers_every_block_once(lens, nq, Hq, Hkv, d, s_max, sm):
-    load = _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, False)
-    if len(lens) <= 512 and sum(load.values()) >= sm and min(lens) == max(lens):
-        assert max(load.values()) - min(load.values()) <= 2 + 1   # equal ranges, but for the item units
-    if len(lens) == 1:
-        _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, True)
+    load = _check_plan(lens, nq, Hq, Hkv, d, s_max, sm)
+    if len(lens) <= 1024 and min(lens) == max(lens) > 0 and sum(load.values()) >= 4 * sm:
+        assert max(load.values()) - min(load.values()) <= 3   # equal ranges, but for the item units
+
+
+@pytest.mark.parametrize("sm", [1, 7, 152])
+@pytest.mark.parametrize("lens,nq,Hq,Hkv,d,s_max,prefix", [
+    ([5, 700, 0, 128], 1, 8, 2, 128, 700, (1000, 1024)), ([300] * 128, 1, 64, 8, 128, 2048, (32768, 32768)),
+    ([0] * 40, 2, 8, 1, 64, 10, (0, 5)), ([40] * 40, 2, 8, 1, 64, 50, (0, 5)), ([7] * 24, 1, 16, 2, 256, 300, (20000, 20480)),
+    ([9] * 1100, 4, 32, 4, 64, 9, (130, 130)), ([0, 3], 8, 8, 2, 64, 9, (999, 500))])
+def test_plan_with_a_prefix(lens, nq, Hq, Hkv, d, s_max, prefix, sm):
+    _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix)
 
 
 # --------------------------------------------------------- the definition, fp64
@@ -302,6 +320,9 @@ CROSS = [  # B, T, H, K, d, S, lens, dtype, out dtype
     (2, 600, 8, 2, 64, 3000, [3000, 1111], BF16, FP32),
     (1, 64, 8, 1, 128, 40000, [40000], FP16, None),              # one triple over many CTAs
     (5, 40, 4, 4, 128, 260, [0, 0, 0, 0, 0], BF16, None),        # nothing to see at all
+    (5, 150, 4, 4, 64, 260, [0, 0, 0, 0, 0], BF16, None),
+    (1, 40, 2, 2, 128, 128, [77], BF16, None),                   # one block for the two tiles
+    (3, 200, 6, 2, 128, 2000, [2000, 129, 0], BF16, None),       # cut triples of both tiles, and a half-empty last
     (40, 40, 4, 1, 64, 200, [(i * 13) % 201 for i in range(40)], BF16, None),
 ]
 
@@ -386,7 +407,7 @@ def test_few_rows_are_a_decode_call(dev):
 
 @gpu
 def test_bad_lengths_are_clamped_and_flagged(dev):
-    for B, T in ((2, 50), (600, 40)):    # lengths staged, and read per item
+    for B, T in ((2, 50), (2, 200), (1100, 40)):    # lengths staged, and read per item
         lens = [200] * (B - 2) + [-3, 999]
         q, k, v, ln = _cross_case(dev, B, T, 2, 1, 64, 200, lens, seed=6)
         out, lse = _run_cross(q, k, v, ln)
@@ -397,10 +418,11 @@ def test_bad_lengths_are_clamped_and_flagged(dev):
 
 @gpu
 def test_more_entries_than_lengths_are_staged(dev):
-    lens = [(i * 29) % 321 for i in range(530)]
-    q, k, v, ln = _cross_case(dev, 530, 40, 2, 2, 64, 320, lens, seed=7)
-    out, lse = _run_cross(q, k, v, ln)
-    _compare("batch 530", out, lse, _cross_want(q, k, v, lens, BF16))
+    for T in (40, 150):
+        lens = [(i * 29) % 321 for i in range(1030)]
+        q, k, v, ln = _cross_case(dev, 1030, T, 2, 2, 64, 320, lens, seed=7)
+        out, lse = _run_cross(q, k, v, ln)
+        _compare("batch 1030", out, lse, _cross_want(q, k, v, lens, BF16))
     assert g.gqa_decode_get_error() == g.GQA_OK
 
 
@@ -459,7 +481,9 @@ PREFIX = [  # B, T, H, K, d, P, room, S, lens, dtype, out dtype, causal
     (24, 1, 16, 2, 64, 777, 800, 300, [0] * 24, BF16, None, False),             # nothing but the prefix
     (3, 1, 8, 1, 128, 0, 64, 300, [0, 5, 300], BF16, None, False),              # few rows, no prefix
     (160, 2, 24, 8, 128, 100, 100, 30, [(i * 37) % 31 for i in range(160)], BF16, None, False),
-    (600, 1, 4, 2, 64, 300, 333, 140, [(i * 7) % 141 for i in range(600)], BF16, None, False),  # lengths not staged
+    (1100, 1, 4, 2, 64, 300, 333, 140, [(i * 7) % 141 for i in range(1100)], BF16, None, False),  # lengths not staged
+    (2, 8, 16, 4, 128, 400, 400, 700, [700, 9], BF16, None, True),              # 64 rows, 32 of their own
+    (40, 8, 16, 4, 128, 400, 400, 700, [(i * 17) % 701 for i in range(40)], FP16, None, True),
     (3, 1, 128, 4, 64, 260, 260, 40, [40, 1, 0], BF16, None, False),            # G = 32
 ]
 
