@@ -22,10 +22,13 @@ namespace {
 // Units of the plan's line (rows_plan.cuh): a key block against two tiles of
 // rows, against one, and a triple's fixed cost -- Q load, pipeline fill,
 // epilogue.
-// Up to this many rows, a merge gives each a CTA.
-constexpr size_t kMergeSharedRows = 4096;
+// CTAs of a merge: a few per SM; and up to this many rows, a CTA takes a row
+// at a time, its warps sharing the pieces.
+constexpr int kMergeCtasPerSm = 4;
+constexpr size_t kMergeSharedRows = 1024;
 
-constexpr int kTwoTileUnits = 2, kOneTileUnits = 2, kItemUnits = 2;
+constexpr int kTwoTileShift = 2, kOneTileShift = 1, kItemUnits = 4;
+constexpr int kLeastUnits = 8;  // of a CTA: below that, starting one costs more than it saves
 
 int group_of(const gqa_desc_t* d) { return d->q_heads / d->kv_heads; }
 int tiles_of(int head_dim) { return head_dim == 256 ? 1 : 2; }
@@ -83,20 +86,19 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     ps.batch = d.batch;
     ps.heads = static_cast<int>(heads);
     ps.max_len = d.max_seqlen;
-    ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits : kTwoTileUnits;
+    ps.block_shift = s.split_keys || tiles == 1 ? kOneTileShift : kTwoTileShift;
     ps.item_units = kItemUnits;
     entries += d.batch;
     units += static_cast<long long>(s.triples) * rows_units(ps, d.max_seqlen);
-    if (units > 1ll << 48) return r;  // (u + 1) * CTAs stays within 64 bits
   }
-  r.plan.dealt = entries > kMaxRowsEntries ? 1 : 0;
+  r.plan.dealt = entries > kMaxRowsEntries || units > INT_MAX ? 1 : 0;
   long long ctas = sm;
   if (r.plan.dealt) {
     const long long triples = static_cast<long long>(r.s[0].triples) + r.s[1].triples;
     if (triples < ctas) ctas = triples;
   } else {
-    const long long blocks = units / (kTwoTileUnits > kOneTileUnits ? kTwoTileUnits : kOneTileUnits);
-    if (blocks < ctas) ctas = blocks < 1 ? 1 : blocks;
+    const long long most = units / kLeastUnits;
+    if (most < ctas) ctas = most < 1 ? 1 : most;
   }
   r.plan.num_ctas = static_cast<int>(ctas);
   for (int i = 0; i < r.n; ++i) {
@@ -246,25 +248,23 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
   m.G = G;
   m.kv_heads = r.kv_heads;
   m.tiles = tiles_of(hd);
-  constexpr int kWarps = kMergeThreads / 32;
+  const size_t ctas = static_cast<size_t>(st->sm_count) * kMergeCtasPerSm;
   if (!r.every_piece) {
     const void* fn = hd == 64    ? reinterpret_cast<const void*>(&gqa_rows_merge_kernel<64>)
                      : hd == 256 ? reinterpret_cast<const void*>(&gqa_rows_merge_kernel<256>)
                                  : reinterpret_cast<const void*>(&gqa_rows_merge_kernel<128>);
-    const int per_triple = m.tiles * m.s[0].tokens * G;
-    return launch_kernel(fn, dim3(static_cast<unsigned>(r.plan.num_ctas), (per_triple + kWarps - 1) / kWarps),
-                         kMergeThreads, 0, &m, stream);
+    return launch_kernel(fn, dim3(static_cast<unsigned>(r.plan.num_ctas), kMergeCtasPerSm), kMergeThreads, 0, &m,
+                         stream);
   }
-  // few rows: a CTA for each, so that its pieces are read by four warps at once
   const bool share = rows <= kMergeSharedRows;
-  const void* fn = hd == 64    ? (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<64, kWarps>)
+  const void* fn = hd == 64    ? (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<64, kMergeWarps>)
                                         : reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<64, 1>))
-                   : hd == 256 ? (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<256, kWarps>)
+                   : hd == 256 ? (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<256, kMergeWarps>)
                                         : reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<256, 1>))
-                               : (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<128, kWarps>)
+                               : (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<128, kMergeWarps>)
                                         : reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<128, 1>));
-  const size_t grid = share ? rows : (rows + kWarps - 1) / kWarps;
-  return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), kMergeThreads, 0, &m, stream);
+  const size_t want = share ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
+  return launch_kernel(fn, dim3(static_cast<unsigned>(want < ctas ? want : ctas)), kMergeThreads, 0, &m, stream);
 }
 
 gqa_status_t check_cross(const gqa_desc_t* d) {
@@ -396,26 +396,26 @@ gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int ma
   }
   const int32_t* raw[2] = {with_prefix ? &prefix_len : kv_lens_host, with_prefix ? kv_lens_host : nullptr};
   std::vector<int32_t> lens;
-  std::vector<long long> pre(1, 0);
+  std::vector<uint32_t> pre(1, 0);
   for (int i = 0; i < r.n; ++i)
     for (int b = 0; b < r.d[i].batch; ++b) {
       const RowsPlanSection& s = r.plan.s[i];
       lens.push_back(clamp_len(raw[i][b], s.max_len));
-      pre.push_back(pre.back() + static_cast<long long>(s.heads) * rows_units(s, lens.back()));
+      pre.push_back(pre.back() + static_cast<uint32_t>(s.heads) * static_cast<uint32_t>(rows_units(s, lens.back())));
     }
   int64_t n = 0;
   for (int c = 0; c < r.plan.num_ctas; ++c) {
     RowsPlanIter it;
-    it.init(r.plan, raw[0], raw[1], lens.data(), pre.data(), c);
+    it.init(&r.plan, raw[0], raw[1], lens.data(), pre.data(), c);
     RowsWork w;
     while (it.next(w)) {
       if (items != nullptr && n < max_items) {
         int32_t* o = items + 9 * n;
         const int groups = r.s[w.section].groups, triple = w.b * r.plan.s[w.section].heads + w.hh;
-        const bool partial = r.every_piece || w.n_pieces > 1;
+        const bool partial = r.every_piece || w.whole == 0;
         o[0] = c; o[1] = w.section; o[2] = w.b; o[3] = w.hh / groups; o[4] = w.hh % groups;
         o[5] = w.blk_begin; o[6] = w.blk_end;
-        o[7] = partial ? rows_piece(r.every_piece, r.plan.dealt != 0, triple, c, w.first_piece != 0) : -1;
+        o[7] = partial ? rows_piece(r.every_piece, r.plan.dealt != 0, triple, c, w.blk_begin == 0) : -1;
         o[8] = w.blk_begin < w.blk_end ? w.n_pieces : 0;
       }
       ++n;

@@ -129,8 +129,8 @@ struct RowsCfg {
   static_assert(256 * kSoftmaxRegs + 128 * kControlRegs <= 384 * kLaunchRegs, "more registers than the launch has");
   static constexpr int kRingBytes = (kStagesK + kStagesV) * kStageBytes;
   static constexpr int kItemBytes = kItemRing * static_cast<int>(sizeof(RowsItem));
-  static constexpr int kPlanBytes = 8 * (kMaxRowsEntries + 1) + 4 * kMaxRowsEntries;
-  static constexpr int kMiscBytes = 512 + kItemBytes + kPlanBytes + 16;
+  static constexpr int kPlanBytes = 4 * (kMaxRowsEntries + 1) + 4 * kMaxRowsEntries;
+  static constexpr int kMiscBytes = 512 + kItemBytes + kPlanBytes + 12;
   static constexpr int kSmemBytes = 1024 + kQBytes + kRingBytes + kMiscBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 256;  // after the two S slots of 128 columns
@@ -156,7 +156,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   uint8_t* misc = vring + NSV * Cfg::kStageBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(misc);
   RowsItem* items_ring = reinterpret_cast<RowsItem*>(misc + 512);
-  long long* s_pre = reinterpret_cast<long long*>(misc + 512 + Cfg::kItemBytes);
+  uint32_t* s_pre = reinterpret_cast<uint32_t*>(misc + 512 + Cfg::kItemBytes);
   int32_t* s_len = reinterpret_cast<int32_t*>(s_pre + kMaxRowsEntries + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_len + kMaxRowsEntries);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -214,11 +214,6 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), Cfg::kTmemCols);
     ptx::tmem_relinquish();
   }
-  // Q rows that no TMA box writes (past tokens * G) stay zero or become an
-  // earlier item's: rows of S that no one reads.
-  for (int i = threadIdx.x; i < Cfg::kQBytes / 16; i += Cfg::kThreads)
-    reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
-  ptx::fence_proxy_async_smem();
   // Lengths may be produced, and outputs still read, by the previous kernel.
   ptx::griddep_wait();
   // The next launch may set itself up; it waits for this grid before it
@@ -436,18 +431,18 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     // ========================================================== plan walker
     if (p.plan.dealt == 0) {
       // exclusive prefix sums of the entries' units
-      long long run = 0;
+      uint32_t run = 0;
       for (int base = 0; base < n_entries; base += 32) {
         const int i = base + lane;
-        long long units = 0;
+        uint32_t units = 0;
         if (i < n_entries) {
           const RowsPlanSection& s = p.plan.s[i < n0 ? 0 : 1];
-          units = static_cast<long long>(s.heads) * rows_units(s, s_len[i]);
+          units = static_cast<uint32_t>(s.heads) * static_cast<uint32_t>(rows_units(s, s_len[i]));
         }
-        long long incl = units;
+        uint32_t incl = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += y;
         }
         if (i < n_entries) s_pre[i] = run + incl - units;
@@ -461,7 +456,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
       int longest = 0;              // blocks of the longest item so far
       RowsPlanIter iter;
-      iter.init(p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
+      iter.init(&p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
       for (uint32_t n = 0; ok; ++n) {
         RowsWork w;
         const bool more = iter.next(w);
@@ -471,7 +466,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         if (more) {
           const RowsSection& s = p.s[w.section];
           const int triple = w.b * p.plan.s[w.section].heads + w.hh;
-          const bool partial = p.every_piece != 0 || w.n_pieces > 1;
+          const bool partial = p.every_piece != 0 || w.whole == 0, first_piece = w.blk_begin == 0;
           const int n_pieces = w.blk_begin < w.blk_end ? w.n_pieces : 0;
           it.section = w.section;
           it.b = w.b;
@@ -481,9 +476,9 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           it.blk_end = w.blk_end;
           it.L = w.L;
           it.piece = partial ? rows_piece(p.every_piece != 0, p.plan.dealt != 0, triple, static_cast<int>(blockIdx.x),
-                                          w.first_piece != 0)
+                                          first_piece)
                              : -1;
-          if (w.first_piece && partial) {
+          if (first_piece && partial) {
             if (p.every_piece == 0)
               cut = make_int2(triple, n_pieces);
             else if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + s.rec + triple, sizeof(int2)))
@@ -620,7 +615,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;  // the scale is positive
         if (first) {
           nm = m_blk == -INFINITY ? kNoMax : -m_blk;
-        } else if (__any_sync(0xffffffffu, m_blk + nm > kRescaleThreshold)) {
+        } else if (__any_sync(0xffffffffu, r < rows && m_blk + nm > kRescaleThreshold)) {
           // O may be rescaled once the value MMA of the block before has landed
           if (!wait_pv(g - 1)) break;
           ptx::tc_fence_after();
@@ -629,7 +624,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2_approx(m_old - m_new);
           nm = m_new == -INFINITY ? kNoMax : -m_new;
           l *= alpha;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < HEAD_DIM / 16; ++c) {
             float o[16];
             ptx::tmem_ld_32x32b_x16(o_addr + 16 * c, o);
@@ -716,7 +711,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
         }
       };
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < HEAD_DIM / 32; ++c) {
         uint32_t o[32];
         if (!empty) {

@@ -7,8 +7,8 @@
 // over normalised fp32 partials, pieces with lse_s = -inf skipped (their rows
 // are never read), in a fixed order: the result is bit-identical from run to
 // run.  A lane owns HEAD_DIM / 32 consecutive elements of a row; a row
-// is one warp's, or (WARPS = 4, launches of few rows) its pieces are dealt to
-// four warps and their sums joined through shared memory.
+// is one warp's, or (WARPS > 1, launches of few rows) its pieces are dealt to
+// a CTA's warps and their sums joined through shared memory.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -19,7 +19,8 @@
 
 namespace gqa {
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
 
 struct RowsMergeSection {
   long long part_row;  // as in RowsSection
@@ -110,6 +111,7 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ o_part, cons
   if constexpr (WARPS > 1) {
     __shared__ float s_acc[WARPS][HEAD_DIM];
     __shared__ float s_w[WARPS];
+    __syncthreads();  // a row before is done with them
 #pragma unroll
     for (int i = 0; i < VEC; ++i) s_acc[warp][lane * VEC + i] = acc[i];
     if (lane == 0) s_w[warp] = W;
@@ -173,21 +175,24 @@ gqa_rows_merge_kernel(const RowsMergeParams p) {
   const int2 rec = p.rec[blockIdx.x];
   if (rec.x < 0 || rec.y <= 0 || 2 * (static_cast<int>(blockIdx.x) + rec.y) > s.pieces) return;
   const int rows = s.tokens * p.G;  // of a tile
-  const int i = static_cast<int>(blockIdx.y) * (kMergeThreads / 32) + (threadIdx.x >> 5);  // row of the triple's tiles
-  const int t = i / rows, r = i - t * rows;
   const int per_batch = p.kv_heads * s.groups;
   const int b = rec.x / per_batch, hg = rec.x - b * per_batch;
   const int h = hg / s.groups, grp = hg - h * s.groups;
-  const int tok = (grp * p.tiles + t) * s.tokens + r / p.G;
-  if (t >= p.tiles || tok >= s.nq) return;
   const long long piece_rows = static_cast<long long>(p.tiles) * rows;
   detail::PieceRun run[2];
-  run[0].first = (2ll * blockIdx.x + 1) * piece_rows + i;
-  run[0].next = 2ll * (blockIdx.x + 1) * piece_rows + i;
   run[0].stride = 2ll * piece_rows;
   run[0].n = rec.y;
-  const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + r % p.G;
-  detail::merge_row<HEAD_DIM, 1>(p.o_part, p.lse_part, run, 1, p.out, p.lse, p.out_dtype, row);
+  // rows of the triple's tiles
+  for (int i = static_cast<int>(blockIdx.y) * kMergeWarps + (threadIdx.x >> 5); i < p.tiles * rows;
+       i += static_cast<int>(gridDim.y) * kMergeWarps) {
+    const int t = i / rows, r = i - t * rows;
+    const int tok = (grp * p.tiles + t) * s.tokens + r / p.G;
+    if (tok >= s.nq) break;
+    run[0].first = (2ll * blockIdx.x + 1) * piece_rows + i;
+    run[0].next = 2ll * (blockIdx.x + 1) * piece_rows + i;
+    const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + r % p.G;
+    detail::merge_row<HEAD_DIM, 1>(p.o_part, p.lse_part, run, 1, p.out, p.lse, p.out_dtype, row);
+  }
 }
 
 // Every row of a batch, from the pieces of one or two sections: its own keys
@@ -199,28 +204,29 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long rows = static_cast<long long>(p.batch) * p.nq * p.Hq;
-  const long long row = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32 / WARPS) +
-                        (WARPS > 1 ? 0 : static_cast<int>(threadIdx.x >> 5));
-  if (row >= rows) return;
-  const long long bt = row / p.Hq;  // b * nq + t
-  const int hq = static_cast<int>(row - bt * p.Hq), h = hq / p.G;
-  detail::PieceRun run[2];
-  for (int i = 0; i < p.n_sections; ++i) {
-    const RowsMergeSection& s = p.s[i];
-    const long long b = bt / s.nq;  // the section's entry, and the token within it
-    const int tok = static_cast<int>(bt - b * s.nq);
-    const int per_group = (s.split_keys ? 1 : p.tiles) * s.tokens;
-    const int grp = tok / per_group, in_group = tok - grp * per_group;
-    const int t = in_group / s.tokens, r = (in_group - t * s.tokens) * p.G + (hq - h * p.G);
-    const int2 rec = p.rec[s.rec + (b * p.kv_heads + h) * s.groups + grp];
-    const long long tile_rows = static_cast<long long>(s.tokens) * p.G;
-    run[i].first = s.part_row + (static_cast<long long>(rec.x) * p.tiles + t) * tile_rows + r;
-    run[i].stride = s.split_keys ? tile_rows : p.tiles * tile_rows;
-    run[i].next = run[i].first + run[i].stride;
-    const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
-    run[i].n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
+  const int mine = WARPS > 1 ? 0 : static_cast<int>(threadIdx.x >> 5);
+  for (long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / WARPS) + mine; row < rows;
+       row += static_cast<long long>(gridDim.x) * (kMergeWarps / WARPS)) {
+    const uint32_t bt = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.Hq);  // b * nq + t
+    const int hq = static_cast<int>(static_cast<uint32_t>(row) - bt * static_cast<uint32_t>(p.Hq)), h = hq / p.G;
+    detail::PieceRun run[2];
+    for (int i = 0; i < p.n_sections; ++i) {
+      const RowsMergeSection& s = p.s[i];
+      const int b = static_cast<int>(bt / static_cast<uint32_t>(s.nq));  // the section's entry, the token within it
+      const int tok = static_cast<int>(bt) - b * s.nq;
+      const int per_group = (s.split_keys ? 1 : p.tiles) * s.tokens;
+      const int grp = tok / per_group, in_group = tok - grp * per_group;
+      const int t = in_group / s.tokens, r = (in_group - t * s.tokens) * p.G + (hq - h * p.G);
+      const int2 rec = p.rec[s.rec + (static_cast<long long>(b) * p.kv_heads + h) * s.groups + grp];
+      const long long tile_rows = static_cast<long long>(s.tokens) * p.G;
+      run[i].first = s.part_row + (static_cast<long long>(rec.x) * p.tiles + t) * tile_rows + r;
+      run[i].stride = s.split_keys ? tile_rows : p.tiles * tile_rows;
+      run[i].next = run[i].first + run[i].stride;
+      const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
+      run[i].n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
+    }
+    detail::merge_row<HEAD_DIM, WARPS>(p.o_part, p.lse_part, run, p.n_sections, p.out, p.lse, p.out_dtype, row);
   }
-  detail::merge_row<HEAD_DIM, WARPS>(p.o_part, p.lse_part, run, p.n_sections, p.out, p.lse, p.out_dtype, row);
 }
 
 }  // namespace gqa

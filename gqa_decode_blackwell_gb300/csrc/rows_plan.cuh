@@ -6,17 +6,19 @@
 // the entry's key blocks.  The sections' triples, in order, are laid along a
 // line of units: a triple with blocks takes item_units for its fixed cost (Q
 // load, pipeline fill, epilogue) and then block_units for every block; one
-// without takes none.  The U units are cut into C equal ranges, one per CTA,
-// and a block belongs to the CTA in whose range it begins.  A range is never
-// shorter than a block, so the CTAs that hold a triple's blocks are
-// consecutive and each holds at least one.
+// without takes none.  The U units are cut into C ranges of equal length (give
+// or take one unit), one per CTA, and a block belongs to the CTA in whose range
+// it begins.  A range is never shorter than a block, so the CTAs that hold a
+// triple's blocks are consecutive and each holds at least one.
 //
 // The units let blocks of different cost share a launch: compute-bound ones
 // of a prefix that many rows share, and memory-bound ones of the sequences'
 // own keys, run side by side on different SMs and end together.
 //
-// Batches with more entries than the kernel stages lengths for are dealt
-// whole, triple by triple, to the CTAs in turn.
+// Batches with more entries than the kernel stages lengths for (or so much work
+// that units would pass 32 bits, in which all of this is computed: emulated
+// 64-bit divisions cost a CTA's start-up microseconds) are dealt whole, triple
+// by triple, to the CTAs in turn.
 #pragma once
 #include <cstdint>
 
@@ -30,7 +32,8 @@ struct RowsPlanSection {
   int batch;        // entries (0: no such section)
   int heads;        // triples of an entry
   int max_len;      // lengths are clamped to [0, max_len]
-  int block_units, item_units;
+  int block_shift;  // a block takes 1 << block_shift units
+  int item_units;
 };
 
 struct RowsPlan {
@@ -43,42 +46,54 @@ struct RowsWork {
   int section, b, hh;      // triple hh of entry b
   int L;
   int blk_begin, blk_end;  // equal: no keys
-  int first_piece, n_pieces;
+  int whole;               // all of the triple's blocks
+  int n_pieces;            // of the triple, where blk_begin is its first block
 };
 
 GQA_HD int rows_units(const RowsPlanSection& s, int L) {
   const int nblk = num_blocks(L);
-  return nblk > 0 ? nblk * s.block_units + s.item_units : 0;
+  return nblk > 0 ? (nblk << s.block_shift) + s.item_units : 0;
 }
 
 struct RowsPlanIter {
-  RowsPlan rp;
-  const int32_t* lens;    // clamped lengths of both sections' entries (dealt: unused)
-  const long long* pre;   // entries + 1 prefix sums of their units
-  const int32_t* raw[2];  // each section's lengths
-  long long U, lo, hi, next_triple;
-  int e, hh, cta, C;
+  const RowsPlan* rp;
+  const int32_t* lens;     // clamped lengths of both sections' entries (dealt: unused)
+  const uint32_t* pre;     // entries + 1 prefix sums of their units
+  const int32_t* raw0;     // each section's lengths
+  const int32_t* raw1;
+  uint32_t U, lo, hi;
+  uint32_t q, rem, C;      // ranges: `rem` of q + 1 units, then of q
+  int e, hh, cta;
+  long long next_triple;
 
-  GQA_HD void init(const RowsPlan& p, const int32_t* raw0, const int32_t* raw1, const int32_t* clamped,
-                   const long long* prefix, int c) {
-    rp = p; lens = clamped; pre = prefix; raw[0] = raw0; raw[1] = raw1; cta = c;
+  // First unit of CTA c's range, and the CTA whose range holds unit u.
+  GQA_HD uint32_t start(uint32_t c) const { return c * q + (c < rem ? c : rem); }
+  GQA_HD int owner(uint32_t u) const {
+    const uint32_t split = rem * (q + 1);
+    return static_cast<int>(u < split ? u / (q + 1) : rem + (u - split) / q);
+  }
+  GQA_HD const RowsPlanSection& section(int entry) const { return rp->s[entry < rp->s[0].batch ? 0 : 1]; }
+
+  GQA_HD void init(const RowsPlan* plan, const int32_t* lens0, const int32_t* lens1, const int32_t* clamped,
+                   const uint32_t* prefix, int c) {
+    rp = plan; lens = clamped; pre = prefix; raw0 = lens0; raw1 = lens1; cta = c;
     next_triple = c;
-    if (rp.dealt) return;
-    const int E = rp.s[0].batch + rp.s[1].batch;
+    if (rp->dealt) return;
+    const int E = rp->s[0].batch + rp->s[1].batch;
     U = pre[E];
-    int longest = 1;
-    for (int i = 0; i < 2; ++i)
-      if (rp.s[i].batch > 0 && rp.s[i].block_units > longest) longest = rp.s[i].block_units;
-    const long long most = div_nonneg(U, longest);
-    C = most < 1 ? 1 : (most < rp.num_ctas ? static_cast<int>(most) : rp.num_ctas);
+    const int w0 = rp->s[0].block_shift, w1 = rp->s[1].block_shift;
+    const uint32_t most = U >> (w0 > w1 ? w0 : w1);  // ranges at least a block long
+    C = most < 1 ? 1 : (most < static_cast<uint32_t>(rp->num_ctas) ? most : static_cast<uint32_t>(rp->num_ctas));
+    q = U / C;
+    rem = U - q * C;
     hh = 0;
-    if (c >= C) {  // this CTA owns nothing
+    if (static_cast<uint32_t>(c) >= C) {  // this CTA owns nothing
       e = E;
       lo = hi = U;
       return;
     }
-    lo = muldiv(c, U, C);
-    hi = muldiv(c + 1, U, C);
+    lo = start(static_cast<uint32_t>(c));
+    hi = start(static_cast<uint32_t>(c) + 1);
     int a = 0, z = E;  // the first entry that reaches lo
     while (a < z) {
       const int mid = (a + z) / 2;
@@ -87,72 +102,69 @@ struct RowsPlanIter {
     e = a;
     if (e < E && pre[e] < lo) {
       const int u = rows_units(section(e), lens[e]);
-      if (u > 0) hh = static_cast<int>(div_nonneg(lo - pre[e], u));
+      if (u > 0) hh = static_cast<int>((lo - pre[e]) / static_cast<uint32_t>(u));
     }
   }
-  GQA_HD const RowsPlanSection& section(int entry) const { return rp.s[entry < rp.s[0].batch ? 0 : 1]; }
-  GQA_HD int owner(long long u) const { return static_cast<int>(div_nonneg((u + 1) * C - 1, U)); }
-  GQA_HD void advance() {
-    if (++hh == section(e).heads) { hh = 0; ++e; }
-  }
-  GQA_HD void emit(RowsWork& w, int blk_begin, int blk_end, int first, int pieces) {
-    w.section = e < rp.s[0].batch ? 0 : 1;
-    w.b = e - (w.section ? rp.s[0].batch : 0);
+  GQA_HD void emit(RowsWork& w, int blk_begin, int blk_end, int whole, int pieces) {
+    w.section = e < rp->s[0].batch ? 0 : 1;
+    w.b = e - (w.section ? rp->s[0].batch : 0);
     w.hh = hh;
     w.L = lens[e];
     w.blk_begin = blk_begin;
     w.blk_end = blk_end;
-    w.first_piece = first;
+    w.whole = whole;
     w.n_pieces = pieces;
-    advance();
   }
   GQA_HD bool next_dealt(RowsWork& w) {
-    const long long n0 = static_cast<long long>(rp.s[0].batch) * rp.s[0].heads;
-    const long long n1 = static_cast<long long>(rp.s[1].batch) * rp.s[1].heads;
+    const long long n0 = static_cast<long long>(rp->s[0].batch) * rp->s[0].heads;
+    const long long n1 = static_cast<long long>(rp->s[1].batch) * rp->s[1].heads;
     if (next_triple >= n0 + n1) return false;
     w.section = next_triple < n0 ? 0 : 1;
     const long long t = next_triple - (w.section ? n0 : 0);
-    const RowsPlanSection& s = rp.s[w.section];
+    const RowsPlanSection& s = rp->s[w.section];
     w.b = static_cast<int>(div_nonneg(t, s.heads));
     w.hh = static_cast<int>(t - static_cast<long long>(w.b) * s.heads);
-    w.L = clamp_len(raw[w.section][w.b], s.max_len);
+    w.L = clamp_len((w.section ? raw1 : raw0)[w.b], s.max_len);
     w.blk_begin = 0;
     w.blk_end = num_blocks(w.L);
-    w.first_piece = 1;
+    w.whole = 1;
     w.n_pieces = 1;
-    next_triple += rp.num_ctas;
+    next_triple += rp->num_ctas;
     return true;
   }
   GQA_HD bool next(RowsWork& w) {
-    if (rp.dealt) return next_dealt(w);
-    const int E = rp.s[0].batch + rp.s[1].batch;
+    if (rp->dealt) return next_dealt(w);
+    const int E = rp->s[0].batch + rp->s[1].batch;
     while (e < E) {
       const RowsPlanSection& s = section(e);
-      const int u = rows_units(s, lens[e]);
-      const long long v = pre[e] + static_cast<long long>(hh) * u;
+      const uint32_t u = static_cast<uint32_t>(rows_units(s, lens[e]));
+      const uint32_t v = pre[e] + static_cast<uint32_t>(hh) * u;
+      bool mine = false;
       if (u == 0) {
-        if ((v >= lo && v < hi) || (v == U && cta == C - 1)) {
+        if ((v >= lo && v < hi) || (v == U && static_cast<uint32_t>(cta) == C - 1)) {
           emit(w, 0, 0, 1, 1);
-          return true;
+          mine = true;
+        } else if (v >= hi) {
+          return false;
         }
+      } else {
         if (v >= hi) return false;
-        advance();
-        continue;
+        const uint32_t nblk = static_cast<uint32_t>(num_blocks(lens[e]));
+        const int sh = s.block_shift;
+        const uint32_t up = (1u << sh) - 1u;
+        const uint32_t first = v + static_cast<uint32_t>(s.item_units);  // where block 0 begins
+        const uint32_t last = first + ((nblk - 1) << sh);                 // and the last one
+        const uint32_t from = lo > first ? (lo - first + up) >> sh : 0;
+        const uint32_t upto = hi > last ? nblk : (hi > first ? (hi - first + up) >> sh : 0);
+        if (from < upto) {
+          const bool whole = from == 0 && upto == nblk;
+          emit(w, static_cast<int>(from), static_cast<int>(upto), whole,
+               from > 0 ? 0 : (whole ? 1 : owner(last) - cta + 1));
+          mine = true;
+        }
       }
-      if (v >= hi) return false;
-      const int nblk = num_blocks(lens[e]), bu = s.block_units;
-      const long long first = v + s.item_units;  // where block 0 begins
-      const long long from = lo > first ? div_nonneg(lo - first + bu - 1, bu) : 0;
-      const long long upto = hi > first ? div_nonneg(hi - first + bu - 1, bu) : 0;
-      const int blk_begin = static_cast<int>(from < nblk ? from : nblk);
-      const int blk_end = static_cast<int>(upto < nblk ? upto : nblk);
-      if (blk_begin >= blk_end) {
-        advance();
-        continue;
-      }
-      const int pieces = owner(first + static_cast<long long>(nblk - 1) * bu) - owner(first) + 1;
-      emit(w, blk_begin, blk_end, blk_begin == 0, pieces);
-      return true;
+      if (++hh == s.heads) { hh = 0; ++e; }
+      if (mine) return true;
     }
     return false;
   }

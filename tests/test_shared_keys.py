@@ -176,7 +176,7 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix=None):
         assert 0 <= cta < ctas and 0 <= h < Hkv and 0 <= grp < groups
         by_triple.setdefault((sec, b, h, grp), []).append((lo, hi, piece, n, cta))
         load[cta] = load.get(cta, 0) + hi - lo
-        if piece >= 0 and n:
+        if piece >= 0 and lo < hi:
             assert piece < pieces and (sec, piece) not in used, "two pieces share a place"
             used.add((sec, piece))
     total = 0
@@ -193,7 +193,7 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix=None):
             assert len(its) == 1 and its[0][0] == its[0][1] and its[0][3] == 0
             continue
         assert [x[1] for x in its[:-1]] == [x[0] for x in its[1:]] and its[0][0] == 0 and its[-1][1] == blocks
-        assert all(lo < hi and n == len(its) for lo, hi, _, n, _ in its)
+        assert all(lo < hi for lo, hi, _, _, _ in its) and its[0][3] == len(its)
         first, ctas_of = its[0][2], [x[4] for x in its]
         assert ctas_of == list(range(ctas_of[0], ctas_of[0] + len(its)))
         if every:          # consecutive places from the first
@@ -214,7 +214,7 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix=None):
 def test_plan_covers_every_block_once(lens, nq, Hq, Hkv, d, s_max, sm):
     load = _check_plan(lens, nq, Hq, Hkv, d, s_max, sm)
     if len(lens) <= 1024 and min(lens) == max(lens) > 0 and sum(load.values()) >= 4 * sm:
-        assert max(load.values()) - min(load.values()) <= 3   # equal ranges, but for the item units
+        assert max(load.values()) - min(load.values()) <= 6   # equal ranges, but for the items' fixed cost
 
 
 @pytest.mark.parametrize("sm", [1, 7, 152])
