@@ -22,9 +22,7 @@ namespace {
 // Units of the plan's line (rows_plan.cuh): a key block against two tiles of
 // rows, against one, and a triple's fixed cost -- Q load, pipeline fill,
 // epilogue.
-// CTAs of a merge: a few per SM; and up to this many rows, a CTA takes a row
-// at a time, its warps sharing the pieces.
-constexpr int kMergeCtasPerSm = 4;
+// Up to this many rows a merge gives each a CTA, whose warps share its pieces.
 constexpr size_t kMergeSharedRows = 1024;
 
 constexpr int kTwoTileShift = 2, kOneTileShift = 1, kItemUnits = 4;
@@ -248,13 +246,14 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
   m.G = G;
   m.kv_heads = r.kv_heads;
   m.tiles = tiles_of(hd);
-  const size_t ctas = static_cast<size_t>(st->sm_count) * kMergeCtasPerSm;
   if (!r.every_piece) {
     const void* fn = hd == 64    ? reinterpret_cast<const void*>(&gqa_rows_merge_kernel<64>)
                      : hd == 256 ? reinterpret_cast<const void*>(&gqa_rows_merge_kernel<256>)
                                  : reinterpret_cast<const void*>(&gqa_rows_merge_kernel<128>);
-    return launch_kernel(fn, dim3(static_cast<unsigned>(r.plan.num_ctas), kMergeCtasPerSm), kMergeThreads, 0, &m,
-                         stream);
+    const int per_cta = kMergeWarps * (hd == 256 ? kCutRows<256> : kCutRows<128>);
+    const int per_triple = m.tiles * m.s[0].tokens * G;
+    return launch_kernel(fn, dim3(static_cast<unsigned>(r.plan.num_ctas), (per_triple + per_cta - 1) / per_cta),
+                         kMergeThreads, 0, &m, stream);
   }
   const bool share = rows <= kMergeSharedRows;
   const void* fn = hd == 64    ? (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<64, kMergeWarps>)
@@ -264,7 +263,7 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
                                : (share ? reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<128, kMergeWarps>)
                                         : reinterpret_cast<const void*>(&gqa_pieces_merge_kernel<128, 1>));
   const size_t want = share ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
-  return launch_kernel(fn, dim3(static_cast<unsigned>(want < ctas ? want : ctas)), kMergeThreads, 0, &m, stream);
+  return launch_kernel(fn, dim3(static_cast<unsigned>(want)), kMergeThreads, 0, &m, stream);
 }
 
 gqa_status_t check_cross(const gqa_desc_t* d) {

@@ -4,11 +4,13 @@
 //   M = max_s lse_s;  w_s = exp(lse_s - M);  O = sum_s w_s O_s / sum_s w_s;
 //   lse = M + ln(sum_s w_s)
 //
-// over normalised fp32 partials, pieces with lse_s = -inf skipped (their rows
-// are never read), in a fixed order: the result is bit-identical from run to
-// run.  A lane owns HEAD_DIM / 32 consecutive elements of a row; a row
-// is one warp's, or (WARPS > 1, launches of few rows) its pieces are dealt to
-// a CTA's warps and their sums joined through shared memory.
+// over normalised fp32 partials, in a fixed order: the result is bit-identical
+// from run to run.  A warp keeps a running maximum and sum over a row's pieces,
+// whose LSEs and values it loads a batch at a time, all of them before the
+// first is used: what bounds the merge is how much it has in flight, not its
+// arithmetic.  A lane owns HEAD_DIM / 32 consecutive elements.  The values of a
+// piece with lse_s = -inf may be anything (they are not written) and take no
+// part.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -51,87 +53,66 @@ struct PieceRun {
   __device__ __forceinline__ long long at(int j) const { return j == 0 ? first : next + (j - 1) * stride; }
 };
 
-__device__ __forceinline__ float max_or_nan(float a, float b) {  // a NaN piece makes the row NaN
-  return a != a || b != b ? NAN : fmaxf(a, b);
-}
+// A row's merge so far: M = max_s lse_s (natural log), W = sum_s exp(lse_s - M), acc = sum_s exp(lse_s - M) O_s.
+template <int VEC>
+struct RowSum {
+  float M, W, acc[VEC];
+  __device__ __forceinline__ void clear() {
+    M = -INFINITY;
+    W = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  }
+  // Adds a piece; an empty one (lse = -inf) leaves everything as it is.
+  __device__ __forceinline__ void add(float lse, const float (&v)[VEC]) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if (lse == -INFINITY) return;
+    const float m = fmaxf(M, lse);  // (a NaN lse makes its own weight NaN)
+    const float a = M == -INFINITY ? 0.f : ptx::ex2_approx((M - m) * kLog2e), b = ptx::ex2_approx((lse - m) * kLog2e);
+    M = m;
+    W = W * a + b;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = acc[e] * a + b * v[e];
+  }
+};
 
-// Merges runs[0 .. n_runs) into row `row`.  With WARPS > 1 the CTA's warps
-// share the row, and every thread of the CTA must call it.
-template <int HEAD_DIM, int WARPS>
-__device__ __forceinline__ void merge_row(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                                          const PieceRun (&runs)[2], int n_runs, void* out, float* lse, int out_dtype,
-                                          long long row) {
+// Pieces first, first + step, ... of a run into R consecutive rows' sums, NB of them in flight.
+template <int HEAD_DIM, int R, int NB>
+__device__ __forceinline__ void add_run(RowSum<HEAD_DIM / 32> (&sum)[R], const float* __restrict__ o_part,
+                                        const float* __restrict__ lse_part, const PieceRun& run, int first, int step) {
   constexpr int VEC = HEAD_DIM / 32;
-  constexpr int kBatch = 32 / VEC;  // partial rows in flight
-  constexpr float kLog2e = 1.4426950408889634f;
-  const int lane = threadIdx.x & 31, warp = WARPS > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
-  float M = -INFINITY;
-  for (int i = 0; i < n_runs; ++i)
-    for (int j = lane; j < runs[i].n; j += 32) M = max_or_nan(M, lse_part[runs[i].at(j)]);
+  const int lane = threadIdx.x & 31;
+  for (int j0 = first; j0 < run.n; j0 += NB * step) {
+    float l[NB][R], v[NB][R][VEC];
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = max_or_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[VEC];
+    for (int q = 0; q < NB; ++q) {
+      const int j = j0 + q * step;
+      const long long at = run.at(j < run.n ? j : j0);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-  float W = 0.f;  // the weights of this lane's pieces
-  if (M != -INFINITY) {
-    for (int i = 0; i < n_runs; ++i) {
-      // this warp's pieces: warp, warp + WARPS, ...; 32 of them at a time
-      for (int j0 = warp; j0 < runs[i].n; j0 += 32 * WARPS) {
-        const int mine = j0 + lane * WARPS;
-        const float l = mine < runs[i].n ? lse_part[runs[i].at(mine)] : -INFINITY;
-        const float w = l == -INFINITY ? 0.f : ptx::ex2_approx((l - M) * kLog2e);
-        W += w;
-        const int left = (runs[i].n - j0 + WARPS - 1) / WARPS, cnt = left < 32 ? left : 32;
-        for (int j = 0; j < cnt; j += kBatch) {
-          float v[kBatch][VEC], wb[kBatch];
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const float ws = __shfl_sync(0xffffffffu, w, (j + q) & 31);
-            wb[q] = j + q < cnt ? ws : 0.f;
-            if (wb[q] != 0.f) {
-              load_vec<VEC>(o_part + runs[i].at(j0 + (j + q) * WARPS) * HEAD_DIM + lane * VEC, v[q]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) v[q][e] = 0.f;
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q)
-            if (wb[q] != 0.f) {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) acc[e] += wb[q] * v[q][e];
-            }
-        }
+      for (int r = 0; r < R; ++r) {
+        l[q][r] = lse_part[at + r];
+        load_vec<VEC>(o_part + (at + r) * HEAD_DIM + lane * VEC, v[q][r]);
       }
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-  }
-  if constexpr (WARPS > 1) {
-    __shared__ float s_acc[WARPS][HEAD_DIM];
-    __shared__ float s_w[WARPS];
-    __syncthreads();  // a row before is done with them
+    for (int q = 0; q < NB; ++q) {
+      if (j0 + q * step >= run.n) break;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s_acc[warp][lane * VEC + i] = acc[i];
-    if (lane == 0) s_w[warp] = W;
-    __syncthreads();
-    if (warp != 0) return;
-    W = 0.f;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) {
-      W += s_w[k];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += s_acc[k][lane * VEC + i];
+      for (int r = 0; r < R; ++r) sum[r].add(l[q][r], v[q][r]);
     }
   }
-  if (M != -INFINITY) {
-    const float inv = 1.0f / W;
+}
+
+template <int HEAD_DIM>
+__device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void* out, float* lse, int out_dtype,
+                                          long long row) {
+  constexpr int VEC = HEAD_DIM / 32;
+  const int lane = threadIdx.x & 31;
+  const bool none = sum.M == -INFINITY;
+  const float inv = none ? 0.f : 1.0f / sum.W;
+  float acc[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] *= inv;
-  }
+  for (int i = 0; i < VEC; ++i) acc[i] = none ? 0.f : sum.acc[i] * inv;
   if (out_dtype == kOutF32) {
     float* dst = static_cast<float*>(out) + row * HEAD_DIM + lane * VEC;
     if constexpr (VEC == 8) {
@@ -159,74 +140,121 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ o_part, cons
     else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }
-  if (lane == 0 && lse != nullptr) lse[row] = M == -INFINITY ? -INFINITY : M + 0.69314718055994531f * __log2f(W);
+  if (lane == 0 && lse != nullptr) lse[row] = none ? -INFINITY : sum.M + 0.69314718055994531f * __log2f(sum.W);
 }
 
 }  // namespace detail
+
+// Rows a warp of the cut triples' merge takes at once: most of those have two
+// pieces, and two pieces of one row are too little to have in flight.
+template <int HEAD_DIM>
+constexpr int kCutRows = HEAD_DIM == 256 ? 2 : 4;
 
 // The cut triples of a launch of one section: blockIdx.x is the CTA of that
 // launch in which a cut triple may begin, blockIdx.y a group of its rows.
 template <int HEAD_DIM>
 __global__ void __launch_bounds__(kMergeThreads)
 gqa_rows_merge_kernel(const RowsMergeParams p) {
+  constexpr int R = kCutRows<HEAD_DIM>;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const RowsMergeSection& s = p.s[0];
   const int2 rec = p.rec[blockIdx.x];
   if (rec.x < 0 || rec.y <= 0 || 2 * (static_cast<int>(blockIdx.x) + rec.y) > s.pieces) return;
   const int rows = s.tokens * p.G;  // of a tile
+  const long long piece_rows = static_cast<long long>(p.tiles) * rows;
+  // rows i .. i + R - 1 of the triple's tiles (past the last one: the last again)
+  const int i0 = (static_cast<int>(blockIdx.y) * kMergeWarps + static_cast<int>(threadIdx.x >> 5)) * R;
+  if (i0 >= piece_rows) return;
+  const int i = i0 + R <= piece_rows ? i0 : static_cast<int>(piece_rows) - R;
+  detail::PieceRun run;
+  run.first = (2ll * blockIdx.x + 1) * piece_rows + i;
+  run.next = 2ll * (blockIdx.x + 1) * piece_rows + i;
+  run.stride = 2ll * piece_rows;
+  run.n = rec.y;
+  detail::RowSum<HEAD_DIM / 32> sum[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) sum[r].clear();
+  detail::add_run<HEAD_DIM, R, 2>(sum, p.o_part, p.lse_part, run, 0, 1);
   const int per_batch = p.kv_heads * s.groups;
   const int b = rec.x / per_batch, hg = rec.x - b * per_batch;
   const int h = hg / s.groups, grp = hg - h * s.groups;
-  const long long piece_rows = static_cast<long long>(p.tiles) * rows;
-  detail::PieceRun run[2];
-  run[0].stride = 2ll * piece_rows;
-  run[0].n = rec.y;
-  // rows of the triple's tiles
-  for (int i = static_cast<int>(blockIdx.y) * kMergeWarps + (threadIdx.x >> 5); i < p.tiles * rows;
-       i += static_cast<int>(gridDim.y) * kMergeWarps) {
-    const int t = i / rows, r = i - t * rows;
-    const int tok = (grp * p.tiles + t) * s.tokens + r / p.G;
-    if (tok >= s.nq) break;
-    run[0].first = (2ll * blockIdx.x + 1) * piece_rows + i;
-    run[0].next = 2ll * (blockIdx.x + 1) * piece_rows + i;
-    const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + r % p.G;
-    detail::merge_row<HEAD_DIM, 1>(p.o_part, p.lse_part, run, 1, p.out, p.lse, p.out_dtype, row);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int t = (i + r) / rows, in_tile = i + r - t * rows;
+    const int tok = (grp * p.tiles + t) * s.tokens + in_tile / p.G;
+    if (tok >= s.nq) continue;
+    const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + in_tile % p.G;
+    detail::write_row<HEAD_DIM>(sum[r], p.out, p.lse, p.out_dtype, row);
   }
 }
 
 // Every row of a batch, from the pieces of one or two sections: its own keys
 // (the last section), and before them the prefix, whose one entry holds all
-// the batch's tokens.
+// the batch's tokens.  WARPS = 1: a warp to a row; else (launches of few rows)
+// a CTA, whose warps take its pieces in turn and join their sums.
 template <int HEAD_DIM, int WARPS>
 __global__ void __launch_bounds__(kMergeThreads)
 gqa_pieces_merge_kernel(const RowsMergeParams p) {
+  constexpr int VEC = HEAD_DIM / 32, NB = WARPS > 1 ? 4 : 8;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const long long rows = static_cast<long long>(p.batch) * p.nq * p.Hq;
-  const int mine = WARPS > 1 ? 0 : static_cast<int>(threadIdx.x >> 5);
-  for (long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / WARPS) + mine; row < rows;
-       row += static_cast<long long>(gridDim.x) * (kMergeWarps / WARPS)) {
-    const uint32_t bt = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.Hq);  // b * nq + t
-    const int hq = static_cast<int>(static_cast<uint32_t>(row) - bt * static_cast<uint32_t>(p.Hq)), h = hq / p.G;
-    detail::PieceRun run[2];
-    for (int i = 0; i < p.n_sections; ++i) {
-      const RowsMergeSection& s = p.s[i];
-      const int b = static_cast<int>(bt / static_cast<uint32_t>(s.nq));  // the section's entry, the token within it
-      const int tok = static_cast<int>(bt) - b * s.nq;
-      const int per_group = (s.split_keys ? 1 : p.tiles) * s.tokens;
-      const int grp = tok / per_group, in_group = tok - grp * per_group;
-      const int t = in_group / s.tokens, r = (in_group - t * s.tokens) * p.G + (hq - h * p.G);
-      const int2 rec = p.rec[s.rec + (static_cast<long long>(b) * p.kv_heads + h) * s.groups + grp];
-      const long long tile_rows = static_cast<long long>(s.tokens) * p.G;
-      run[i].first = s.part_row + (static_cast<long long>(rec.x) * p.tiles + t) * tile_rows + r;
-      run[i].stride = s.split_keys ? tile_rows : p.tiles * tile_rows;
-      run[i].next = run[i].first + run[i].stride;
-      const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
-      run[i].n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
-    }
-    detail::merge_row<HEAD_DIM, WARPS>(p.o_part, p.lse_part, run, p.n_sections, p.out, p.lse, p.out_dtype, row);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint32_t rows = static_cast<uint32_t>(p.batch) * static_cast<uint32_t>(p.nq) * static_cast<uint32_t>(p.Hq);
+  const uint32_t row = WARPS > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + warp;
+  if (row >= rows) return;
+  const uint32_t bt = row / static_cast<uint32_t>(p.Hq);  // b * nq + t
+  const int hq = static_cast<int>(row - bt * static_cast<uint32_t>(p.Hq)), h = hq / p.G;
+  detail::PieceRun run[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    run[i].n = 0;
+    if (i >= p.n_sections) continue;
+    const RowsMergeSection& s = p.s[i];
+    const int b = static_cast<int>(bt / static_cast<uint32_t>(s.nq));  // the section's entry, the token within it
+    const int tok = static_cast<int>(bt) - b * s.nq;
+    const int per_group = (s.split_keys ? 1 : p.tiles) * s.tokens;
+    const int grp = tok / per_group, in_group = tok - grp * per_group;
+    const int t = in_group / s.tokens, r = (in_group - t * s.tokens) * p.G + (hq - h * p.G);
+    const int2 rec = p.rec[s.rec + (static_cast<long long>(b) * p.kv_heads + h) * s.groups + grp];
+    const long long tile_rows = static_cast<long long>(s.tokens) * p.G;
+    run[i].first = s.part_row + (static_cast<long long>(rec.x) * p.tiles + t) * tile_rows + r;
+    run[i].stride = s.split_keys ? tile_rows : p.tiles * tile_rows;
+    run[i].next = run[i].first + run[i].stride;
+    const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
+    run[i].n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
   }
+  detail::RowSum<VEC> sum[1];
+  sum[0].clear();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    detail::add_run<HEAD_DIM, 1, NB>(sum, p.o_part, p.lse_part, run[i], WARPS > 1 ? warp : 0, WARPS);
+  if constexpr (WARPS > 1) {
+    __shared__ float s_acc[WARPS][HEAD_DIM], s_m[WARPS], s_w[WARPS];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s_acc[warp][lane * VEC + e] = sum[0].acc[e];
+    if (lane == 0) {
+      s_m[warp] = sum[0].M;
+      s_w[warp] = sum[0].W;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    constexpr float kLog2e = 1.4426950408889634f;
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) M = fmaxf(M, s_m[k]);
+    sum[0].clear();
+    sum[0].M = M;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      if (s_m[k] == -INFINITY) continue;
+      const float w = ptx::ex2_approx((s_m[k] - M) * kLog2e);
+      sum[0].W += w * s_w[k];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum[0].acc[e] += w * s_acc[k][lane * VEC + e];
+    }
+  }
+  detail::write_row<HEAD_DIM>(sum[0], p.out, p.lse, p.out_dtype, row);
 }
 
 }  // namespace gqa
