@@ -313,51 +313,78 @@ def decode(q, k_cache, v_cache, seqlens, *, num_splits: int = 0, scale: float = 
     return out, lse
 
 
-def _check_devices(stream, **tensors):
-    """Every tensor on one CUDA device, which the call then makes current: the
-    C library computes on the current device."""
-    first = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if first is None:
-            first = t.device
-        elif t.device != first:
-            raise ValueError(f"{name} is on {t.device}, not on {first}")
-    device = getattr(stream, "device", None)
-    if device is not None and device != first:
-        raise ValueError(f"the stream is on {device}, not on {first}")
-    return first
+_TYPE_CODES = None
 
 
-def _on_device(device, call):
-    """call() with `device` current."""
+def _type_codes():
+    """gqa_dtype_t of each torch type (built on first use: torch is imported then)."""
+    global _TYPE_CODES
+    if _TYPE_CODES is None:
+        import torch
+
+        _TYPE_CODES = {torch.bfloat16: GQA_DTYPE_BF16, torch.float16: GQA_DTYPE_FP16, torch.float32: GQA_DTYPE_FP32}
+    return _TYPE_CODES
+
+
+def _shared_desc(q, k, out_dtype, scale, causal):
+    """Description of q [B, nq, Hq, d] against k [B, S_max, Hkv, d], and q's device index."""
+    codes = _type_codes()
+    in_code = codes.get(q.dtype)
+    if in_code != GQA_DTYPE_BF16 and in_code != GQA_DTYPE_FP16:
+        raise ValueError(f"q must be bf16 or fp16, not {q.dtype}")
+    out_code = in_code if out_dtype is None else codes.get(out_dtype)
+    if out_code is None:
+        raise ValueError(f"unsupported output type {out_dtype}")
+    device = q.get_device()
+    if device < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and the keys must have four dimensions")
+    B, nq, Hq, d = q.shape
+    Bk, s_max, Hkv, dk = k.shape
+    if Bk != B or dk != d:
+        raise ValueError(f"q {tuple(q.shape)} and keys {tuple(k.shape)} disagree")
+    return gqa_desc_t(B, nq, Hq, Hkv, d, s_max, scale, 1 if causal else 0, out_code, in_code, GQA_REDUCE_AUTO), device
+
+
+def _check_call(device, q, keys, lengths, out, lse, workspace, stream):
+    """Types, layouts and devices of a call's tensors (their shapes beyond q and
+    k are the caller's to check).  Returns the raw stream."""
     import torch
 
-    if torch.cuda.current_device() == device.index:
-        return call()
+    dtype = q.dtype
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    for t in keys:
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError("keys and values must be contiguous, of q's type and on its device")
+    for t, n in lengths:
+        if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"lengths must be {n} contiguous int32 on q's device")
+    if out.shape != q.shape or not out.is_contiguous() or out.get_device() != device:
+        raise ValueError("out must be contiguous, of q's shape and on its device")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()
+                            or lse.get_device() != device):
+        raise ValueError("lse must be contiguous fp32 [B, nq, Hq] on q's device")
+    if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != device):
+        raise ValueError("workspace must be contiguous and on q's device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, not on q's device")
+    return stream.cuda_stream
+
+
+def _on_device(device, fn, *args):
+    """fn(*args) with `device` current (the C library computes on the current device)."""
+    import torch
+
+    if torch._C._cuda_getDevice() == device:
+        return fn(*args)
     with torch.cuda.device(device):
-        return call()
-
-
-def _outputs_ok(q, out, lse, workspace):
-    import torch
-
-    if out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous fp32 {tuple(q.shape[:3])} tensor")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-
-
-def _lengths_ok(name, t, n):
-    import torch
-
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must hold {n} contiguous int32")
+        return fn(*args)
 
 
 def _bytes_of(t) -> int:
@@ -366,50 +393,45 @@ def _bytes_of(t) -> int:
 
 def gqa_cross_workspace_size(q, k, *, out_dtype=None) -> int:
     """Bytes gqa_cross_attn needs for q [B, nq, Hq, d] against keys [B, S_max, Hkv, d]."""
-    desc = make_desc(q, k, out_dtype=out_dtype)
-    return _on_device(_check_devices(None, q=q, k=k),
-                      lambda: int(lib().gqa_cross_workspace_size(ctypes.byref(desc))))
+    desc, device = _shared_desc(q, k, out_dtype, 0.0, False)
+    return int(_on_device(device, lib().gqa_cross_workspace_size, ctypes.byref(desc)))
 
 
 def gqa_cross_attn(q, k, v, kv_lens, out, lse=None, workspace=None, *, scale: float = 0.0, stream=None) -> None:
     """Cross attention into ``out`` (and ``lse``); see gqa_cross_attn in ``include/gqa_shared_keys.h``."""
-    _inputs_ok(q, k, v, kv_lens)
-    _lengths_ok("kv_lens", kv_lens, q.shape[0])
-    _outputs_ok(q, out, lse, workspace)
-    device = _check_devices(stream, q=q, k=k, v=v, kv_lens=kv_lens, out=out, lse=lse, workspace=workspace)
-    desc = make_desc(q, k, scale=scale, out_dtype=out.dtype)
-    rc = _on_device(device, lambda: lib().gqa_cross_attn(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(out), _ptr(lse), _ptr(workspace),
-        _bytes_of(workspace), _stream(stream)))
-    _check(rc, "gqa_cross_attn")
+    desc, device = _shared_desc(q, k, out.dtype, scale, False)
+    if v.shape != k.shape:
+        raise ValueError("k and v shapes differ")
+    raw = _check_call(device, q, (k, v), ((kv_lens, desc.batch),), out, lse, workspace, stream)
+    rc = _on_device(device, lib().gqa_cross_attn, ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    kv_lens.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(workspace), _bytes_of(workspace), raw)
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_cross_attn")
 
 
 def gqa_prefix_workspace_size(q, k_prefix, k_cache, *, causal: bool = False, out_dtype=None) -> int:
     """Bytes gqa_prefix_attn needs for a decode step q, k_cache behind k_prefix [max_prefix, Hkv, d]."""
-    desc = make_desc(q, k_cache, causal=causal, out_dtype=out_dtype)
-    return _on_device(_check_devices(None, q=q, k_prefix=k_prefix, k_cache=k_cache), lambda: int(
-        lib().gqa_prefix_workspace_size(ctypes.byref(desc), int(k_prefix.shape[0]))))
+    desc, device = _shared_desc(q, k_cache, out_dtype, 0.0, causal)
+    return int(_on_device(device, lib().gqa_prefix_workspace_size, ctypes.byref(desc), int(k_prefix.shape[0])))
 
 
 def gqa_prefix_attn(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens, out, lse=None, workspace=None, *,
                     scale: float = 0.0, causal: bool = False, stream=None) -> None:
     """Decode attention behind a shared prefix into ``out`` (and ``lse``); see
     gqa_prefix_attn in ``include/gqa_shared_keys.h``."""
-    _inputs_ok(q, k_cache, v_cache, seqlens)
-    _inputs_ok(q, k_prefix, v_prefix, prefix_len)
+    desc, device = _shared_desc(q, k_cache, out.dtype, scale, causal)
+    if v_cache.shape != k_cache.shape or v_prefix.shape != k_prefix.shape:
+        raise ValueError("k and v shapes differ")
     if k_prefix.dim() != 3 or k_prefix.shape[1:] != k_cache.shape[2:]:
         raise ValueError(f"prefix {tuple(k_prefix.shape)} and cache {tuple(k_cache.shape)} disagree")
-    _lengths_ok("seqlens", seqlens, q.shape[0])
-    _lengths_ok("prefix_len", prefix_len, 1)
-    _outputs_ok(q, out, lse, workspace)
-    device = _check_devices(stream, q=q, k_prefix=k_prefix, v_prefix=v_prefix, prefix_len=prefix_len,
-                            k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, out=out, lse=lse, workspace=workspace)
-    desc = make_desc(q, k_cache, scale=scale, causal=causal, out_dtype=out.dtype)
-    rc = _on_device(device, lambda: lib().gqa_prefix_attn(
-        ctypes.byref(desc), _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), int(k_prefix.shape[0]),
-        _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(out), _ptr(lse), _ptr(workspace), _bytes_of(workspace),
-        _stream(stream)))
-    _check(rc, "gqa_prefix_attn")
+    raw = _check_call(device, q, (k_prefix, v_prefix, k_cache, v_cache), ((prefix_len, 1), (seqlens, desc.batch)), out,
+                      lse, workspace, stream)
+    rc = _on_device(device, lib().gqa_prefix_attn, ctypes.byref(desc), q.data_ptr(), k_prefix.data_ptr(),
+                    v_prefix.data_ptr(), prefix_len.data_ptr(), k_prefix.shape[0], k_cache.data_ptr(),
+                    v_cache.data_ptr(), seqlens.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(workspace),
+                    _bytes_of(workspace), raw)
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_prefix_attn")
 
 
 def _allocate(q, out_dtype, workspace_bytes, stream):
