@@ -169,45 +169,27 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
                 Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NT, S_FULL = Q_EMPTY + NT, P_FULL = S_FULL + 2,
-                O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing;
-  static_assert(ITEM_EMPTY + kItemRing <= 64, "barrier words");
+                O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing,
+                N_BARRIERS = ITEM_EMPTY + kItemRing;
+  static_assert(N_BARRIERS <= 64, "barrier words");
 
   // (a shuffle tells the compiler that it is the same in all the warp)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int n0 = p.plan.s[0].batch, n_entries = n0 + p.plan.s[1].batch;
 
   // ---------------------------------------------------------------- set-up
-  if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < NSK; ++i) {
-      ptx::mbar_init(BAR(K_FULL + i), 1);
-      ptx::mbar_init(BAR(K_EMPTY + i), 1);
+  if (warp == 0) {
+    for (int i = lane; i < N_BARRIERS; i += 32) {
+      uint32_t arrivals = 1;
+      if (i >= P_FULL && i < P_FULL + 2) arrivals = 4;         // the softmax warps of a tile
+      if (i >= ITEM_EMPTY) arrivals = Cfg::kSoftmaxWarps + 2;  // softmax warps, producer, issuer
+      ptx::mbar_init(BAR(i), arrivals);
     }
-    for (uint32_t i = 0; i < NSV; ++i) {
-      ptx::mbar_init(BAR(V_FULL + i), 1);
-      ptx::mbar_init(BAR(V_EMPTY + i), 1);
-    }
-    for (int i = 0; i < NT; ++i) {
-      ptx::mbar_init(BAR(Q_FULL + i), 1);
-      ptx::mbar_init(BAR(Q_EMPTY + i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(BAR(S_FULL + i), 1);
-      ptx::mbar_init(BAR(P_FULL + i), 4);  // one arrival per softmax warp of the tile
-      ptx::mbar_init(BAR(O_FULL + i), 1);
-    }
-    ptx::mbar_init(BAR(DRAIN), 1);
-    for (int i = 0; i < kItemRing; ++i) {
-      ptx::mbar_init(BAR(ITEM_FULL + i), 1);
-      ptx::mbar_init(BAR(ITEM_EMPTY + i), Cfg::kSoftmaxWarps + 2);  // softmax warps, producer, issuer
-    }
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     ptx::fence_barrier_init();
-    for (int i = 0; i < 2; ++i) {
-      if (p.plan.s[i].batch == 0) continue;
-      ptx::prefetch_tensormap(&p.s[i].tm_q);
-      ptx::prefetch_tensormap(&p.s[i].tm_k);
-      ptx::prefetch_tensormap(&p.s[i].tm_v);
-    }
+  } else if (warp == kProducerWarp && lane < 6 && p.plan.s[lane / 3].batch != 0) {
+    const RowsSection& s = p.s[lane / 3];
+    ptx::prefetch_tensormap(lane % 3 == 0 ? &s.tm_q : lane % 3 == 1 ? &s.tm_k : &s.tm_v);
   }
   __syncwarp();
   if (warp == kMmaWarp) {
@@ -600,7 +582,11 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         if ((blk + 1) * kBlockN > it.L - causal_cut) {
           const int seen = sees - blk * kBlockN < tail ? sees - blk * kBlockN : tail;
 #pragma unroll
-          for (int j = 0; j < 128; ++j) x[j] = j < seen ? x[j] : 0xff800000u;  // -inf
+          for (int c = 0; c < 128; c += 32) {
+            if (!__any_sync(0xffffffffu, seen < c + 32)) continue;
+#pragma unroll
+            for (int j = c; j < c + 32; ++j) x[j] = j < seen ? x[j] : 0xff800000u;  // -inf
+          }
         }
 
         float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3])};
@@ -712,30 +698,26 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         }
       };
 #pragma unroll 1
-      for (int c = 0; c < HEAD_DIM / 32; ++c) {
-        uint32_t o[32];
+      for (int c = 0; c < HEAD_DIM / 16; ++c) {  // 16 columns at a time
+        float o[16];
         if (!empty) {
-          ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+          ptx::tmem_ld_32x32b_x16(o_addr + 16 * c, o);
           ptx::tmem_wait_ld();
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = empty ? 0u : __float_as_uint(inv == 0.f ? 0.f : __uint_as_float(o[j]) * inv);
+        for (int j = 0; j < 16; ++j) o[j] = empty || inv == 0.f ? 0.f : o[j] * inv;
         if (store) {
+          uint32_t v[8];
           if (out16) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t v[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = pack16(__uint_as_float(o[16 * q + 2 * j]), __uint_as_float(o[16 * q + 2 * j + 1]));
-              put(dst + 64 * c + 32 * q, v);
-            }
+            for (int j = 0; j < 8; ++j) v[j] = pack16(o[2 * j], o[2 * j + 1]);
+            put(dst + 32 * c, v);
           } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t v[8];
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = o[8 * q + j];
-              put(dst + 128 * c + 32 * q, v);
+              for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(o[8 * q + j]);
+              put(dst + 64 * c + 32 * q, v);
             }
           }
         }
