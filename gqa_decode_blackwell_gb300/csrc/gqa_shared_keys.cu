@@ -25,8 +25,8 @@ namespace {
 // Up to this many rows a merge gives each a CTA, whose warps share its pieces.
 constexpr size_t kMergeSharedRows = 1024;
 
-constexpr int kTwoTileShift = 2, kOneTileShift = 1, kItemUnits = 4;
-constexpr int kLeastUnits = 8;  // of a CTA: below that, starting one costs more than it saves
+constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kItemUnits = 16;
+constexpr int kLeastUnits = 20;  // of a CTA: below that, starting one costs more than it saves
 
 int group_of(const gqa_desc_t* d) { return d->q_heads / d->kv_heads; }
 int tiles_of(int head_dim) { return head_dim == 256 ? 1 : 2; }
@@ -84,7 +84,7 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     ps.batch = d.batch;
     ps.heads = static_cast<int>(heads);
     ps.max_len = d.max_seqlen;
-    ps.block_shift = s.split_keys || tiles == 1 ? kOneTileShift : kTwoTileShift;
+    ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits : kTwoTileUnits;
     ps.item_units = kItemUnits;
     entries += d.batch;
     units += static_cast<long long>(s.triples) * rows_units(ps, d.max_seqlen);

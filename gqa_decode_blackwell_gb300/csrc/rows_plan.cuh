@@ -32,7 +32,7 @@ struct RowsPlanSection {
   int batch;        // entries (0: no such section)
   int heads;        // triples of an entry
   int max_len;      // lengths are clamped to [0, max_len]
-  int block_shift;  // a block takes 1 << block_shift units
+  int block_units;  // of a block
   int item_units;
 };
 
@@ -52,7 +52,7 @@ struct RowsWork {
 
 GQA_HD int rows_units(const RowsPlanSection& s, int L) {
   const int nblk = num_blocks(L);
-  return nblk > 0 ? (nblk << s.block_shift) + s.item_units : 0;
+  return nblk > 0 ? nblk * s.block_units + s.item_units : 0;
 }
 
 struct RowsPlanIter {
@@ -81,8 +81,8 @@ struct RowsPlanIter {
     if (rp->dealt) return;
     const int E = rp->s[0].batch + rp->s[1].batch;
     U = pre[E];
-    const int w0 = rp->s[0].block_shift, w1 = rp->s[1].block_shift;
-    const uint32_t most = U >> (w0 > w1 ? w0 : w1);  // ranges at least a block long
+    const uint32_t w0 = static_cast<uint32_t>(rp->s[0].block_units), w1 = static_cast<uint32_t>(rp->s[1].block_units);
+    const uint32_t most = U / (w0 > w1 ? w0 : w1);  // ranges at least a block long
     C = most < 1 ? 1 : (most < static_cast<uint32_t>(rp->num_ctas) ? most : static_cast<uint32_t>(rp->num_ctas));
     q = U / C;
     rem = U - q * C;
@@ -150,12 +150,11 @@ struct RowsPlanIter {
       } else {
         if (v >= hi) return false;
         const uint32_t nblk = static_cast<uint32_t>(num_blocks(lens[e]));
-        const int sh = s.block_shift;
-        const uint32_t up = (1u << sh) - 1u;
+        const uint32_t bu = static_cast<uint32_t>(s.block_units);
         const uint32_t first = v + static_cast<uint32_t>(s.item_units);  // where block 0 begins
-        const uint32_t last = first + ((nblk - 1) << sh);                 // and the last one
-        const uint32_t from = lo > first ? (lo - first + up) >> sh : 0;
-        const uint32_t upto = hi > last ? nblk : (hi > first ? (hi - first + up) >> sh : 0);
+        const uint32_t last = first + (nblk - 1) * bu;                    // and the last one
+        const uint32_t from = lo > first ? (lo - first + bu - 1) / bu : 0;
+        const uint32_t upto = hi > last ? nblk : (hi > first ? (hi - first + bu - 1) / bu : 0);
         if (from < upto) {
           const bool whole = from == 0 && upto == nblk;
           emit(w, static_cast<int>(from), static_cast<int>(upto), whole,
