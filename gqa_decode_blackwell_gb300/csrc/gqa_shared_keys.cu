@@ -26,6 +26,7 @@ namespace {
 constexpr size_t kMergeSharedRows = 1024;
 
 constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kItemUnits = 16;
+constexpr int kRecordUnits = 1, kZerosUnits = 6;  // of a triple without keys: its record, or its zeros
 constexpr int kLeastUnits = 20;  // of a CTA: below that, starting one costs more than it saves
 
 int group_of(const gqa_desc_t* d) { return d->q_heads / d->kv_heads; }
@@ -86,6 +87,7 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     ps.max_len = d.max_seqlen;
     ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits : kTwoTileUnits;
     ps.item_units = kItemUnits;
+    ps.empty_units = r.every_piece ? kRecordUnits : kZerosUnits;
     entries += d.batch;
     units += static_cast<long long>(s.triples) * rows_units(ps, d.max_seqlen);
   }
@@ -186,7 +188,6 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
     s.groups = r.s[i].groups;
     s.split_keys = r.s[i].split_keys;
     s.causal = d.causal != 0 ? 1 : 0;
-    s.triples = r.s[i].triples;
   }
   p.plan = r.plan;
   const RowsWs w = rows_ws(r);

@@ -13,8 +13,9 @@
 //
 // A tile's rows are the G query heads of T = 128 / G consecutive query tokens
 // (row t*G + g), so one TMA box brings them and the heads of a KV head share
-// its keys.  Rows past T*G, and tokens past the last one, hold zeros and are
-// never written out.
+// its keys.  Tokens past the last one are zeros, rows past T*G whatever was
+// there before; a row of the MMA reaches no other row, and neither is ever
+// written out.
 //
 // Warps: 4 softmax warps per tile, then one TMA producer, one MMA issuer and
 // one that walks the plan and hands the others their items through a ring in
@@ -68,7 +69,6 @@ struct RowsSection {
   int groups;           // tile groups of an entry: triples are h * groups + group
   int split_keys;       // both tiles hold the same rows
   int causal;           // token t sees keys j <= L - nq + t
-  int triples;          // of the section
 };
 
 struct RowsParams {
@@ -103,8 +103,7 @@ struct RowsItem {
   int piece;              // where its partials go; -1: final output
 };
 constexpr int kItemRing = 4;
-constexpr uint64_t kBlockNs = 20000;       // far more than a key block of an item takes
-constexpr uint32_t kPlanSuspendNs = 1000;  // the plan walker is ahead: its waits may sleep
+constexpr uint64_t kBlockNs = 20000;  // far more than a key block of an item takes
 
 template <int HEAD_DIM>
 struct RowsCfg {
@@ -439,7 +438,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       int longest = 0;              // blocks of the longest item so far
       RowsPlanIter iter;
       iter.init(&p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
-      for (uint32_t n = 0; ok; ++n) {
+      for (uint32_t n = 0; ok;) {
         RowsWork w;
         const bool more = iter.next(w);
         RowsItem it;
@@ -466,18 +465,21 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             else if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + s.rec + triple, sizeof(int2)))
               p.rec[s.rec + triple] = make_int2(it.piece, n_pieces);
           }
+          // no keys and partials only: its record says all (dealt triples are handed on all the same, so that
+          // no role waits for the walk over a long run of them)
+          if (n_pieces == 0 && first_piece && p.every_piece != 0 && p.plan.dealt == 0) continue;
         }
         const int i = static_cast<int>(n % kItemRing);
         // as long as the items in the ring may take
         if (n >= kItemRing)
           ok = ptx::mbar_wait_bounded(BAR(ITEM_EMPTY + i), ((n / kItemRing) & 1u) ^ 1u, abort_flag,
-                                      p.timeout_ns + static_cast<uint64_t>(longest) * kItemRing * kBlockNs,
-                                      kPlanSuspendNs);
+                                      p.timeout_ns + static_cast<uint64_t>(longest) * kItemRing * kBlockNs);
         if (it.blk_end - it.blk_begin > longest) longest = it.blk_end - it.blk_begin;
         if (!ok) break;
         items_ring[i] = it;
         ptx::mbar_arrive(BAR(ITEM_FULL + i));
         if (!more) break;
+        ++n;
       }
       if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
       // after a timeout too, so that the merge never reads what an earlier call left

@@ -6,7 +6,8 @@
 // the entry's key blocks.  The sections' triples, in order, are laid along a
 // line of units: a triple with blocks takes item_units for its fixed cost (Q
 // load, pipeline fill, epilogue) and then block_units for every block; one
-// without takes none.  The U units are cut into C ranges of equal length (give
+// without takes empty_units (zeros to write, or only a record), so that a
+// batch's empty entries are spread like its work.  The U units are cut into C ranges of equal length (give
 // or take one unit), one per CTA, and a block belongs to the CTA in whose range
 // it begins.  A range is never shorter than a block, so the CTAs that hold a
 // triple's blocks are consecutive and each holds at least one.
@@ -34,6 +35,7 @@ struct RowsPlanSection {
   int max_len;      // lengths are clamped to [0, max_len]
   int block_units;  // of a block
   int item_units;
+  int empty_units;  // of a triple without blocks
 };
 
 struct RowsPlan {
@@ -52,7 +54,7 @@ struct RowsWork {
 
 GQA_HD int rows_units(const RowsPlanSection& s, int L) {
   const int nblk = num_blocks(L);
-  return nblk > 0 ? nblk * s.block_units + s.item_units : 0;
+  return nblk > 0 ? nblk * s.block_units + s.item_units : s.empty_units;
 }
 
 struct RowsPlanIter {
@@ -100,10 +102,8 @@ struct RowsPlanIter {
       if (pre[mid + 1] > lo || pre[mid] >= lo) z = mid; else a = mid + 1;
     }
     e = a;
-    if (e < E && pre[e] < lo) {
-      const int u = rows_units(section(e), lens[e]);
-      if (u > 0) hh = static_cast<int>((lo - pre[e]) / static_cast<uint32_t>(u));
-    }
+    if (e < E && pre[e] < lo)
+      hh = static_cast<int>((lo - pre[e]) / static_cast<uint32_t>(rows_units(section(e), lens[e])));
   }
   GQA_HD void emit(RowsWork& w, int blk_begin, int blk_end, int whole, int pieces) {
     w.section = e < rp->s[0].batch ? 0 : 1;
@@ -139,17 +139,15 @@ struct RowsPlanIter {
       const RowsPlanSection& s = section(e);
       const uint32_t u = static_cast<uint32_t>(rows_units(s, lens[e]));
       const uint32_t v = pre[e] + static_cast<uint32_t>(hh) * u;
+      if (v >= hi) return false;
+      const uint32_t nblk = static_cast<uint32_t>(num_blocks(lens[e]));
       bool mine = false;
-      if (u == 0) {
-        if ((v >= lo && v < hi) || (v == U && static_cast<uint32_t>(cta) == C - 1)) {
+      if (nblk == 0) {
+        if (v >= lo) {
           emit(w, 0, 0, 1, 1);
           mine = true;
-        } else if (v >= hi) {
-          return false;
         }
       } else {
-        if (v >= hi) return false;
-        const uint32_t nblk = static_cast<uint32_t>(num_blocks(lens[e]));
         const uint32_t bu = static_cast<uint32_t>(s.block_units);
         const uint32_t first = v + static_cast<uint32_t>(s.item_units);  // where block 0 begins
         const uint32_t last = first + (nblk - 1) * bu;                    // and the last one

@@ -217,6 +217,19 @@ def test_plan_covers_every_block_once(lens, nq, Hq, Hkv, d, s_max, sm):
         assert max(load.values()) - min(load.values()) <= 6   # equal ranges, but for the items' fixed cost
 
 
+@pytest.mark.parametrize("lens,nq,prefix", [([0] * 256, 1, (32768, 32768)), ([300] * 128 + [0] * 384, 1, (0, 4096)),
+                                            ([0] * 512, 200, None), ([900] * 8 + [0] * 500, 200, None)])
+def test_entries_without_keys_are_spread(lens, nq, prefix):
+    """A padded batch's empty entries are dealt over the CTAs, not left to one of them."""
+    desc = _desc(batch=len(lens), q_tokens=nq, q_heads=32, kv_heads=4, head_dim=128, max_seqlen=1024)
+    ctas, _, _, items = g.gqa_shared_keys_plan(desc, lens, *(prefix or (0, 0)), 152)
+    empty = np.bincount(items[items[:, 5] == items[:, 6], 0], minlength=ctas)
+    # a CTA's share of the line is U / ctas units, and an empty triple takes at least one of them
+    blocks = int((items[:, 6] - items[:, 5]).sum())
+    units = 7 * blocks + 16 * len(items) + 6 * int(empty.sum())
+    assert int(empty.max()) <= -(-units // ctas)
+
+
 @pytest.mark.parametrize("sm", [1, 7, 152])
 @pytest.mark.parametrize("lens,nq,Hq,Hkv,d,s_max,prefix", [
     ([5, 700, 0, 128], 1, 8, 2, 128, 700, (1000, 1024)), ([300] * 128, 1, 64, 8, 128, 2048, (32768, 32768)),
