@@ -19,15 +19,19 @@
 namespace gqa {
 namespace {
 
-// Units of the plan's line (rows_plan.cuh): a key block against two tiles of
-// rows, against one, and a triple's fixed cost -- Q load, pipeline fill,
-// epilogue.
-// Up to this many rows a merge gives each a CTA, whose warps share its pieces.
+// Units of the plan's line (rows_plan.cuh), of ~0.25 us: a key block against
+// two tiles of rows (~1.7 us) and against one (~1), a triple's fixed cost --
+// Q load, pipeline fill, epilogue -- and writing the zeros of one without
+// keys.  Measured on GB300 at head_dim 128: 128 sequences behind 32768 shared
+// keys take 199 us with 7 / 4 / 16 and 236 us with equal costs for both kinds
+// of block and 4 for a triple; 64 prompts of 200 tokens, 60 of them without
+// keys, 35 us with 6 units for those and 39 us with 10.
+constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kItemUnits = 16, kZerosUnits = 6;
+// Up to this many rows a merge gives each a CTA, whose warps share its pieces;
+// beyond, a warp to a row.  Measured on GB300, a whole call: 384 rows of 256
+// 28.2 us (33.3 with a warp each), 1024 rows of 128 the same both ways, 2048
+// rows of 64 30.9 us (25.8).
 constexpr size_t kMergeSharedRows = 1024;
-
-constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kItemUnits = 16;
-constexpr int kRecordUnits = 1, kZerosUnits = 6;  // of a triple without keys: its record, or its zeros
-constexpr int kLeastUnits = 20;  // of a CTA: below that, starting one costs more than it saves
 
 int group_of(const gqa_desc_t* d) { return d->q_heads / d->kv_heads; }
 int tiles_of(int head_dim) { return head_dim == 256 ? 1 : 2; }
@@ -87,7 +91,7 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     ps.max_len = d.max_seqlen;
     ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits : kTwoTileUnits;
     ps.item_units = kItemUnits;
-    ps.empty_units = r.every_piece ? kRecordUnits : kZerosUnits;
+    ps.empty_units = r.every_piece ? 0 : kZerosUnits;
     entries += d.batch;
     units += static_cast<long long>(s.triples) * rows_units(ps, d.max_seqlen);
   }
@@ -97,7 +101,11 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     const long long triples = static_cast<long long>(r.s[0].triples) + r.s[1].triples;
     if (triples < ctas) ctas = triples;
   } else {
-    const long long most = units / kLeastUnits;
+    // a CTA per block at most (RowsPlanIter: ranges at least a block long):
+    // 4 rows of a 64-element head behind 512 keys take 10.0 us so, and 12.7
+    // with half as many
+    const int w0 = r.plan.s[0].block_units, w1 = r.plan.s[1].block_units;
+    const long long most = units / (w0 > w1 ? w0 : w1);
     if (most < ctas) ctas = most < 1 ? 1 : most;
   }
   r.plan.num_ctas = static_cast<int>(ctas);
@@ -404,22 +412,30 @@ gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int ma
       pre.push_back(pre.back() + static_cast<uint32_t>(s.heads) * static_cast<uint32_t>(rows_units(s, lens.back())));
     }
   int64_t n = 0;
+  auto list = [&](int c, const RowsWork& w) {
+    if (items != nullptr && n < max_items) {
+      int32_t* o = items + 9 * n;
+      const int groups = r.s[w.section].groups, triple = w.b * r.plan.s[w.section].heads + w.hh;
+      const bool partial = r.every_piece || w.whole == 0, keys = w.blk_begin < w.blk_end;
+      o[0] = c; o[1] = w.section; o[2] = w.b; o[3] = w.hh / groups; o[4] = w.hh % groups;
+      o[5] = w.blk_begin; o[6] = w.blk_end;
+      o[7] = partial && keys ? rows_piece(r.every_piece, r.plan.dealt != 0, triple, c, w.blk_begin == 0) : -1;
+      o[8] = keys ? w.n_pieces : 0;
+    }
+    ++n;
+  };
   for (int c = 0; c < r.plan.num_ctas; ++c) {
     RowsPlanIter it;
     it.init(&r.plan, raw[0], raw[1], lens.data(), pre.data(), c);
     RowsWork w;
-    while (it.next(w)) {
-      if (items != nullptr && n < max_items) {
-        int32_t* o = items + 9 * n;
-        const int groups = r.s[w.section].groups, triple = w.b * r.plan.s[w.section].heads + w.hh;
-        const bool partial = r.every_piece || w.whole == 0;
-        o[0] = c; o[1] = w.section; o[2] = w.b; o[3] = w.hh / groups; o[4] = w.hh % groups;
-        o[5] = w.blk_begin; o[6] = w.blk_end;
-        o[7] = partial ? rows_piece(r.every_piece, r.plan.dealt != 0, triple, c, w.blk_begin == 0) : -1;
-        o[8] = w.blk_begin < w.blk_end ? w.n_pieces : 0;
-      }
-      ++n;
-    }
+    while (it.next(w)) list(c, w);
+  }
+  for (int e = 0; e < static_cast<int>(lens.size()) && r.every_piece && !r.plan.dealt; ++e) {
+    RowsWork w;
+    std::memset(&w, 0, sizeof w);
+    w.section = e < r.plan.s[0].batch ? 0 : 1;
+    w.b = e - (w.section ? r.plan.s[0].batch : 0);
+    for (; lens[e] == 0 && w.hh < r.plan.s[w.section].heads; ++w.hh) list(empty_owner(r.plan, e), w);
   }
   if (num_items) *num_items = n;
   return GQA_OK;

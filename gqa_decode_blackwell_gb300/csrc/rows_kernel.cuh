@@ -209,6 +209,17 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (p.every_piece != 0 && p.plan.dealt == 0) {
+    // the records of entries without keys, which the plan does not list: one
+    // thread of this kernel, an item at a time, takes ~0.5 us for each
+    for (int i = blockIdx.x; i < n_entries; i += p.plan.num_ctas) {  // empty_owner
+      if (s_len[i] > 0) continue;
+      const int sec = i < n0 ? 0 : 1, heads = p.plan.s[sec].heads;
+      int2* rec = p.rec + p.s[sec].rec + static_cast<long long>(i - (sec ? n0 : 0)) * heads;
+      for (int hh = threadIdx.x; hh < heads; hh += Cfg::kThreads)
+        if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, rec + hh, sizeof(int2))) rec[hh] = make_int2(-1, 0);
+    }
+  }
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -438,7 +449,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       int longest = 0;              // blocks of the longest item so far
       RowsPlanIter iter;
       iter.init(&p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
-      for (uint32_t n = 0; ok;) {
+      for (uint32_t n = 0; ok; ++n) {
         RowsWork w;
         const bool more = iter.next(w);
         RowsItem it;
@@ -465,9 +476,6 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             else if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + s.rec + triple, sizeof(int2)))
               p.rec[s.rec + triple] = make_int2(it.piece, n_pieces);
           }
-          // no keys and partials only: its record says all (dealt triples are handed on all the same, so that
-          // no role waits for the walk over a long run of them)
-          if (n_pieces == 0 && first_piece && p.every_piece != 0 && p.plan.dealt == 0) continue;
         }
         const int i = static_cast<int>(n % kItemRing);
         // as long as the items in the ring may take
@@ -479,7 +487,6 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         items_ring[i] = it;
         ptx::mbar_arrive(BAR(ITEM_FULL + i));
         if (!more) break;
-        ++n;
       }
       if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
       // after a timeout too, so that the merge never reads what an earlier call left

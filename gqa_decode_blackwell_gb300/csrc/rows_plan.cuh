@@ -6,8 +6,9 @@
 // the entry's key blocks.  The sections' triples, in order, are laid along a
 // line of units: a triple with blocks takes item_units for its fixed cost (Q
 // load, pipeline fill, epilogue) and then block_units for every block; one
-// without takes empty_units (zeros to write, or only a record), so that a
-// batch's empty entries are spread like its work.  The U units are cut into C ranges of equal length (give
+// without takes empty_units for the zeros to write, so that a batch's empty
+// entries are spread like its work -- or none and is not listed, where all
+// there is to write is a record (empty_owner).  The U units are cut into C ranges of equal length (give
 // or take one unit), one per CTA, and a block belongs to the CTA in whose range
 // it begins.  A range is never shorter than a block, so the CTAs that hold a
 // triple's blocks are consecutive and each holds at least one.
@@ -35,7 +36,7 @@ struct RowsPlanSection {
   int max_len;      // lengths are clamped to [0, max_len]
   int block_units;  // of a block
   int item_units;
-  int empty_units;  // of a triple without blocks
+  int empty_units;  // of a triple without blocks; 0: such triples are not listed
 };
 
 struct RowsPlan {
@@ -143,7 +144,7 @@ struct RowsPlanIter {
       const uint32_t nblk = static_cast<uint32_t>(num_blocks(lens[e]));
       bool mine = false;
       if (nblk == 0) {
-        if (v >= lo) {
+        if (u > 0 && v >= lo) {
           emit(w, 0, 0, 1, 1);
           mine = true;
         }
@@ -166,6 +167,10 @@ struct RowsPlanIter {
     return false;
   }
 };
+
+// The CTA that records the triples of entry e (of both sections) that has no
+// keys, in launches that do not list those.
+GQA_HD int empty_owner(const RowsPlan& p, int e) { return e % p.num_ctas; }
 
 // Where a piece's partials go: indexes of pieces that no two pieces of a
 // section share.  every_piece: triple + CTA (both grow along the line, never

@@ -223,11 +223,13 @@ def test_entries_without_keys_are_spread(lens, nq, prefix):
     """A padded batch's empty entries are dealt over the CTAs, not left to one of them."""
     desc = _desc(batch=len(lens), q_tokens=nq, q_heads=32, kv_heads=4, head_dim=128, max_seqlen=1024)
     ctas, _, _, items = g.gqa_shared_keys_plan(desc, lens, *(prefix or (0, 0)), 152)
-    empty = np.bincount(items[items[:, 5] == items[:, 6], 0], minlength=ctas)
-    # a CTA's share of the line is U / ctas units, and an empty triple takes at least one of them
-    blocks = int((items[:, 6] - items[:, 5]).sum())
-    units = 7 * blocks + 16 * len(items) + 6 * int(empty.sum())
-    assert int(empty.max()) <= -(-units // ctas)
+    empty = items[items[:, 5] == items[:, 6]]
+    if prefix:   # records of whole entries, in turn
+        most, share = np.bincount(np.unique(empty[:, :3], axis=0)[:, 0]).max(), (len(lens) + 1) / ctas
+    else:        # of the plan's line, on which a triple takes 6 units, with keys 16 and 7 a block
+        most = np.bincount(empty[:, 0]).max()
+        share = (6 * len(empty) + 16 * (len(items) - len(empty)) + 7 * (items[:, 6] - items[:, 5]).sum()) / ctas / 6
+    assert most <= math.ceil(share)
 
 
 @pytest.mark.parametrize("sm", [1, 7, 152])
