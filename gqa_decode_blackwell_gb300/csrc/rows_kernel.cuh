@@ -551,11 +551,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           // V rows past the end hold whatever the buffer holds there; zero
           // them (up to the capacity, past which TMA wrote zeros) so that
           // 0 * garbage cannot reach O.  One tile's warps do it, before their
-          // P lets the issuer start on this V.  The parity wait is sound: a
+          // P lets the issuer start on this V; 8 lanes to a row (a row each
+          // would have all 32 on the same banks).  The parity wait is sound: a
           // complete S says that every PV issued before it has landed, among
           // them the one that read the stage's V before (one tile: that is
           // PV(g-1), issued after this S, and waited for).
-          const int cap = p.plan.s[it.section].max_len - blk * kBlockN;
+          const int cap = min(p.plan.s[it.section].max_len - blk * kBlockN, kBlockN);
           if ((t == 0 || split_keys) && cap > tail) {
             if constexpr (NT == 1) {
               if (g >= 1 && !wait_pv(g - 1)) break;
@@ -564,13 +565,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             for (int hf = 0; hf < TPB; ++hf) {
               const uint32_t n = (u0 + static_cast<uint32_t>(i)) * TPB + hf, stage = n % NSV;
               if (!wait(V_FULL + static_cast<int>(stage), n / NSV)) break;
-              if (r >= tail && r < cap) {
+              uint8_t* z = vring + stage * Cfg::kStageBytes + (lane & 7) * 16;
+#pragma unroll 1
+              for (int row = tail + (warp & 3) * 4 + (lane >> 3); row < cap; row += 16) {
 #pragma unroll
-                for (int kc = 0; kc < TCH; ++kc) {
-                  uint4* z = reinterpret_cast<uint4*>(vring + stage * Cfg::kStageBytes + kc * 16384 + r * 128);
-#pragma unroll
-                  for (int c = 0; c < 8; ++c) z[c] = make_uint4(0, 0, 0, 0);
-                }
+                for (int kc = 0; kc < TCH; ++kc)
+                  *reinterpret_cast<uint4*>(z + kc * 16384 + row * 128) = make_uint4(0, 0, 0, 0);
               }
             }
             if (!ok) break;
