@@ -20,13 +20,14 @@ namespace gqa {
 namespace {
 
 // Units of the plan's line (rows_plan.cuh), of ~0.25 us: a key block against
-// two tiles of rows (~1.7 us) and against one (~1), a triple's fixed cost --
-// Q load, pipeline fill, epilogue -- and writing the zeros of one without
-// keys.  Measured on GB300 at head_dim 128: 128 sequences behind 32768 shared
+// two tiles of rows (~1.7 us), against one in turn with the next block (~1) and
+// against one alone, a triple's fixed cost -- Q load, pipeline fill, epilogue
+// -- and writing the zeros of one without keys.  Measured on GB300 at head_dim 128: 128 sequences behind 32768 shared
 // keys take 199 us with 7 / 4 / 16 and 236 us with equal costs for both kinds
-// of block and 4 for a triple; 64 prompts of 200 tokens, 60 of them without
+// of block and 4 for a triple; 32 sequences of up to 512 keys behind 4000 31.7
+// us with 6 for the prefix's lone tiles and 37 us with 4; 64 prompts of 200 tokens, 60 of them without
 // keys, 35 us with 6 units for those and 39 us with 10.
-constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kItemUnits = 16, kZerosUnits = 6;
+constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kLoneTileUnits = 6, kItemUnits = 16, kZerosUnits = 6;
 // Up to this many rows a merge gives each a CTA, whose warps share its pieces;
 // beyond, a warp to a row.  Measured on GB300, a whole call: 384 rows of 256
 // 28.2 us (33.3 with a warp each), 1024 rows of 128 the same both ways, 2048
@@ -37,9 +38,24 @@ int group_of(const gqa_desc_t* d) { return d->q_heads / d->kv_heads; }
 int tiles_of(int head_dim) { return head_dim == 256 ? 1 : 2; }
 
 // Few rows fit the decode kernel, which puts the keys along the MMA's M
-// dimension and streams them with a 16- or 32-column tile.
+// dimension and streams them with a 16- or 32-column tile.  Measured on GB300
+// (decode kernel, rows kernel): 8 x 8 KV heads of 4096 keys, 4 rows 23.0 and
+// 31.4 us, 32 rows 27.1 and 33.6; 8 KV heads of 512 keys, 32 rows 10.8 and
+// 10.3; 64 x 8 of 1000 keys, 32 rows 58.1 and 64.6.
 bool few_rows(const gqa_desc_t* d) {
   return static_cast<long long>(d->q_tokens) * group_of(d) <= GQA_MAX_QROWS;
+}
+
+// Rows that fit one tile are given to both tiles, with the key blocks in turn:
+// the softmax of one runs under the other's MMAs.  At head_dim 128 a full tile
+// is better left alone, since each piece then writes, and the merge reads, half
+// as much, and its blocks come no faster than memory brings them.  Measured on
+// GB300 (split, not split): 2 x 8 triples of 128 rows of 128, 4096 keys 23.6
+// and 20.8 us, 32768 keys 61.4 and 58.8; of 64 rows 19.6 and 20.4, 56.2 and
+// 57.8; 4 x 4 triples of 128 rows of 64, 16384 keys 27.8 and 31.9.
+bool split_keys(const gqa_desc_t& d, int tiles) {
+  const int G = group_of(&d), tokens = kTileRows / G;
+  return tiles == 2 && d.q_tokens <= tokens && (d.head_dim == 64 || d.q_tokens * G <= kTileRows / 2);
 }
 
 // One launch of the rows kernel: its sections, its plan and where each
@@ -71,14 +87,14 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
   r.d[0] = *d0;
   if (d1 != nullptr) r.d[1] = *d1;
   const int tiles = tiles_of(d0->head_dim), G = group_of(d0), most_tokens = kTileRows / G;
-  // Rows that fit one tile are given to both, with the keys in turn; every
-  // triple then leaves partials.  So do all triples of a prefix's launch.
+  // Triples of rows that fit one tile all leave partials, and so do all triples
+  // of a prefix's launch.
   r.every_piece = r.n == 2 || r.d[0].q_tokens <= most_tokens;
   long long entries = 0, units = 0;
   for (int i = 0; i < r.n; ++i) {
     const gqa_desc_t& d = r.d[i];
     auto& s = r.s[i];
-    s.split_keys = tiles == 2 && d.q_tokens <= most_tokens ? 1 : 0;
+    s.split_keys = split_keys(d, tiles) ? 1 : 0;
     s.tokens = d.q_tokens < most_tokens ? d.q_tokens : most_tokens;
     const int per_group = (s.split_keys ? 1 : tiles) * s.tokens;
     s.groups = (d.q_tokens - 1) / per_group + 1;
@@ -89,7 +105,9 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     ps.batch = d.batch;
     ps.heads = static_cast<int>(heads);
     ps.max_len = d.max_seqlen;
-    ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits : kTwoTileUnits;
+    ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits
+                     : d.q_tokens <= most_tokens ? kLoneTileUnits
+                                                 : kTwoTileUnits;
     ps.item_units = kItemUnits;
     ps.empty_units = r.every_piece ? 0 : kZerosUnits;
     entries += d.batch;

@@ -148,7 +148,7 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
 // Rows a warp of the cut triples' merge takes at once: most of those have two
 // pieces, and two pieces of one row are too little to have in flight.
 template <int HEAD_DIM>
-constexpr int kCutRows = HEAD_DIM == 256 ? 2 : 4;
+constexpr int kCutRows = HEAD_DIM == 256 ? 1 : 4;
 
 // The cut triples of a launch of one section: blockIdx.x is the CTA of that
 // launch in which a cut triple may begin, blockIdx.y a group of its rows.

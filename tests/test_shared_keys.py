@@ -182,7 +182,7 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix=None):
     total = 0
     for sec, (sec_lens, tokens_in, cap) in enumerate(sections):
         tokens, groups, split, _ = info[sec].tolist()
-        assert tokens == min(tokens_in, 128 // G) and split == (tiles == 2 and tokens_in <= 128 // G)
+        assert tokens == min(tokens_in, 128 // G) and split == (tiles == 2 and tokens_in <= 128 // G and (d == 64 or tokens_in * G <= 64))
         assert groups == -(-tokens_in // (tokens * (1 if split else tiles)))
         total += len(sec_lens) * Hkv * groups
     assert len(by_triple) == total
@@ -339,6 +339,8 @@ CROSS = [  # B, T, H, K, d, S, lens, dtype, out dtype
     (1, 40, 2, 2, 128, 128, [77], BF16, None),                   # one block for the two tiles
     (3, 200, 6, 2, 128, 2000, [2000, 129, 0], BF16, None),       # cut triples of both tiles, and a half-empty last
     (40, 40, 4, 1, 64, 200, [(i * 13) % 201 for i in range(40)], BF16, None),
+    (2, 32, 32, 8, 128, 1300, [1300, 257], BF16, None),          # one full tile: its keys are not split
+    (3, 16, 32, 8, 128, 1300, [1300, 0, 129], FP16, FP32),       # half a tile: they are
 ]
 
 
