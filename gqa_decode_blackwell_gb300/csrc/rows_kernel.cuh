@@ -24,12 +24,25 @@
 // max and sum need no exchange, P goes back into the TMEM columns of its S
 // (16-bit, the value MMA's A operand) and never passes through shared memory.
 //   head_dim 64, 128: two tiles; one's softmax runs under the other's MMAs.
-//     They are 256 rows that share each K/V block, or, where 128 rows hold
-//     all the query rows there are, the same rows with the key blocks dealt to
-//     them in turn ("split keys"): each then leaves a partial of its own.
+//     They are 256 rows that share each K/V block, or, where few rows are all
+//     there are, the same rows with the key blocks dealt to them in turn
+//     ("split keys"): each then leaves a partial of its own.
 //   head_dim 256: O takes half of TMEM, so there is one tile, with two S
 //     slots: the next block's QK runs under this block's softmax.  K and V
 //     blocks are two ring tiles each, their 128-element d-halves.
+//
+// What bounds it, measured on GB300 (bf16): at head_dim 128 a step of two
+// tiles takes ~3300 cycles, in which the tensor core works for 2048, the
+// exponential units for 1024 and shared memory for ~2048 (Q and K at QK, V at
+// PV, the next blocks' arrival).  S, softmax, P and PV of a tile are a chain,
+// and two tiles' S and O fill TMEM, so the gaps of one are filled by the other
+// alone: 2048 tokens of 32 heads against 8192 keys, 4 of them, run at 1.35
+// PFLOP/s (800 us).  At head_dim 256 the one tile takes its K and V, 64 bytes
+// a clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of
+// 16 heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
+// few, a block costs what its chain takes (~1900 cycles, split between two
+// tiles) and an item ~5600 more; a CTA starts its first K load after ~4 us,
+// most of it code fetched for the first time.
 //
 // The running max is only replaced when it grows by more than 8 (log2 units),
 // as in the decode kernel; a warp whose rows need it rescales its own lanes
@@ -121,7 +134,8 @@ struct RowsCfg {
   // Two tiles: three warpgroups (softmax, softmax, and the other roles with an
   // idle warp), so that registers can move from the third to the softmax
   // warps, which hold a row of 128 scores each: 384 threads x 168 at launch =
-  // 256 x 208 + 128 x 88.  One tile: 224 threads have registers enough.
+  // 256 x 208 + 128 x 88 (with 168 for all and the plan walked by every role,
+  // rows spilled: long prompts took 1230 us, 905 since).  One tile: 224 threads have registers enough.
   static constexpr bool kMoveRegs = kTiles == 2;
   static constexpr int kThreads = kMoveRegs ? 384 : 224;
   static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kControlRegs = 88;

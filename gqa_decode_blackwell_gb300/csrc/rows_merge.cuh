@@ -8,7 +8,9 @@
 // from run to run.  A warp keeps a running maximum and sum over a row's pieces,
 // whose LSEs and values it loads a batch at a time, all of them before the
 // first is used: what bounds the merge is how much it has in flight, not its
-// arithmetic.  A lane owns HEAD_DIM / 32 consecutive elements.  The values of a
+// arithmetic (loads of one piece at a time: prompts of 256 tokens 115 us a call,
+// not 94; the merge alone takes 12 us there for 80 MB of partials, and 13 for
+// the 8192 rows of 128 sequences behind a prefix).  A lane owns HEAD_DIM / 32 consecutive elements.  The values of a
 // piece with lse_s = -inf may be anything (they are not written) and take no
 // part.
 #pragma once
@@ -146,7 +148,8 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
 }  // namespace detail
 
 // Rows a warp of the cut triples' merge takes at once: most of those have two
-// pieces, and two pieces of one row are too little to have in flight.
+// pieces, and two pieces of one short row are little to have in flight (prompts
+// 90.6 us a call, 91.1 with a row at a time; wide heads 50.1 so, 50.7 with 2).
 template <int HEAD_DIM>
 constexpr int kCutRows = HEAD_DIM == 256 ? 1 : 4;
 
