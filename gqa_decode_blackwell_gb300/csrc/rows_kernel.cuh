@@ -32,12 +32,12 @@
 //     blocks are two ring tiles each, their 128-element d-halves.
 //
 // What bounds it, measured on GB300 (bf16): at head_dim 128 a step of two
-// tiles takes ~3300 cycles, in which the tensor core works for 2048, the
+// tiles takes ~3200 cycles, in which the tensor core works for 2048, the
 // exponential units for 1024 and shared memory for ~2048 (Q and K at QK, V at
 // PV, the next blocks' arrival).  S, softmax, P and PV of a tile are a chain,
 // and two tiles' S and O fill TMEM, so the gaps of one are filled by the other
-// alone: 2048 tokens of 32 heads against 8192 keys, 4 of them, run at 1.35
-// PFLOP/s (800 us).  At head_dim 256 the one tile takes its K and V, 64 bytes
+// alone: 2048 tokens of 32 heads against 8192 keys, 4 of them, run at 1.4
+// PFLOP/s (766-800 us, by box).  At head_dim 256 the one tile takes its K and V, 64 bytes
 // a clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of
 // 16 heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
 // few, a block costs what its chain takes (~1900 cycles, split between two
@@ -181,8 +181,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // awaited one is known to be complete; with one tile, QK(g) is issued ahead
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
-                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NT, S_FULL = Q_EMPTY + NT, P_FULL = S_FULL + 2,
-                O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing,
+                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NT, S_FULL = Q_EMPTY + NT, P_HALF = S_FULL + 2,
+                P_FULL = P_HALF + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing,
                 N_BARRIERS = ITEM_EMPTY + kItemRing;
   static_assert(N_BARRIERS <= 64, "barrier words");
 
@@ -194,7 +194,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   if (warp == 0) {
     for (int i = lane; i < N_BARRIERS; i += 32) {
       uint32_t arrivals = 1;
-      if (i >= P_FULL && i < P_FULL + 2) arrivals = 4;         // the softmax warps of a tile
+      if (i >= P_HALF && i < P_FULL + 2) arrivals = 4;         // the softmax warps of a tile
       if (i >= ITEM_EMPTY) arrivals = Cfg::kSoftmaxWarps + 2;  // softmax warps, producer, issuer
       ptx::mbar_init(BAR(i), arrivals);
     }
@@ -393,21 +393,31 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         auto pv = [&](int j) {
           const uint32_t slot = slot_of(j), blk = block_of(j);
           const uint32_t o_tmem = tmem_base + Cfg::kOCol + (NT == 1 ? 0u : slot * HEAD_DIM);
-          wait(P_FULL + static_cast<int>(slot), g[slot]);
-          ++g[slot];
+          constexpr int KK = kBlockN / 16, PARTS = NT == 1 ? 1 : 2;
           const bool first = j < (NT == 1 ? 1 : ahead);
+          // (V first: it has most often arrived, and P is the one waited for)
+          if (TPB == 1 && (!two || slot == 0u)) wait(V_FULL + static_cast<int>(blk % NSV), blk / NSV);
+          // P comes in two halves, so that the first one's MMAs run under the
+          // last exponentials: 4 x 2048 tokens of 32 heads against 8192 keys
+          // 766 us and not 797, a batch behind 32768 keys 194 and not 199
+          // (thirds at 1/2 and 3/4: 812, 205).  One tile waits for V, not P.
 #pragma unroll
-          for (int hf = 0; hf < TPB; ++hf) {
-            const uint32_t m = blk * TPB + hf, stage = m % NSV;
-            if (!two || slot == 0u) wait(V_FULL + static_cast<int>(stage), m / NSV);
-            if (!ok) return;
-            ptx::tc_fence_after();
-            const uint32_t vd = v_lo + ((stage * Cfg::kStageBytes) >> 4);
+          for (int part = 0; part < PARTS; ++part) {
+            wait((part + 1 < PARTS ? P_HALF : P_FULL) + static_cast<int>(slot), g[slot]);
 #pragma unroll
-            for (int kk = 0; kk < kBlockN / 16; ++kk)
-              ptx::mma_f16_ts_elect(leader, o_tmem + hf * Cfg::kTileDim, tmem_base + slot * kBlockN + kk * 8,
-                                    vd + kk * (2048 >> 4), v_hi, idesc_pv, (kk > 0 || !first) ? 1u : 0u);
+            for (int hf = 0; hf < TPB; ++hf) {
+              const uint32_t m = blk * TPB + hf, stage = m % NSV;
+              if (TPB > 1) wait(V_FULL + static_cast<int>(stage), m / NSV);
+              if (!ok) return;
+              ptx::tc_fence_after();
+              const uint32_t vd = v_lo + ((stage * Cfg::kStageBytes) >> 4);
+#pragma unroll
+              for (int kk = part * (KK / PARTS); kk < (part + 1) * (KK / PARTS); ++kk)
+                ptx::mma_f16_ts_elect(leader, o_tmem + hf * Cfg::kTileDim, tmem_base + slot * kBlockN + kk * 8,
+                                      vd + kk * (2048 >> 4), v_hi, idesc_pv, (kk > 0 || !first) ? 1u : 0u);
+            }
           }
+          ++g[slot];
           ptx::mma_commit_elect(leader, BAR(O_FULL + static_cast<int>(slot)));
           if (!two || slot == 1u) {
 #pragma unroll
@@ -593,6 +603,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         }
         if (!active) {  // no row of this warp is read: whatever its lanes hold may stand for P
           __syncwarp();
+          if (NT == 2 && lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
           if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + static_cast<int>(slot)));
           continue;
         }
@@ -658,6 +669,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
                                              nm2), a, b);
             x[k] = __float_as_uint(ptx::ex2_in_order(a));
             x[k + 1] = __float_as_uint(ptx::ex2_in_order(b));
+          }
+          if (NT == 2 && c == 2) {  // the first two quarters' stores have had a quarter's time
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j)
