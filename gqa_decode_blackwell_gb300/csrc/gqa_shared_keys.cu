@@ -8,7 +8,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <vector>
 
 #include "../../include/gqa_shared_keys.h"
 #include "host.h"
@@ -421,13 +420,16 @@ gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int ma
     info[4 * i + 3] = static_cast<int>(r.s[i].pieces);
   }
   const int32_t* raw[2] = {with_prefix ? &prefix_len : kv_lens_host, with_prefix ? kv_lens_host : nullptr};
-  std::vector<int32_t> lens;
-  std::vector<uint32_t> pre(1, 0);
-  for (int i = 0; i < r.n; ++i)
-    for (int b = 0; b < r.d[i].batch; ++b) {
+  // as the kernel stages them (a dealt plan walks the lengths themselves)
+  int32_t lens[kMaxRowsEntries];
+  uint32_t pre[kMaxRowsEntries + 1] = {0};
+  int entries = 0;
+  for (int i = 0; i < r.n && !r.plan.dealt; ++i)
+    for (int b = 0; b < r.d[i].batch; ++b, ++entries) {
       const RowsPlanSection& s = r.plan.s[i];
-      lens.push_back(clamp_len(raw[i][b], s.max_len));
-      pre.push_back(pre.back() + static_cast<uint32_t>(s.heads) * static_cast<uint32_t>(rows_units(s, lens.back())));
+      lens[entries] = clamp_len(raw[i][b], s.max_len);
+      pre[entries + 1] =
+          pre[entries] + static_cast<uint32_t>(s.heads) * static_cast<uint32_t>(rows_units(s, lens[entries]));
     }
   int64_t n = 0;
   auto list = [&](int c, const RowsWork& w) {
@@ -444,11 +446,11 @@ gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int ma
   };
   for (int c = 0; c < r.plan.num_ctas; ++c) {
     RowsPlanIter it;
-    it.init(&r.plan, raw[0], raw[1], lens.data(), pre.data(), c);
+    it.init(&r.plan, raw[0], raw[1], lens, pre, c);
     RowsWork w;
     while (it.next(w)) list(c, w);
   }
-  for (int e = 0; e < static_cast<int>(lens.size()) && r.every_piece && !r.plan.dealt; ++e) {
+  for (int e = 0; e < entries && r.every_piece; ++e) {
     RowsWork w;
     std::memset(&w, 0, sizeof w);
     w.section = e < r.plan.s[0].batch ? 0 : 1;

@@ -98,7 +98,8 @@ gqa_status_t gqa_prefix_attn(const gqa_desc_t* desc, const void* q, const void* 
  *   items    (if not NULL) up to max_items records of 9 int32 each: cta,
  *            section, b, h, tile group, blk_begin, blk_end, piece (-1 = final
  *            output), n_pieces (of the triple, in the item of its first block),
- *            in the order each CTA processes them
+ *            in the order each CTA processes them; triples without keys of
+ *            which there is only that to record come last
  *   *num_items  their total count
  * sm_count and lengths as gqa_decode_plan; any output but items may be NULL.
  */
