@@ -341,6 +341,8 @@ CROSS = [  # B, T, H, K, d, S, lens, dtype, out dtype
     (40, 40, 4, 1, 64, 200, [(i * 13) % 201 for i in range(40)], BF16, None),
     (2, 32, 32, 8, 128, 1300, [1300, 257], BF16, None),          # one full tile: its keys are not split
     (3, 16, 32, 8, 128, 1300, [1300, 0, 129], FP16, FP32),       # half a tile: they are
+    (300, 40, 4, 1, 64, 300, [0] * 200 + [300] * 100, BF16, None),   # a padded batch: cut triples after empty ones
+    (300, 12, 16, 2, 128, 300, [300, 0, 0] * 100, FP16, None),       # and one whose triples all leave partials
 ]
 
 
@@ -502,6 +504,8 @@ PREFIX = [  # B, T, H, K, d, P, room, S, lens, dtype, out dtype, causal
     (2, 8, 16, 4, 128, 400, 400, 700, [700, 9], BF16, None, True),              # 64 rows, 32 of their own
     (40, 8, 16, 4, 128, 400, 400, 700, [(i * 17) % 701 for i in range(40)], FP16, None, True),
     (3, 1, 128, 4, 64, 260, 260, 40, [40, 1, 0], BF16, None, False),            # G = 32
+    (400, 1, 16, 2, 128, 700, 800, 300, [0] * 390 + list(range(10)), FP16, None, False),   # a padded batch
+    (400, 1, 8, 4, 256, 0, 800, 300, [300] + [0] * 399, BF16, None, False),
 ]
 
 
@@ -618,6 +622,45 @@ def test_two_streams_at_once(dev):
     for ga, gb in got:
         assert torch.equal(ga[0], want_a[0]) and torch.equal(ga[1], want_a[1])
         assert torch.equal(gb[0], want_b[0]) and torch.equal(gb[1], want_b[1])
+    assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
+def test_calls_in_a_row_share_a_workspace(dev):
+    """Different calls back to back on one stream, eagerly and as a graph, in
+    one workspace that holds NaNs at first: the results of each alone."""
+    a = _cross_case(dev, 2, 400, 8, 2, 128, 3000, [3000, 1700], seed=15)
+    b = _prefix_case(dev, 48, 1, 16, 2, 64, 3000, 3000, 400, [(i * 31) % 400 for i in range(48)], seed=16)
+    c = _cross_case(dev, 5, 20, 8, 2, 128, 900, [900, 0, 0, 17, 500], seed=17)
+    want = [g.cross_attention(*a), g.prefix_decode(*b), g.cross_attention(*c)]
+    torch.cuda.synchronize()
+    need = max(g.gqa_cross_workspace_size(a[0], a[1]), g.gqa_prefix_workspace_size(b[0], b[1], b[4]),
+               g.gqa_cross_workspace_size(c[0], c[1]))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=dev)
+    got = [[torch.empty_like(t) for t in w] for w in want]
+
+    def all_three():
+        g.gqa_cross_attn(*a, *got[0], ws)
+        g.gqa_prefix_attn(*b, *got[1], ws)
+        g.gqa_cross_attn(*c, *got[2], ws)
+
+    def check():
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+            o.fill_(math.nan)
+            l.fill_(math.nan)
+
+    for _ in range(5):
+        all_three()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(5):
+            all_three()
+    ws.fill_(255)
+    graph.replay()
+    check()
     assert g.gqa_decode_get_error() == g.GQA_OK
 
 
