@@ -33,13 +33,15 @@
 //
 // What bounds it, measured on GB300 (bf16): at head_dim 128 a step of two
 // tiles takes ~3200 cycles, in which the tensor core works for 2048, the
-// exponential units for 1024 and shared memory for ~2048 (Q and K at QK, V at
-// PV, the next blocks' arrival).  S, softmax, P and PV of a tile are a chain,
-// and two tiles' S and O fill TMEM, so the gaps of one are filled by the other
-// alone: 2048 tokens of 32 heads against 8192 keys, 4 of them, run at 1.4
-// PFLOP/s (766-800 us, by box).  At head_dim 256 the one tile takes its K and V, 64 bytes
-// a clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of
-// 16 heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
+// exponential units for 1024 and shared memory for ~2048 (Q and K at QK, which
+// alone take all of its 128 bytes a clock; V at PV, the next blocks' arrival).
+// The two add up rather than overlap: without exponentials, maxima and sums
+// (wrong results, to see) the kernel is only 8% faster, since a QK that shares
+// shared memory with an arriving block takes 750-950 cycles and not 516.  2048
+// tokens of 32 heads against 8192 keys, 4 of them, run at 1.4 PFLOP/s (766-800
+// us, by box).  At head_dim 256 the one tile takes its K and V, 64 bytes a
+// clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of 16
+// heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
 // few, a block costs what its chain takes (~1900 cycles, split between two
 // tiles) and an item ~5600 more; a CTA starts its first K load after ~4 us,
 // most of it code fetched for the first time.
@@ -658,29 +660,35 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
 
         // P, in place of the scores: 16-bit, two to a column
         const uint64_t nm2 = ptx::pack_f32x2(nm, nm);
+        auto exps = [&](int c) {  // of 16 columns
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int k = 32 * c + 2 * j;
+          for (int k = 16 * c; k < 16 * c + 16; k += 2) {
             float a, b;
             ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale2,
                                              nm2), a, b);
             x[k] = __float_as_uint(ptx::ex2_in_order(a));
             x[k + 1] = __float_as_uint(ptx::ex2_in_order(b));
           }
-          if (NT == 2 && c == 2) {  // the first two quarters' stores have had a quarter's time
+        };
+        auto put_p = [&](int c) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            w[j] = pack16(__uint_as_float(x[16 * c + 2 * j]), __uint_as_float(x[16 * c + 2 * j + 1]));
+          ptx::tmem_st_32x32b_x8u(s_addr + 8 * c, w);
+        };
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          exps(c);
+          if (NT == 2 && c == 6) {  // the first half's stores, up to columns 79 by now, have had time
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[j] = pack16(__uint_as_float(x[32 * c + 2 * j]), __uint_as_float(x[32 * c + 2 * j + 1]));
-          ptx::tmem_st_32x32b_x16u(s_addr + 16 * c, w);
+          if (c > 0) put_p(c - 1);  // under the next exponentials, whose unit then does not wait for it
         }
+        put_p(7);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
