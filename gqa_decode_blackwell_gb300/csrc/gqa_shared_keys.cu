@@ -22,8 +22,8 @@ namespace {
 // two tiles of rows (~1.7 us), against one in turn with the next block (~1) and
 // against one alone, a triple's fixed cost -- Q load, pipeline fill, epilogue
 // -- and writing the zeros of one without keys.  Measured on GB300 at head_dim 128: 128 sequences behind 32768 shared
-// keys take 199 us with 7 / 4 / 16 and 236 us with equal costs for both kinds
-// of block and 4 for a triple; 32 sequences of up to 512 keys behind 4000 31.7
+// keys take 195 us so, 228 with 4 units for everything, 228 with 4 only for a
+// triple; 32 sequences of up to 512 keys behind 4000 31.7
 // us with 6 for the prefix's lone tiles and 37 us with 4; 64 prompts of 200 tokens, 60 of them without
 // keys, 35 us with 6 units for those and 39 us with 10.
 constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kLoneTileUnits = 6, kItemUnits = 16, kZerosUnits = 6;
