@@ -8,10 +8,11 @@
 // load, pipeline fill, epilogue) and then block_units for every block; one
 // without takes empty_units for the zeros to write, so that a batch's empty
 // entries are spread like its work -- or none and is not listed, where all
-// there is to write is a record (empty_owner).  The U units are cut into C ranges of equal length (give
-// or take one unit), one per CTA, and a block belongs to the CTA in whose range
-// it begins.  A range is never shorter than a block, so the CTAs that hold a
-// triple's blocks are consecutive and each holds at least one.
+// there is to write is a record (empty_owner).  The U units are cut into C
+// ranges of equal length (give or take one unit), one per CTA, and a block
+// belongs to the CTA in whose range it begins.  A range is never shorter than
+// a block, so the CTAs that hold a triple's blocks are consecutive and each
+// holds at least one.
 //
 // The units let blocks of different cost share a launch: compute-bound ones
 // of a prefix that many rows share, and memory-bound ones of the sequences'
@@ -28,7 +29,7 @@
 
 namespace gqa {
 
-constexpr int kMaxRowsEntries = 1024;  // batch entries whose lengths are staged in shared memory
+constexpr int kMaxRowsEntries = 4096;  // batch entries whose lengths are staged in shared memory
 
 struct RowsPlanSection {
   int batch;        // entries (0: no such section)
@@ -75,6 +76,15 @@ struct RowsPlanIter {
     const uint32_t split = rem * (q + 1);
     return static_cast<int>(u < split ? u / (q + 1) : rem + (u - split) / q);
   }
+  // The first entry from `a` on that holds units past u (the number of entries if none does).
+  GQA_HD int reaching(uint32_t u, int a) const {
+    int z = rp->s[0].batch + rp->s[1].batch;
+    while (a < z) {
+      const int mid = (a + z) / 2;
+      if (pre[mid + 1] > u) z = mid; else a = mid + 1;
+    }
+    return a;
+  }
   GQA_HD const RowsPlanSection& section(int entry) const { return rp->s[entry < rp->s[0].batch ? 0 : 1]; }
 
   GQA_HD void init(const RowsPlan* plan, const int32_t* lens0, const int32_t* lens1, const int32_t* clamped,
@@ -97,12 +107,7 @@ struct RowsPlanIter {
     }
     lo = start(static_cast<uint32_t>(c));
     hi = start(static_cast<uint32_t>(c) + 1);
-    int a = 0, z = E;  // the first entry that reaches lo
-    while (a < z) {
-      const int mid = (a + z) / 2;
-      if (pre[mid + 1] > lo || pre[mid] >= lo) z = mid; else a = mid + 1;
-    }
-    e = a;
+    e = reaching(lo, 0);
     if (e < E && pre[e] < lo)
       hh = static_cast<int>((lo - pre[e]) / static_cast<uint32_t>(rows_units(section(e), lens[e])));
   }
@@ -139,12 +144,16 @@ struct RowsPlanIter {
     while (e < E) {
       const RowsPlanSection& s = section(e);
       const uint32_t u = static_cast<uint32_t>(rows_units(s, lens[e]));
+      if (u == 0) {  // a run of these may be long
+        e = reaching(pre[e], e + 1);
+        continue;
+      }
       const uint32_t v = pre[e] + static_cast<uint32_t>(hh) * u;
       if (v >= hi) return false;
       const uint32_t nblk = static_cast<uint32_t>(num_blocks(lens[e]));
       bool mine = false;
       if (nblk == 0) {
-        if (u > 0 && v >= lo) {
+        if (v >= lo) {
           emit(w, 0, 0, 1, 1);
           mine = true;
         }

@@ -210,6 +210,7 @@ def _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix=None):
     ([4096] * 4, 2048, 32, 8, 128, 4096), ([1, 0, 129, 1000, 128], 77, 12, 12, 64, 1023), ([0, 0], 50, 8, 1, 64, 512),
     ([131072], 64, 64, 8, 128, 131072), ([5001, 4000], 333, 16, 2, 256, 5001), ([700], 33, 3, 1, 128, 700),
     ([-5, 9999, 300], 100, 24, 8, 128, 600), ([1], 1, 128, 1, 64, 1), ([300] * 1100, 40, 4, 4, 64, 300),
+    ([300] * 4097, 40, 4, 4, 64, 300), ([300] * 4096, 20, 4, 4, 64, 300),
     ([0, 0, 5, 0, 0, 700, 0], 200, 4, 2, 128, 700), ([100, 90], 129, 2, 2, 64, 128)])
 def test_plan_covers_every_block_once(lens, nq, Hq, Hkv, d, s_max, sm):
     load = _check_plan(lens, nq, Hq, Hkv, d, s_max, sm)
@@ -236,7 +237,8 @@ def test_entries_without_keys_are_spread(lens, nq, prefix):
 @pytest.mark.parametrize("lens,nq,Hq,Hkv,d,s_max,prefix", [
     ([5, 700, 0, 128], 1, 8, 2, 128, 700, (1000, 1024)), ([300] * 128, 1, 64, 8, 128, 2048, (32768, 32768)),
     ([0] * 40, 2, 8, 1, 64, 10, (0, 5)), ([40] * 40, 2, 8, 1, 64, 50, (0, 5)), ([7] * 24, 1, 16, 2, 256, 300, (20000, 20480)),
-    ([9] * 1100, 4, 32, 4, 64, 9, (130, 130)), ([0, 3], 8, 8, 2, 64, 9, (999, 500))])
+    ([9] * 1100, 4, 32, 4, 64, 9, (130, 130)), ([9] * 4096, 4, 32, 4, 64, 9, (130, 130)),
+    ([0] * 900 + [300] * 20, 1, 8, 2, 64, 300, (999, 999)), ([7] * 9 + [0] * 900 + [300] * 20, 1, 8, 2, 64, 300, (0, 9)), ([0, 3], 8, 8, 2, 64, 9, (999, 500))])
 def test_plan_with_a_prefix(lens, nq, Hq, Hkv, d, s_max, prefix, sm):
     _check_plan(lens, nq, Hq, Hkv, d, s_max, sm, prefix)
 
@@ -446,6 +448,17 @@ def test_more_entries_than_lengths_are_staged(dev):
 
 
 @gpu
+@pytest.mark.parametrize("T", [40, 150])
+def test_a_batch_dealt_whole(dev, T):
+    """More entries than the kernel stages: triples go to the CTAs whole, in turn."""
+    lens = [(i * 29) % 162 - 1 for i in range(4100)]
+    q, k, v, ln = _cross_case(dev, 4100, T, 2, 2, 64, 160, lens, seed=18)
+    out, lse = _run_cross(q, k, v, ln)
+    _compare("batch 4100", out, lse, _cross_want(q, k, v, lens, BF16))
+    assert g.gqa_decode_get_error() == g.GQA_ERR_BAD_SEQLEN
+
+
+@gpu
 def test_cross_offsets_past_32_bits(dev):
     """K and V of 2.1e9 elements each: only the last batch entry's last head holds anything but zeros."""
     B, S, K, d, T = 2, 8200, 1024, 128, 40
@@ -506,6 +519,7 @@ PREFIX = [  # B, T, H, K, d, P, room, S, lens, dtype, out dtype, causal
     (3, 1, 128, 4, 64, 260, 260, 40, [40, 1, 0], BF16, None, False),            # G = 32
     (400, 1, 16, 2, 128, 700, 800, 300, [0] * 390 + list(range(10)), FP16, None, False),   # a padded batch
     (400, 1, 8, 4, 256, 0, 800, 300, [300] + [0] * 399, BF16, None, False),
+    (4100, 1, 4, 2, 64, 300, 333, 140, [(i * 7) % 141 for i in range(4100)], BF16, None, False),   # lengths not staged
 ]
 
 
