@@ -18,15 +18,21 @@
 namespace gqa {
 namespace {
 
-// Units of the plan's line (rows_plan.cuh), of ~0.25 us: a key block against
-// two tiles of rows (~1.7 us), against one in turn with the next block (~1) and
-// against one alone, a triple's fixed cost -- Q load, pipeline fill, epilogue
-// -- and writing the zeros of one without keys.  Measured on GB300 at head_dim 128: 128 sequences behind 32768 shared
-// keys take 195 us so, 228 with 4 units for everything, 228 with 4 only for a
-// triple; 32 sequences of up to 512 keys behind 4000 31.7
-// us with 6 for the prefix's lone tiles and 37 us with 4; 64 prompts of 200 tokens, 60 of them without
-// keys, 35 us with 6 units for those and 39 us with 10.
-constexpr int kTwoTileUnits = 7, kOneTileUnits = 4, kLoneTileUnits = 6, kItemUnits = 16, kZerosUnits = 6;
+// Units of the plan's line (rows_plan.cuh), of ~0.12 us: a key block against two
+// tiles of rows, against one tile alone, at head_dim 256, against few rows (split
+// between the tiles); a triple's fixed cost -- Q load, pipeline fill, epilogue --
+// with many rows and with few; the zeros of a triple without keys.  Measured on
+// GB300, us per call, with the units of a split block and item beside:
+//   7, 16 (here)   128 sequences of up to 2048 keys behind 32768 (64 / 8 heads of
+//                  128) 185; 1020 of 200 behind 2000 (32 / 8) 326; 256 of 400
+//                  behind 16000 144; 32 of up to 512 behind 4000 28.1
+//   8, 32          191, 437, 175, 32.6
+//   8, 20          182, 363, 159, 28.2
+//   6, 12          203, 293, 162, 27.5
+// (a lone tile at 8 units instead of 12: the last of these 37 us, not 31.7, as it
+// was then; 64 prompts of 200 tokens, 60 without keys, 35 us, 39 with zeros at 20.)
+constexpr int kTwoTileUnits = 14, kLoneTileUnits = 12, kWideUnits = 8, kItemUnits = 32, kZerosUnits = 12;
+constexpr int kSplitUnits = 7, kSplitItemUnits = 16;
 // Up to this many rows a merge gives each a CTA, whose warps share its pieces;
 // beyond, a warp to a row.  Measured on GB300, a whole call: 384 rows of 256
 // 28.2 us (33.3 with a warp each), 1024 rows of 128 the same both ways, 2048
@@ -64,7 +70,7 @@ struct RowsLaunch {
   float scale;
   int n;                  // sections
   gqa_desc_t d[2];        // each section as a problem of its own
-  struct { int tokens, groups, split_keys, triples; long long pieces, part_row, rec; } s[2];
+  struct { int tokens, groups, split_keys, shift, triples; long long pieces, part_row, rec; } s[2];
   RowsPlan plan;
   bool every_piece;
   long long part_rows, records;
@@ -95,6 +101,7 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     auto& s = r.s[i];
     s.split_keys = split_keys(d, tiles) ? 1 : 0;
     s.tokens = d.q_tokens < most_tokens ? d.q_tokens : most_tokens;
+    s.shift = s.split_keys && s.tokens * G <= kTileRows / 2 ? kTileRows / 2 : 0;
     const int per_group = (s.split_keys ? 1 : tiles) * s.tokens;
     s.groups = (d.q_tokens - 1) / per_group + 1;
     const long long heads = static_cast<long long>(d.kv_heads) * s.groups;
@@ -103,11 +110,13 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     RowsPlanSection& ps = r.plan.s[i];
     ps.batch = d.batch;
     ps.heads = static_cast<int>(heads);
+    ps.groups = s.groups;
     ps.max_len = d.max_seqlen;
-    ps.block_units = s.split_keys || tiles == 1 ? kOneTileUnits
+    ps.block_units = tiles == 1                  ? kWideUnits
+                     : s.split_keys              ? kSplitUnits
                      : d.q_tokens <= most_tokens ? kLoneTileUnits
                                                  : kTwoTileUnits;
-    ps.item_units = kItemUnits;
+    ps.item_units = s.split_keys ? kSplitItemUnits : kItemUnits;
     ps.empty_units = r.every_piece ? 0 : kZerosUnits;
     entries += d.batch;
     units += static_cast<long long>(s.triples) * rows_units(ps, d.max_seqlen);
@@ -141,15 +150,15 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
 }
 
 struct RowsWs {
-  size_t lse_off, rec_off, total;
+  size_t ml_off, rec_off, total;
 };
 
 RowsWs rows_ws(const RowsLaunch& r) {
   RowsWs w{0, 0, 0};
   if (r.part_rows == 0) return w;
   const size_t rows = static_cast<size_t>(r.part_rows);
-  w.lse_off = round_up(rows * r.head_dim * sizeof(float), kWsAlign);
-  w.rec_off = w.lse_off + round_up(rows * sizeof(float), kWsAlign);
+  w.ml_off = round_up(rows * r.head_dim * sizeof(float), kWsAlign);
+  w.rec_off = w.ml_off + round_up(rows * sizeof(float2), kWsAlign);
   w.total = w.rec_off + round_up(static_cast<size_t>(r.records) * sizeof(int2), kWsAlign);
   return w;
 }
@@ -212,16 +221,17 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
     s.tokens = r.s[i].tokens;
     s.groups = r.s[i].groups;
     s.split_keys = r.s[i].split_keys;
+    s.shift = r.s[i].shift;
     s.causal = d.causal != 0 ? 1 : 0;
   }
   p.plan = r.plan;
   const RowsWs w = rows_ws(r);
   if (w.total > 0) {
     p.o_part = reinterpret_cast<float*>(ws);
-    p.lse_part = reinterpret_cast<float*>(ws + w.lse_off);
+    p.ml_part = reinterpret_cast<float2*>(ws + w.ml_off);
     p.rec = reinterpret_cast<int2*>(ws + w.rec_off);
-    p.o_part_bytes = w.lse_off;
-    p.lse_part_bytes = w.rec_off - w.lse_off;
+    p.o_part_bytes = w.ml_off;
+    p.ml_part_bytes = w.rec_off - w.ml_off;
     p.rec_bytes = w.total - w.rec_off;
   }
   const gqa_desc_t& last = r.d[r.n - 1];  // the batch as the caller sees it
@@ -251,7 +261,7 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
   RowsMergeParams m;
   std::memset(&m, 0, sizeof m);
   m.o_part = p.o_part;
-  m.lse_part = p.lse_part;
+  m.ml_part = p.ml_part;
   m.rec = p.rec;
   m.n_sections = r.n;
   for (int i = 0; i < r.n; ++i) {

@@ -43,8 +43,9 @@
 // clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of 16
 // heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
 // few, a block costs what its chain takes (~1900 cycles, split between two
-// tiles) and an item ~5600 more; a CTA starts its first K load after ~4 us,
-// most of it code fetched for the first time.
+// tiles) and an item ~4600 more: its QK, softmax, PV and epilogue follow one
+// another, with little to run under them.  A CTA starts its first K load after
+// ~4 us, most of it code fetched for the first time.
 //
 // The running max is only replaced when it grows by more than 8 (log2 units),
 // as in the decode kernel; a warp whose rows need it rescales its own lanes
@@ -54,7 +55,7 @@
 // Work: rows_plan.cuh.  A launch has one section of batch entries (cross
 // attention), or two: a prefix that a batch shares, all its rows as one
 // entry, and the sequences' own keys.  Triples that are cut, or all of them
-// (every_piece), leave fp32 partials (normalised O_s, lse_s) for
+// (every_piece), leave fp32 partials (O_s, its maximum and sum) for
 // rows_merge.cuh.
 //
 // Every wait is bounded, as in the decode kernel.
@@ -83,6 +84,10 @@ struct RowsSection {
   int tokens;           // query tokens of a tile: at most 128 / G
   int groups;           // tile groups of an entry: triples are h * groups + group
   int split_keys;       // both tiles hold the same rows
+  // TMEM lane of the second tile's first row: 0, or 64 where split tiles have at
+  // most 64 rows, whose warps then are not those of the first tile's scheduler
+  // (behind a long prefix 189 us, 192 without)
+  int shift;
   int causal;           // token t sees keys j <= L - nq + t
 };
 
@@ -92,7 +97,7 @@ struct RowsParams {
   void* out;            // [B, nq, Hq, d] bf16, fp16 or fp32: the rows of uncut triples
   float* lse;           // [B, nq, Hq] or null
   float* o_part;        // partial rows of d; a piece of a section holds kTiles * tokens * G of them, tile by tile
-  float* lse_part;      // one per partial row
+  float2* ml_part;      // its maximum (log2 units) and sum, one per partial row; sum 0: it saw nothing
   // every_piece: rec[triple] = {first piece, pieces} (0 pieces: no keys), the
   // pieces consecutive.  Else rec[CTA] = {triple, pieces} of the cut triple
   // that begins in this CTA (at most one), or {-1, 0}; its pieces are
@@ -106,7 +111,7 @@ struct RowsParams {
   unsigned long long timeout_ns;
   unsigned int* err_word;
   // byte extents of the buffers the kernel writes, checked by -DGQA_DEBUG builds
-  unsigned long long out_bytes, lse_bytes, o_part_bytes, lse_part_bytes, rec_bytes;
+  unsigned long long out_bytes, lse_bytes, o_part_bytes, ml_part_bytes, rec_bytes;
 };
 
 // One item of a CTA: a range of key blocks of one triple.
@@ -114,6 +119,11 @@ struct RowsItem {
   int section, b, h;
   int tok0;               // the first query token of its tiles
   int blk_begin, blk_end; // blk_begin < 0: no further item
+  int turn;               // the first block taken is blk_begin + turn; after the last comes blk_begin
+  __device__ __forceinline__ int block(int i) const {  // the i-th taken
+    const int b = blk_begin + turn + i;
+    return b < blk_end ? b : b - (blk_end - blk_begin);
+  }
   int L;                  // keys of entry b
   int piece;              // where its partials go; -1: final output
 };
@@ -303,14 +313,15 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           ptx::mbar_arrive_expect_tx(BAR(Q_FULL + slot), static_cast<uint32_t>(KCH * s.tokens * p.G * 128));
 #pragma unroll
           for (int kc = 0; kc < KCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384), &s.tm_q, BAR(Q_FULL + slot),
+            ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384 + s.shift * 128), &s.tm_q, BAR(Q_FULL + slot),
                              kc * 64, it.h * p.G, it.tok0 + t * s.tokens, it.b);
         }
         // K0, then K(i+1), V(i): at most one block of K ahead of its V
-        if (ok) ok = load_block(false, it, it.blk_begin);
-        for (int blk = it.blk_begin; blk < it.blk_end && ok; ++blk) {
-          if (blk + 1 < it.blk_end) ok = load_block(false, it, blk + 1);
-          if (ok) ok = load_block(true, it, blk);
+        const int n = it.blk_end - it.blk_begin;
+        if (ok) ok = load_block(false, it, it.block(0));
+        for (int i = 0; i < n && ok; ++i) {
+          if (i + 1 < n) ok = load_block(false, it, it.block(i + 1));
+          if (ok) ok = load_block(true, it, it.block(i));
         }
         if (!ok) break;
       }
@@ -364,6 +375,9 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         const bool two = nt == 2;
         const int steps = two ? 2 * n : n;
         const int ahead = NT == 1 ? 1 : (two || __shfl_sync(0xffffffffu, p.s[it.section].split_keys, 0) != 0 ? 2 : 1);
+        // (16-byte units)  Shifted rows are at `shift` in their Q slot: the second tile reads it from its start,
+        // the first one from there on, each with rows of other data beside its own.
+        const uint32_t q_shift = __shfl_sync(0xffffffffu, static_cast<uint32_t>(p.s[it.section].shift), 0) * 8;
         auto slot_of = [&](int j) -> uint32_t {
           return NT == 1 ? (u + static_cast<uint32_t>(j)) & 1u : (ahead == 2 ? static_cast<uint32_t>(j) & 1u : 0u);
         };
@@ -376,7 +390,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             if (!two || slot == 0u) wait(K_FULL + static_cast<int>(stage), m / NSK);
             if (!ok) return;
             ptx::tc_fence_after();
-            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4), kd = k_lo + ((stage * Cfg::kStageBytes) >> 4);
+            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4) + (slot == 0u ? q_shift : 0u), kd = k_lo + ((stage * Cfg::kStageBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < Cfg::kTileDim / 16; ++kk) {
               const int k = hf * (Cfg::kTileDim / 16) + kk;
@@ -492,6 +506,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           it.tok0 = (w.hh - it.h * s.groups) * (NT * s.tokens);
           it.blk_begin = w.blk_begin;
           it.blk_end = w.blk_end;
+          it.turn = w.turn;
           it.L = w.L;
           it.piece = partial ? rows_piece(p.every_piece != 0, p.plan.dealt != 0, triple, static_cast<int>(blockIdx.x),
                                           first_piece)
@@ -559,15 +574,17 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       const bool split_keys = NT == 2 && p.s[it.section].split_keys != 0;
       if (!split_keys && t >= slots_of(it)) continue;
       const int rows = p.s[it.section].tokens * p.G;   // of a tile
-      const bool active = (warp & 3) * 32 < rows;      // this warp holds any of them
+      const int first_lane = t == 1 ? p.s[it.section].shift : 0;
+      const int rr = r - first_lane;                   // the row within the tile
+      const bool active = rr >= lane && rr - lane < rows;  // this warp holds any of them
       // the last key this row sees is L - 1, or (causal) L - nq + its token
       const int causal_cut = p.s[it.section].causal != 0 ? p.s[it.section].nq - 1 : 0;
-      const int sees = it.L - causal_cut + (causal_cut != 0 ? it.tok0 + r / p.G : 0);
+      const int sees = it.L - causal_cut + (causal_cut != 0 ? it.tok0 + rr / p.G : 0);
       const int step = split_keys ? 2 : 1, i0 = split_keys ? t : 0;
 
       float nm = kNoMax, l = 0.f;  // -max (log2 units; kNoMax while it is -inf) and the sum of this row
       for (int i = i0; i < n_blk; i += step, ++g) {
-        const int blk = it.blk_begin + i;
+        const int blk = it.block(i);
         const uint32_t slot = NT == 2 ? static_cast<uint32_t>(t) : (g & 1u);
         const uint32_t s_addr = tmem_base + lanes + slot * kBlockN;
         const bool first = i == i0;
@@ -637,7 +654,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;  // the scale is positive
         if (first) {
           nm = m_blk == -INFINITY ? kNoMax : -m_blk;
-        } else if (__any_sync(0xffffffffu, r < rows && m_blk + nm > kRescaleThreshold)) {
+        } else if (__any_sync(0xffffffffu, rr < rows && m_blk + nm > kRescaleThreshold)) {
           // O may be rescaled once the value MMA of the block before has landed
           if (!wait_pv(g - 1)) break;
           ptx::tc_fence_after();
@@ -715,30 +732,41 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         ptx::tc_fence_after();
       }
       const RowsSection& sec = p.s[it.section];
+      if (partial) {
+        // O as it stands, with its maximum and sum: the merge normalises.  Rows
+        // of tokens past the last one have a place too, which nothing reads.
+        const long long prow = sec.part_row + (static_cast<long long>(it.piece) * NT + t) * rows + rr;
+        float* dst = p.o_part + prow * HEAD_DIM;
+        const bool store = rr < rows && !empty && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
+        if (rr < rows && detail::write_ok(p.err_word, p.ml_part, p.ml_part_bytes, p.ml_part + prow, sizeof(float2)))
+          p.ml_part[prow] = make_float2(-nm, l);
+        if (empty) continue;
+#pragma unroll 1
+        for (int c = 0; c < HEAD_DIM; c += 32) {
+          uint32_t o[4][8];
+          ptx::tmem_ld_32x32b_x32(o_addr + c, o[0]);
+          ptx::tmem_wait_ld();
+          if (store) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ptx::st_global_v8(dst + c + 8 * q, o[q]);
+          }
+          __syncwarp();  // the next TMEM load is the whole warp's
+        }
+        continue;
+      }
       const int r_tok = r / p.G, tok = it.tok0 + (split_keys ? 0 : t * sec.tokens) + r_tok;
       const bool row_valid = r_tok < sec.tokens && tok < sec.nq;
       const long long row = (static_cast<long long>(it.b) * sec.nq + tok) * p.Hq + it.h * p.G + (r - r_tok * p.G);
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // a row that saw only -inf scores: 0; NaN stays NaN
       const float lse = l > 0.f || l != l ? 0.69314718055994531f * (__log2f(l) - nm) : -INFINITY;
-      const long long prow = sec.part_row + (static_cast<long long>(it.piece) * NT + t) * rows + r;
-      const bool out16 = !partial && p.out_dtype != kOutF32;
-      uint8_t* dst;
-      bool store;
-      if (partial) {
-        dst = reinterpret_cast<uint8_t*>(p.o_part + prow * HEAD_DIM);
-        store = row_valid && !empty && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
-        if (row_valid && detail::write_ok(p.err_word, p.lse_part, p.lse_part_bytes, p.lse_part + prow, 4ull))
-          p.lse_part[prow] = lse;
-      } else {
-        dst = static_cast<uint8_t*>(p.out) + row * (HEAD_DIM * (out16 ? 2 : 4));
-        store = row_valid &&
-                detail::write_ok(p.err_word, p.out, p.out_bytes, dst, HEAD_DIM * (out16 ? 2ull : 4ull));
-        if (row_valid && p.lse != nullptr && detail::write_ok(p.err_word, p.lse, p.lse_bytes, p.lse + row, 4ull))
-          p.lse[row] = lse;
-      }
-      const bool v32 = partial || p.out_v32 != 0;
+      const bool out16 = p.out_dtype != kOutF32;
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + row * (HEAD_DIM * (out16 ? 2 : 4));
+      const bool store =
+          row_valid && detail::write_ok(p.err_word, p.out, p.out_bytes, dst, HEAD_DIM * (out16 ? 2ull : 4ull));
+      if (row_valid && p.lse != nullptr && detail::write_ok(p.err_word, p.lse, p.lse_bytes, p.lse + row, 4ull))
+        p.lse[row] = lse;
       auto put = [&](uint8_t* to, const uint32_t (&v)[8]) {
-        if (v32) {
+        if (p.out_v32 != 0) {
           ptx::st_global_v8(to, v);
         } else {
           reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
@@ -769,7 +797,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             }
           }
         }
-        __syncwarp();  // the next TMEM load is the whole warp's
+        __syncwarp();
       }
     }
     if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);

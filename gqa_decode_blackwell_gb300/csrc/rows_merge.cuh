@@ -1,18 +1,18 @@
-// Log-sum-exp merge of the partials of rows_kernel.cuh, and of a shared
-// prefix's partials with those of each sequence's own keys:
+// Merge of the partials of rows_kernel.cuh, and of a shared prefix's partials
+// with those of each sequence's own keys.  A piece s of a row is O_s, not
+// normalised, its maximum m_s (log2 units) and its sum l_s:
 //
-//   M = max_s lse_s;  w_s = exp(lse_s - M);  O = sum_s w_s O_s / sum_s w_s;
-//   lse = M + ln(sum_s w_s)
+//   M = max_s m_s;  w_s = 2^(m_s - M);  W = sum_s w_s l_s;
+//   O = sum_s w_s O_s / W;  lse = ln 2 (M + log2 W)
 //
-// over normalised fp32 partials, in a fixed order: the result is bit-identical
-// from run to run.  A warp keeps a running maximum and sum over a row's pieces,
-// whose LSEs and values it loads a batch at a time, all of them before the
-// first is used: what bounds the merge is how much it has in flight, not its
-// arithmetic (loads of one piece at a time: prompts of 256 tokens 115 us a call,
-// not 94; the merge alone takes 12 us there for 80 MB of partials, and 13 for
-// the 8192 rows of 128 sequences behind a prefix).  A lane owns HEAD_DIM / 32 consecutive elements.  The values of a
-// piece with lse_s = -inf may be anything (they are not written) and take no
-// part.
+// in fp32, in a fixed order: the result is bit-identical from run to run.  A
+// warp keeps a running maximum and sums over a row's pieces, whose values it
+// loads a batch at a time, all of them before the first is used: what bounds
+// the merge is how much it has in flight, not its arithmetic (loads of one
+// piece at a time: prompts of 256 tokens 115 us a call, not 94; the merge alone
+// takes 12 us there for 80 MB of partials).  A lane owns HEAD_DIM / 32
+// consecutive elements.  A piece with l_s = 0 saw nothing, and its O_s, which
+// may be anything, takes no part.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -35,7 +35,7 @@ struct RowsMergeSection {
 
 struct RowsMergeParams {
   const float* o_part;
-  const float* lse_part;
+  const float2* ml_part;
   const int2* rec;
   int n_sections;
   RowsMergeSection s[2];
@@ -55,7 +55,7 @@ struct PieceRun {
   __device__ __forceinline__ long long at(int j) const { return j == 0 ? first : next + (j - 1) * stride; }
 };
 
-// A row's merge so far: M = max_s lse_s (natural log), W = sum_s exp(lse_s - M), acc = sum_s exp(lse_s - M) O_s.
+// A row's merge so far: M = max_s m_s, W = sum_s 2^(m_s - M) l_s, acc = sum_s 2^(m_s - M) O_s.
 template <int VEC>
 struct RowSum {
   float M, W, acc[VEC];
@@ -65,42 +65,43 @@ struct RowSum {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
   }
-  // Adds a piece; an empty one (lse = -inf) leaves everything as it is.
-  __device__ __forceinline__ void add(float lse, const float (&v)[VEC]) {
-    constexpr float kLog2e = 1.4426950408889634f;
-    if (lse == -INFINITY) return;
-    const float m = fmaxf(M, lse);  // (a NaN lse makes its own weight NaN)
-    const float a = M == -INFINITY ? 0.f : ptx::ex2_approx((M - m) * kLog2e), b = ptx::ex2_approx((lse - m) * kLog2e);
+  // Adds a piece; an empty one leaves everything as it is.
+  __device__ __forceinline__ void add(float2 ml, const float (&v)[VEC]) {
+    if (ml.y == 0.f) return;
+    const float m = fmaxf(M, ml.x);
+    const float a = M == -INFINITY ? 0.f : ptx::ex2_approx(M - m), b = ptx::ex2_approx(ml.x - m);
     M = m;
-    W = W * a + b;
+    W = W * a + b * ml.y;  // (a NaN sum stays one)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) acc[e] = acc[e] * a + b * v[e];
   }
 };
 
-// Pieces first, first + step, ... of a run into R consecutive rows' sums, NB of them in flight.
-template <int HEAD_DIM, int R, int NB>
-__device__ __forceinline__ void add_run(RowSum<HEAD_DIM / 32> (&sum)[R], const float* __restrict__ o_part,
-                                        const float* __restrict__ lse_part, const PieceRun& run, int first, int step) {
+// Pieces first, first + step, ... of n (piece j begins at partial row at(j)) into R consecutive rows' sums, NB of
+// them in flight.
+template <int HEAD_DIM, int R, int NB, typename At>
+__device__ __forceinline__ void add_pieces(RowSum<HEAD_DIM / 32> (&sum)[R], const RowsMergeParams& p, const At& at, int n,
+                                           int first, int step) {
   constexpr int VEC = HEAD_DIM / 32;
   const int lane = threadIdx.x & 31;
-  for (int j0 = first; j0 < run.n; j0 += NB * step) {
-    float l[NB][R], v[NB][R][VEC];
+  for (int j0 = first; j0 < n; j0 += NB * step) {
+    float2 ml[NB][R];
+    float v[NB][R][VEC];
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
       const int j = j0 + q * step;
-      const long long at = run.at(j < run.n ? j : j0);
+      const long long row = at(j < n ? j : j0);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        l[q][r] = lse_part[at + r];
-        load_vec<VEC>(o_part + (at + r) * HEAD_DIM + lane * VEC, v[q][r]);
+        ml[q][r] = p.ml_part[row + r];
+        load_vec<VEC>(p.o_part + (row + r) * HEAD_DIM + lane * VEC, v[q][r]);
       }
     }
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
-      if (j0 + q * step >= run.n) break;
+      if (j0 + q * step >= n) break;
 #pragma unroll
-      for (int r = 0; r < R; ++r) sum[r].add(l[q][r], v[q][r]);
+      for (int r = 0; r < R; ++r) sum[r].add(ml[q][r], v[q][r]);
     }
   }
 }
@@ -110,7 +111,7 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
                                           long long row) {
   constexpr int VEC = HEAD_DIM / 32;
   const int lane = threadIdx.x & 31;
-  const bool none = sum.M == -INFINITY;
+  const bool none = sum.W == 0.f;
   const float inv = none ? 0.f : 1.0f / sum.W;
   float acc[VEC];
 #pragma unroll
@@ -142,7 +143,7 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
     else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }
-  if (lane == 0 && lse != nullptr) lse[row] = none ? -INFINITY : sum.M + 0.69314718055994531f * __log2f(sum.W);
+  if (lane == 0 && lse != nullptr) lse[row] = none ? -INFINITY : 0.69314718055994531f * (sum.M + __log2f(sum.W));
 }
 
 }  // namespace detail
@@ -178,7 +179,7 @@ gqa_rows_merge_kernel(const RowsMergeParams p) {
   detail::RowSum<HEAD_DIM / 32> sum[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) sum[r].clear();
-  detail::add_run<HEAD_DIM, R, 2>(sum, p.o_part, p.lse_part, run, 0, 1);
+  detail::add_pieces<HEAD_DIM, R, 2>(sum, p, [&](int j) { return run.at(j); }, run.n, 0, 1);
   const int per_batch = p.kv_heads * s.groups;
   const int b = rec.x / per_batch, hg = rec.x - b * per_batch;
   const int h = hg / s.groups, grp = hg - h * s.groups;
@@ -199,7 +200,7 @@ gqa_rows_merge_kernel(const RowsMergeParams p) {
 template <int HEAD_DIM, int WARPS>
 __global__ void __launch_bounds__(kMergeThreads)
 gqa_pieces_merge_kernel(const RowsMergeParams p) {
-  constexpr int VEC = HEAD_DIM / 32, NB = WARPS > 1 ? 4 : 8;
+  constexpr int VEC = HEAD_DIM / 32, NB = 4;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -229,9 +230,9 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
   }
   detail::RowSum<VEC> sum[1];
   sum[0].clear();
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    detail::add_run<HEAD_DIM, 1, NB>(sum, p.o_part, p.lse_part, run[i], WARPS > 1 ? warp : 0, WARPS);
+  const int n0 = run[0].n;
+  detail::add_pieces<HEAD_DIM, 1, NB>(sum, p, [&](int j) { return j < n0 ? run[0].at(j) : run[1].at(j - n0); },
+                                      n0 + run[1].n, WARPS > 1 ? warp : 0, WARPS);
   if constexpr (WARPS > 1) {
     __shared__ float s_acc[WARPS][HEAD_DIM], s_m[WARPS], s_w[WARPS];
 #pragma unroll
@@ -242,7 +243,6 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
     }
     __syncthreads();
     if (warp != 0) return;
-    constexpr float kLog2e = 1.4426950408889634f;
     float M = -INFINITY;
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) M = fmaxf(M, s_m[k]);
@@ -250,8 +250,8 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
     sum[0].M = M;
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) {
-      if (s_m[k] == -INFINITY) continue;
-      const float w = ptx::ex2_approx((s_m[k] - M) * kLog2e);
+      if (s_w[k] == 0.f) continue;
+      const float w = ptx::ex2_approx(s_m[k] - M);
       sum[0].W += w * s_w[k];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum[0].acc[e] += w * s_acc[k][lane * VEC + e];
