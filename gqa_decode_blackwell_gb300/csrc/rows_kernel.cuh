@@ -637,8 +637,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
 #pragma unroll
           for (int c = 0; c < 128; c += 32) {
             if (!__any_sync(0xffffffffu, seen < c + 32)) continue;
+            // bits, which the hardware moves to predicates several at a time: half the code of comparisons
+            const uint32_t vis = seen >= c + 32 ? 0xffffffffu : seen <= c ? 0u : (1u << (seen - c)) - 1u;
 #pragma unroll
-            for (int j = c; j < c + 32; ++j) x[j] = j < seen ? x[j] : 0xff800000u;  // -inf
+            for (int j = c; j < c + 32; ++j) x[j] = (vis >> (j - c)) & 1u ? x[j] : 0xff800000u;  // -inf
           }
         }
 
