@@ -194,8 +194,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
                 Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NT, S_FULL = Q_EMPTY + NT, P_HALF = S_FULL + 2,
-                P_FULL = P_HALF + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1, ITEM_EMPTY = ITEM_FULL + kItemRing,
-                N_BARRIERS = ITEM_EMPTY + kItemRing;
+                P_FULL = P_HALF + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1,
+                ITEM_EMPTY = ITEM_FULL + kItemRing, N_BARRIERS = ITEM_EMPTY + kItemRing;
   static_assert(N_BARRIERS <= 64, "barrier words");
 
   // (a shuffle tells the compiler that it is the same in all the warp)
@@ -313,8 +313,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           ptx::mbar_arrive_expect_tx(BAR(Q_FULL + slot), static_cast<uint32_t>(KCH * s.tokens * p.G * 128));
 #pragma unroll
           for (int kc = 0; kc < KCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384 + s.shift * 128), &s.tm_q, BAR(Q_FULL + slot),
-                             kc * 64, it.h * p.G, it.tok0 + t * s.tokens, it.b);
+            ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384 + s.shift * 128), &s.tm_q,
+                             BAR(Q_FULL + slot), kc * 64, it.h * p.G, it.tok0 + t * s.tokens, it.b);
         }
         // K0, then K(i+1), V(i): at most one block of K ahead of its V
         const int n = it.blk_end - it.blk_begin;
@@ -390,7 +390,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             if (!two || slot == 0u) wait(K_FULL + static_cast<int>(stage), m / NSK);
             if (!ok) return;
             ptx::tc_fence_after();
-            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4) + (slot == 0u ? q_shift : 0u), kd = k_lo + ((stage * Cfg::kStageBytes) >> 4);
+            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4) + (slot == 0u ? q_shift : 0u);
+            const uint32_t kd = k_lo + ((stage * Cfg::kStageBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < Cfg::kTileDim / 16; ++kk) {
               const int k = hf * (Cfg::kTileDim / 16) + kk;
@@ -401,7 +402,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           ptx::mma_commit_elect(leader, BAR(S_FULL + static_cast<int>(slot)));
           if (!two || slot == 1u) {  // the block's last use
 #pragma unroll
-            for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>((blk * TPB + hf) % NSK)));
+            for (int hf = 0; hf < TPB; ++hf)
+              ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>((blk * TPB + hf) % NSK)));
           }
           if (j + 1 == steps)
             for (int t = 0; t < nt; ++t) ptx::mma_commit_elect(leader, BAR(Q_EMPTY + static_cast<int>((uq + t) % NT)));
@@ -437,7 +439,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           ptx::mma_commit_elect(leader, BAR(O_FULL + static_cast<int>(slot)));
           if (!two || slot == 1u) {
 #pragma unroll
-            for (int hf = 0; hf < TPB; ++hf) ptx::mma_commit_elect(leader, BAR(V_EMPTY + static_cast<int>((blk * TPB + hf) % NSV)));
+            for (int hf = 0; hf < TPB; ++hf)
+              ptx::mma_commit_elect(leader, BAR(V_EMPTY + static_cast<int>((blk * TPB + hf) % NSV)));
           }
         };
 #pragma unroll 1
@@ -739,7 +742,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         // of tokens past the last one have a place too, which nothing reads.
         const long long prow = sec.part_row + (static_cast<long long>(it.piece) * NT + t) * rows + rr;
         float* dst = p.o_part + prow * HEAD_DIM;
-        const bool store = rr < rows && !empty && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
+        const bool store =
+            rr < rows && !empty && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, dst, HEAD_DIM * 4ull);
         if (rr < rows && detail::write_ok(p.err_word, p.ml_part, p.ml_part_bytes, p.ml_part + prow, sizeof(float2)))
           p.ml_part[prow] = make_float2(-nm, l);
         if (empty) continue;

@@ -80,8 +80,8 @@ struct RowSum {
 // Pieces first, first + step, ... of n (piece j begins at partial row at(j)) into R consecutive rows' sums, NB of
 // them in flight.
 template <int HEAD_DIM, int R, int NB, typename At>
-__device__ __forceinline__ void add_pieces(RowSum<HEAD_DIM / 32> (&sum)[R], const RowsMergeParams& p, const At& at, int n,
-                                           int first, int step) {
+__device__ __forceinline__ void add_pieces(RowSum<HEAD_DIM / 32> (&sum)[R], const RowsMergeParams& p, const At& at,
+                                           int n, int first, int step) {
   constexpr int VEC = HEAD_DIM / 32;
   const int lane = threadIdx.x & 31;
   for (int j0 = first; j0 < n; j0 += NB * step) {
