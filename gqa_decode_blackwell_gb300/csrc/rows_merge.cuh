@@ -149,10 +149,11 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
 }  // namespace detail
 
 // Rows a warp of the cut triples' merge takes at once: most of those have two
-// pieces, and two pieces of one short row are little to have in flight (prompts
-// 90.6 us a call, 91.1 with a row at a time; wide heads 50.1 so, 50.7 with 2).
+// pieces, and two pieces of one short row are little to have in flight, while
+// many rows leave few warps on an SM (prompts, rows of 128: 86.7 us a call with 2,
+// 87.3 with 4, 96.5 with 8; wide heads, of 256: 50.1 with 1, 50.7 with 2).
 template <int HEAD_DIM>
-constexpr int kCutRows = HEAD_DIM == 256 ? 1 : 4;
+constexpr int kCutRows = HEAD_DIM == 256 ? 1 : 2;
 
 // The cut triples of a launch of one section: blockIdx.x is the CTA of that
 // launch in which a cut triple may begin, blockIdx.y a group of its rows.
