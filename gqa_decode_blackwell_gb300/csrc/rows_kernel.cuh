@@ -325,16 +325,15 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         }
         if (!ok) break;
       }
-      if (!ok) {
-        detail::set_error(p.err_word, kErrTimeout, abort_flag);
-        // let the copies already issued land before the CTA exits
-        for (uint32_t u = tk > NSK ? tk - NSK : 0u; u < tk; ++u)
-          ptx::mbar_wait_bounded(BAR(K_FULL + static_cast<int>(u % NSK)), (u / NSK) & 1u, nullptr, p.timeout_ns);
-        for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
-          ptx::mbar_wait_bounded(BAR(V_FULL + static_cast<int>(u % NSV)), (u / NSV) & 1u, nullptr, p.timeout_ns);
-        for (uint32_t u = tq > NT ? tq - NT : 0u; u < tq; ++u)
-          ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(u % NT)), (u / NT) & 1u, nullptr, p.timeout_ns);
-      }
+      if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
+      // The copies issued last land before the CTA exits, whether this thread
+      // gave up or another role does while they are on their way.
+      for (uint32_t u = tk > NSK ? tk - NSK : 0u; u < tk; ++u)
+        ptx::mbar_wait_bounded(BAR(K_FULL + static_cast<int>(u % NSK)), (u / NSK) & 1u, nullptr, p.timeout_ns);
+      for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
+        ptx::mbar_wait_bounded(BAR(V_FULL + static_cast<int>(u % NSV)), (u / NSV) & 1u, nullptr, p.timeout_ns);
+      for (uint32_t u = tq > NT ? tq - NT : 0u; u < tq; ++u)
+        ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(u % NT)), (u / NT) & 1u, nullptr, p.timeout_ns);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
