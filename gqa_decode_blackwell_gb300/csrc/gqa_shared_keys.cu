@@ -247,7 +247,8 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
   p.every_piece = r.every_piece ? 1 : 0;
   const float scale = r.scale > 0.f ? r.scale : 1.0f / std::sqrt(static_cast<float>(r.head_dim));
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.timeout_ns = wait_timeout_ns();
+  const int longest = r.d[0].max_seqlen > last.max_seqlen ? r.d[0].max_seqlen : last.max_seqlen;
+  p.timeout_ns = wait_timeout_ns() + items_in_ring_ns(longest);
   const bool f16 = r.in_dtype == GQA_DTYPE_FP16;
   const int hd = r.head_dim;
   const KernelRef ref = hd == 64 ? rows_kernel_ref_64(f16) : hd == 256 ? rows_kernel_ref_256(f16) : rows_kernel_ref_128(f16);

@@ -58,7 +58,8 @@
 // (every_piece), leave fp32 partials (O_s, its maximum and sum) for
 // rows_merge.cuh.
 //
-// Every wait is bounded, as in the decode kernel.
+// Every wait is bounded, as in the decode kernel, with the time that the items
+// in the ring may take on top (items_in_ring_ns).
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -108,7 +109,7 @@ struct RowsParams {
   int out_v32;          // out is 32-byte aligned
   int every_piece;      // every triple leaves partials, none writes out / lse
   float scale_log2;
-  unsigned long long timeout_ns;
+  unsigned long long timeout_ns;  // of a wait: items_in_ring_ns() among it
   unsigned int* err_word;
   // byte extents of the buffers the kernel writes, checked by -DGQA_DEBUG builds
   unsigned long long out_bytes, lse_bytes, o_part_bytes, ml_part_bytes, rec_bytes;
@@ -129,6 +130,13 @@ struct RowsItem {
 };
 constexpr int kItemRing = 4;
 constexpr uint64_t kBlockNs = 20000;  // far more than a key block of an item takes
+
+// A role may have nothing to do while others work through all the items of the
+// ring: the plan's warp, when it is full, and the second tile's warps, where a
+// last group of rows fills one tile only, which leave the items they have no
+// part in at once and then wait for the next one, or for its first scores.  So
+// every wait may take as long as that, beside its timeout.
+GQA_HD uint64_t items_in_ring_ns(int max_len) { return static_cast<uint64_t>(num_blocks(max_len)) * kItemRing * kBlockNs; }
 
 template <int HEAD_DIM>
 struct RowsCfg {
@@ -488,7 +496,6 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     if (lane == 0) {
       bool ok = true;
       int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
-      int longest = 0;              // blocks of the longest item so far
       RowsPlanIter iter;
       iter.init(&p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
       for (uint32_t n = 0; ok; ++n) {
@@ -521,11 +528,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           }
         }
         const int i = static_cast<int>(n % kItemRing);
-        // as long as the items in the ring may take
         if (n >= kItemRing)
-          ok = ptx::mbar_wait_bounded(BAR(ITEM_EMPTY + i), ((n / kItemRing) & 1u) ^ 1u, abort_flag,
-                                      p.timeout_ns + static_cast<uint64_t>(longest) * kItemRing * kBlockNs);
-        if (it.blk_end - it.blk_begin > longest) longest = it.blk_end - it.blk_begin;
+          ok = ptx::mbar_wait_bounded(BAR(ITEM_EMPTY + i), ((n / kItemRing) & 1u) ^ 1u, abort_flag, p.timeout_ns);
         if (!ok) break;
         items_ring[i] = it;
         ptx::mbar_arrive(BAR(ITEM_FULL + i));

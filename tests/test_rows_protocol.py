@@ -21,7 +21,8 @@ Checked at every step:
 - nothing stands still, and nothing is in flight when the CTA ends.
 
 With one wait that runs out, whichever and whenever, every agent still ends
-and no load is left in flight.
+and no load is left in flight.  And no wait takes longer than the blocks of the
+items in the ring, which is what a wait is allowed beside its timeout.
 """
 import random
 from collections import namedtuple
@@ -406,6 +407,20 @@ def test_a_wait_that_runs_out_ends_every_role(d):
         whole.run()
         cta = Cta(SHAPES[d], items, rng, give_up_at=rng.randint(1, whole.waits))
         cta.run()
+
+
+def test_waits_take_no_longer_than_the_items_in_the_ring():
+    """The second tile's warps leave items of one tile at once.  Their next wait then spans the items that the first
+    tile still works on: more than one item (so that a timeout of one must not be all they have), but never more
+    blocks than RING items hold, and the few that are under way."""
+    rng = random.Random(5)
+    longest = 0
+    for _ in range(40):
+        items = [Item(rng.choice([25, 30]), rng.choice(["lone", "lone", "lone", "two"]), False) for _ in range(12)]
+        cta = Cta(SHAPES[128], items, rng)
+        cta.run()
+        longest = max(longest, cta.longest_wait)
+    assert 2 * 30 < longest <= RING * 30 + 4
 
 
 @pytest.mark.parametrize("d,mistake,found", [
