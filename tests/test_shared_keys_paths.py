@@ -126,3 +126,124 @@ def test_maxima_that_climb_behind_a_prefix(dev, B, T, H, K, dtype, causal, d):
             sees[:, P:] = torch.arange(L, device=dev)[None, :] <= (L - T + torch.arange(T, device=dev))[:, None]
         _compare(f"entry {b}", out[b:b + 1], lse[b:b + 1],
                  [_attend(q[b].double(), keys, values, sees, d ** -0.5, dtype, dtype)])
+
+
+# ------------------------------------------------------------------ dealt plans
+MANY = 4200   # entries: more than the kernel stages lengths for
+
+
+def _dealt(items):
+    """Every triple whole, triple t of a launch in CTA t mod the grid."""
+    order = np.lexsort((items[:, 4], items[:, 3], items[:, 2], items[:, 1]))
+    ctas = items[:, 0].max() + 1
+    return bool((items[:, 8] <= 1).all() and (items[order, 0] == np.arange(len(items)) % ctas).all())
+
+
+def _many(dev, T, H, K, d, S, dtype, lens, seed):
+    gen = torch.Generator(dev).manual_seed(seed)
+    q = _rand(gen, len(lens), T, H, d, dtype=dtype)
+    k, v = _rand(gen, len(lens), S, K, d, dtype=dtype), _rand(gen, len(lens), S, K, d, dtype=dtype)
+    ln = torch.tensor(lens, dtype=torch.int32, device=dev)
+    past = torch.arange(S, device=dev)[None, :] >= ln[:, None]
+    k[past], v[past] = math.nan, math.inf
+    return q, k, v, ln
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype,T,H,K", [(128, torch.float16, 40, 2, 2), (128, BF16, 129, 2, 1),
+                                           (256, BF16, 20, 4, 2), (256, torch.float16, 140, 1, 1)])
+def test_dealt_batches(dev, d, dtype, T, H, K):
+    lens = [(i * 29) % 301 for i in range(MANY)]
+    q, k, v, ln = _many(dev, T, H, K, d, 300, dtype, lens, seed=1)
+    assert _dealt(_items(q, k, lens)[1])
+    out, lse = g.cross_attention(q, k, v, ln)
+    torch.cuda.synchronize()
+    assert g.gqa_decode_get_error() == g.GQA_OK
+    assert torch.isfinite(out).all()
+    for b in list(range(0, MANY, 31)) + [MANY - 1]:
+        _sample(out, lse, q, k, v, b, range(T), lens[b])
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype,T,H,K,causal", [(128, torch.float16, 3, 4, 2, True), (256, BF16, 2, 4, 1, True),
+                                                  (256, torch.float16, 1, 2, 2, False)])
+def test_dealt_batches_behind_a_prefix(dev, d, dtype, T, H, K, causal):
+    lens, P, room = [(i * 29) % 151 for i in range(MANY)], 333, 400
+    q, k, v, ln = _many(dev, T, H, K, d, 150, dtype, lens, seed=2)
+    gen = torch.Generator(dev).manual_seed(3)
+    kp, vp = _rand(gen, room, K, d, dtype=dtype), _rand(gen, room, K, d, dtype=dtype)
+    kp[P:], vp[P:] = math.inf, math.nan
+    assert _dealt(_items(q, k, lens, P, room)[1])
+    out, lse = g.prefix_decode(q, kp, vp, torch.tensor([P], dtype=torch.int32, device=dev), k, v, ln, causal=causal)
+    torch.cuda.synchronize()
+    assert g.gqa_decode_get_error() == g.GQA_OK
+    assert torch.isfinite(out).all()
+    for b in list(range(0, MANY, 31)) + [1, 2, MANY - 1]:
+        L = lens[b]
+        sees = torch.ones(T, P + L, dtype=torch.bool, device=dev)
+        if causal:
+            sees[:, P:] = torch.arange(L, device=dev)[None, :] <= (L - T + torch.arange(T, device=dev))[:, None]
+        _compare(f"entry {b}", out[b:b + 1], lse[b:b + 1],
+                 [_attend(q[b].double(), torch.cat([kp[:P], k[b, :L]]).double(), torch.cat([vp[:P], v[b, :L]]).double(),
+                          sees, d ** -0.5, dtype, dtype)])
+
+
+HUGE = dict(batch=2, q_tokens=320000, q_heads=2, kv_heads=2, head_dim=64, max_seqlen=1 << 22)   # 2.3e9 units
+
+
+def test_units_past_32_bits_are_dealt():
+    _check_plan([300, 1000], HUGE["q_tokens"], 2, 2, 64, HUGE["max_seqlen"], 152)
+    assert _dealt(g.gqa_shared_keys_plan(_desc(**HUGE), [300, 1000], 0, 0, 152)[3])
+    fits = dict(HUGE, q_tokens=290000)
+    assert not _dealt(g.gqa_shared_keys_plan(_desc(**fits), [300, 1000], 0, 0, 152)[3])
+
+
+@gpu
+def test_a_call_of_so_many_units(dev):
+    lens, T = [300, 1000], HUGE["q_tokens"]
+    gen = torch.Generator(dev).manual_seed(4)
+    q = _rand(gen, 2, T, 2, 64)
+    k, v = (torch.empty(2, HUGE["max_seqlen"], 2, 64, dtype=BF16, device=dev) for _ in range(2))
+    for b, L in enumerate(lens):
+        k[b, :L], v[b, :L] = _rand(gen, L, 2, 64), _rand(gen, L, 2, 64)
+        k[b, L: L + 200], v[b, L: L + 200] = math.nan, math.nan
+    out, lse = g.cross_attention(q, k, v, torch.tensor(lens, dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    assert g.gqa_decode_get_error() == g.GQA_OK
+    assert torch.isfinite(out).all()
+    for b in range(2):
+        for at in range(0, T, 40000):
+            _sample(out, lse, q, k, v, b, range(at, at + 300), lens[b])
+        _sample(out, lse, q, k, v, b, range(T - 300, T), lens[b])
+
+
+@gpu
+def test_debug_build_of_dealt_batches(dev):
+    """The bounds-checked build catches no write outside a buffer where triples are dealt whole."""
+    import ctypes
+
+    from gqa_decode_blackwell_gb300 import build as gbuild
+
+    gbuild.build_debug()
+    L = g.load_library(gbuild.DEBUG_LIB)
+    assert L.gqa_decode_get_error(1) == g.GQA_OK
+    stream = torch.cuda.current_stream().cuda_stream
+    lens = [(i * 29) % 161 for i in range(MANY)]
+    kp = torch.ones(130, 2, 128, dtype=BF16, device=dev)
+    P = torch.tensor([130], dtype=torch.int32, device=dev)
+    for T, prefix in ((40, False), (150, False), (2, True)):
+        q, k, v, ln = _many(dev, T, 2, 2, 128, 160, BF16, lens, seed=5)
+        want = g.prefix_decode(q, kp, kp, P, k, v, ln) if prefix else g.cross_attention(q, k, v, ln)
+        out, lse = torch.full_like(want[0], math.nan), torch.full_like(want[1], math.nan)
+        n = g.gqa_prefix_workspace_size(q, kp, k) if prefix else g.gqa_cross_workspace_size(q, k)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        desc = g.make_desc(q, k)
+        end = [ln.data_ptr(), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, stream]
+        if prefix:
+            rc = L.gqa_prefix_attn(ctypes.byref(desc), q.data_ptr(), kp.data_ptr(), kp.data_ptr(), P.data_ptr(), 130,
+                                   k.data_ptr(), v.data_ptr(), *end)
+        else:
+            rc = L.gqa_cross_attn(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), *end)
+        torch.cuda.synchronize()
+        assert rc == g.GQA_OK and L.gqa_decode_get_error(1) == g.GQA_OK
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
