@@ -247,3 +247,63 @@ def test_debug_build_of_dealt_batches(dev):
         torch.cuda.synchronize()
         assert rc == g.GQA_OK and L.gqa_decode_get_error(1) == g.GQA_OK
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# -------------------------------------------------------- infinities and NaN seen
+def _expect(what, out, lse, want):
+    """As _compare, with NaN and infinities where the definition has them."""
+    o, l, to, tl = want
+    got, gl = out.double(), lse.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(o)), (what, "NaN of O")
+    assert torch.equal(torch.isnan(gl), torch.isnan(l)), (what, "NaN of the LSE")
+    for x, w, t in ((got, o, to), (gl, l, tl)):
+        far = torch.isinf(w)
+        assert torch.equal(x[far], w[far]) and not torch.isinf(x[~far]).any(), (what, "infinities")
+        fine = torch.isfinite(w)
+        assert ((x - w).abs()[fine] <= t[fine]).all(), (what, (x - w).abs()[fine].max().item())
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T", [40, 300], ids=["rows of one tile", "rows of two"])
+@pytest.mark.parametrize("dtype", [BF16, torch.float16], ids=["bf16", "fp16"])
+def test_infinities_and_nan_that_are_seen(dev, T, d, dtype):
+    """One head each: scores of -inf (some, whole blocks, all), a NaN in
+    K, in V, in one row of q, infinite V.  The other heads are as they were."""
+    K, S = 8, 30000
+    gen = torch.Generator(dev).manual_seed(d)
+    q, k, v = _rand(gen, 1, T, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype)
+    ln = torch.tensor([S], dtype=torch.int32, device=dev)
+    clean, clean_lse = g.cross_attention(q.abs(), k, v, ln)
+    q = q.abs()
+    k[0, ::3, 0, 0] = -math.inf           # q is positive: a score of -inf
+    k[0, torch.arange(S, device=dev) // 128 % 4 < 2, 1, 5] = -math.inf   # whole blocks, the first ones of many items
+    k[0, :, 2, 1] = -math.inf             # nothing left
+    k[0, 1234, 3, 2] = math.nan
+    v[0, 77, 4, 3] = math.nan
+    v[0, S - 1, 5, 4], v[0, 0, 5, 5] = math.inf, -math.inf
+    q[0, T // 2, 6, 1] = math.nan
+    out, lse = g.cross_attention(q, k, v, ln)
+    torch.cuda.synchronize()
+    assert g.gqa_decode_get_error() == g.GQA_OK
+    assert torch.equal(out[:, :, 7], clean[:, :, 7]) and torch.equal(lse[:, :, 7], clean_lse[:, :, 7])
+
+    sees = torch.ones(T, S, dtype=torch.bool, device=dev)
+    for h in range(K):
+        qd, kd, vd = q[0, :, h:h + 1].double(), k[0, :, h:h + 1].double(), v[0, :, h:h + 1].double()
+        if h < 3:                          # a score of -inf is a key that is not seen
+            hidden = torch.isinf(kd).any(-1)[:, 0]
+            kd = torch.where(torch.isinf(kd), 0.0, kd)
+            o, l, to, tl = _attend(qd, kd, vd, sees & ~hidden[None, :], d ** -0.5, dtype, dtype)
+        else:                              # bounds from finite stand-ins, values as they come
+            zq, zk, zv = (torch.where(torch.isfinite(x), x, 0.0) for x in (qd, kd, vd))
+            o, l, to, tl = _attend(zq, zk, zv, sees, d ** -0.5, dtype, dtype)
+            if h == 3:
+                o, l = torch.full_like(o, math.nan), torch.full_like(l, math.nan)
+            elif h == 4:
+                o[..., 3] = math.nan
+            elif h == 5:
+                o[..., 4], o[..., 5] = math.inf, -math.inf
+            elif h == 6:
+                o[T // 2], l[T // 2] = math.nan, math.nan
+        _expect(f"head {h}", out[0, :, h:h + 1], lse[0, :, h:h + 1], (o, l, to, tl))
