@@ -6,9 +6,10 @@
 //   M = max_s lse_s;  w_s = exp(lse_s - M);  O = sum_s w_s O_s / sum_s w_s;
 //   lse = M + ln(sum_s w_s).
 // A split with lse_s = -inf is empty and its partial is ignored; a row whose
-// splits are all empty gets O = 0 and lse = -inf.  The splits are summed in a fixed order,
-// so the output is bit-identical from run to run, and the maximum is taken here
-// from the staged lse values (no global running-max buffer, nothing to reset).
+// splits are all empty gets O = 0 and lse = -inf; an lse_s of NaN makes the row
+// NaN.  The splits are summed in a fixed order, so the output is bit-identical
+// from run to run, and the maximum is taken here from the staged lse values (no
+// global running-max buffer, nothing to reset).
 //
 // One warp per row; each lane owns 8 (head_dim 256), 4 (128) or 2 (64)
 // consecutive output elements, read as 32-, 16- or 8-byte vectors per split.
@@ -133,9 +134,9 @@ gqa_combine_kernel(const CombineParams p) {
   if (n <= 64) {
     if (lane >= n) l0 = -INFINITY;
     if (lane + 32 >= n) l1 = -INFINITY;
-    float M = fmaxf(l0, l1);
+    float M = ptx::max_nan(l0, l1);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 16; o >= 1; o >>= 1) M = ptx::max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M != -INFINITY) {
       const float w0 = l0 == -INFINITY ? 0.f : ptx::ex2_approx((l0 - M) * kLog2e);
       const float w1 = l1 == -INFINITY ? 0.f : ptx::ex2_approx((l1 - M) * kLog2e);
@@ -184,9 +185,9 @@ gqa_combine_kernel(const CombineParams p) {
     // many splits: the maximum first, then weights and sums, 32 at a time
     float M = -INFINITY;
     for (int s0 = 0; s0 < n; s0 += 32)
-      if (s0 + lane < n) M = fmaxf(M, lse_at(s0 + lane));
+      if (s0 + lane < n) M = ptx::max_nan(M, lse_at(s0 + lane));
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 16; o >= 1; o >>= 1) M = ptx::max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M != -INFINITY) {
       float W = 0.f;
       for (int s0 = 0; s0 < n; s0 += 32) {

@@ -1079,7 +1079,7 @@ gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
         float M = -INFINITY;
 #pragma unroll
         for (int s2 = 0; s2 < kMaxClusterK; ++s2)
-          if (s2 < static_cast<int>(kc)) M = fmaxf(M, recv_lse[s2 * NPAD + n]);
+          if (s2 < static_cast<int>(kc)) M = ptx::max_nan(M, recv_lse[s2 * NPAD + n]);
         if (M != -INFINITY) {
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           float W = 0.f;
@@ -1547,11 +1547,11 @@ gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
         if (writer) {
           float inv[NC];
 #pragma unroll
-          for (int n = 0; n < NC; ++n) inv[n] = lt[n] > 0.f ? ptx::rcp_approx(lt[n]) : 0.f;
+          for (int n = 0; n < NC; ++n) inv[n] = lt[n] != 0.f ? ptx::rcp_approx(lt[n]) : 0.f;
           float lse_d = -INFINITY;  // the LSE of column d_row, when this thread holds it
 #pragma unroll
           for (int n = 0; n < NC; ++n)
-            if (c0 + n == d_row && lt[n] > 0.f) lse_d = 0.69314718055994531f * (__log2f(lt[n]) - nms8[n]);
+            if (c0 + n == d_row && lt[n] != 0.f) lse_d = 0.69314718055994531f * (__log2f(lt[n]) - nms8[n]);
 #pragma unroll
           for (int h2 = 0; h2 < kRowsOut; ++h2) {
             float vals[NC];
@@ -1570,7 +1570,8 @@ gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
         uint8_t* obuf = obuf_of(static_cast<int>(k_out % NB));
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          const float inv = lt[n] > 0.f ? ptx::rcp_approx(lt[n]) : 0.f;
+          // (a sum of NaN, of a NaN score, is not an empty row: it stays NaN)
+          const float inv = lt[n] != 0.f ? ptx::rcp_approx(lt[n]) : 0.f;
           const int ng = c0 + n;
           if (ng < nv) {
 #pragma unroll
@@ -1594,7 +1595,7 @@ gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
           for (int n = 0; n < NC; ++n)
             if (c0 + n == d_row) { lt_n = lt[n]; m_n = -nms8[n]; }
           lse_of(static_cast<int>(k_out % NB))[d_row] =
-              lt_n > 0.f ? 0.69314718055994531f * (m_n + __log2f(lt_n)) : -INFINITY;
+              lt_n != 0.f ? 0.69314718055994531f * (m_n + __log2f(lt_n)) : -INFINITY;
         }
       }
       if (threadIdx.x == kSoftmaxThread0 + 32) GQA_TRACE_STAMP(ep_ts, TR_EP_SENT - TR_EP_L);

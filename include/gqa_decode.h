@@ -223,7 +223,7 @@ gqa_status_t gqa_decode_splitkv(const gqa_desc_t* desc, const void* q, const voi
  * lse = M + ln sum_s w_s, summing splits in index order (bit-reproducible).
  * Splits with lse_s = -inf are skipped (their o_part values are ignored and
  * may be anything, NaN included); a row with no valid split gets O = 0,
- * lse = -inf.
+ * lse = -inf; an lse_s of NaN makes the row NaN.
  *   o_part    fp32 [num_splits, rows, head_dim], 16-byte aligned
  *   lse_part  fp32 [num_splits, rows]
  *   out       [rows, head_dim] of out_dtype, 16-byte aligned

@@ -263,18 +263,14 @@ def _expect(what, out, lse, want):
         assert ((x - w).abs()[fine] <= t[fine]).all(), (what, (x - w).abs()[fine].max().item())
 
 
-@gpu
-@pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("T", [40, 300], ids=["rows of one tile", "rows of two"])
-@pytest.mark.parametrize("dtype", [BF16, torch.float16], ids=["bf16", "fp16"])
-def test_infinities_and_nan_that_are_seen(dev, T, d, dtype):
+def _check_seen(dev, T, d, dtype, S, call):
     """One head each: scores of -inf (some, whole blocks, all), a NaN in
     K, in V, in one row of q, infinite V.  The other heads are as they were."""
-    K, S = 8, 30000
+    K = 8
     gen = torch.Generator(dev).manual_seed(d)
     q, k, v = _rand(gen, 1, T, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype)
     ln = torch.tensor([S], dtype=torch.int32, device=dev)
-    clean, clean_lse = g.cross_attention(q.abs(), k, v, ln)
+    clean, clean_lse = call(q.abs(), k, v, ln)
     q = q.abs()
     k[0, ::3, 0, 0] = -math.inf           # q is positive: a score of -inf
     k[0, torch.arange(S, device=dev) // 128 % 4 < 2, 1, 5] = -math.inf   # whole blocks, the first ones of many items
@@ -283,7 +279,7 @@ def test_infinities_and_nan_that_are_seen(dev, T, d, dtype):
     v[0, 77, 4, 3] = math.nan
     v[0, S - 1, 5, 4], v[0, 0, 5, 5] = math.inf, -math.inf
     q[0, T // 2, 6, 1] = math.nan
-    out, lse = g.cross_attention(q, k, v, ln)
+    out, lse = call(q, k, v, ln)
     torch.cuda.synchronize()
     assert g.gqa_decode_get_error() == g.GQA_OK
     assert torch.equal(out[:, :, 7], clean[:, :, 7]) and torch.equal(lse[:, :, 7], clean_lse[:, :, 7])
@@ -307,3 +303,43 @@ def test_infinities_and_nan_that_are_seen(dev, T, d, dtype):
             elif h == 6:
                 o[T // 2], l[T // 2] = math.nan, math.nan
         _expect(f"head {h}", out[0, :, h:h + 1], lse[0, :, h:h + 1], (o, l, to, tl))
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T", [40, 300], ids=["rows of one tile", "rows of two"])
+@pytest.mark.parametrize("dtype", [BF16, torch.float16], ids=["bf16", "fp16"])
+def test_infinities_and_nan_that_are_seen(dev, T, d, dtype):
+    _check_seen(dev, T, d, dtype, 30000, g.cross_attention)
+
+
+WAYS = {"cross attention": g.cross_attention, "one split": lambda *a: g.decode(*a, num_splits=1),
+        "combine": lambda *a: g.decode(*a, num_splits=5, reduction="combine"),
+        "many splits": lambda *a: g.decode(*a, num_splits=64, reduction="combine"),
+        "cluster": lambda *a: g.decode(*a, num_splits=4, reduction="cluster")}
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 9, 32])
+@pytest.mark.parametrize("way", WAYS)
+def test_infinities_and_nan_that_few_rows_see(dev, way, T, d):
+    """The decode kernel, whose result few rows have, and each of its merges."""
+    for dtype, S in ((BF16, 20000), (torch.float16, 1300)):
+        _check_seen(dev, T, d, dtype, S, WAYS[way])
+
+
+@gpu
+def test_a_partial_of_nan_is_not_an_empty_one(dev):
+    """gqa_decode_combine: an LSE of NaN beside empty splits, and beside full ones, in both of its loops."""
+    for n in (3, 64):
+        o = torch.randn(n, 4, 64, device=dev)
+        lse = torch.zeros(n, 4, device=dev)
+        lse[:, 0] = -math.inf
+        lse[1, 0] = lse[1, 1] = math.nan
+        lse[:, 2] = -math.inf
+        out, l = torch.empty(4, 64, device=dev), torch.empty(4, device=dev)
+        g.gqa_decode_combine(o, lse, out, l)
+        assert torch.isnan(out[:2]).all() and torch.isnan(l[:2]).all()
+        assert (out[2] == 0).all() and l[2] == -math.inf
+        assert torch.isfinite(out[3]).all() and torch.isfinite(l[3])
