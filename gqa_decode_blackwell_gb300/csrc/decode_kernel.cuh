@@ -756,17 +756,16 @@ gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
         }
       }
       for (int hf = 0; hf < TPB && ok && have_prev; ++hf) ok = load_tile(true, pb, ph, pblk, hf);
-      if (!ok) {
-        detail::set_error(p.err_word, kErrTimeout, abort_flag);
-        // let the copies already issued land before the CTA exits
-        for (uint32_t u = tk > NSK ? tk - NSK : 0u; u < tk; ++u)
-          ptx::mbar_wait_bounded(BAR(RING_FULL + u % NSK), (u / NSK) & 1u, nullptr, p.timeout_ns);
-        for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
-          ptx::mbar_wait_bounded(BAR(RING_FULL + NSK + u % NSV), (u / NSV) & 1u, nullptr, p.timeout_ns);
-        for (int k = (kq > static_cast<int>(NB) ? kq - static_cast<int>(NB) : 0); k < kq; ++k)
-          ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(static_cast<uint32_t>(k) % NB)),
-                                 (static_cast<uint32_t>(k) / NB) & 1u, nullptr, p.timeout_ns);
-      }
+      if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
+      // The copies issued last land before the CTA exits, whether this thread
+      // gave up or another role does while they are on their way.
+      for (uint32_t u = tk > NSK ? tk - NSK : 0u; u < tk; ++u)
+        ptx::mbar_wait_bounded(BAR(RING_FULL + u % NSK), (u / NSK) & 1u, nullptr, p.timeout_ns);
+      for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
+        ptx::mbar_wait_bounded(BAR(RING_FULL + NSK + u % NSV), (u / NSV) & 1u, nullptr, p.timeout_ns);
+      for (int k = (kq > static_cast<int>(NB) ? kq - static_cast<int>(NB) : 0); k < kq; ++k)
+        ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(static_cast<uint32_t>(k) % NB)),
+                               (static_cast<uint32_t>(k) / NB) & 1u, nullptr, p.timeout_ns);
     }
     __syncwarp();
   }
