@@ -312,6 +312,11 @@ gqa_status_t check_cross(const gqa_desc_t* d) {
   return rows > 0 && d->q_tokens > INT_MAX / rows ? GQA_ERR_UNSUPPORTED : GQA_OK;
 }
 
+// The rows of a sequence's own keys, all there are of a causal section, are one
+// tile, or the same in both (split_keys): the kernel's causal limit is a row's
+// place in its tile.
+static_assert(2 * GQA_MAX_QROWS <= kTileRows, "a sequence's own rows are split by keys, never by tokens");
+
 // The prefix as a problem of its own: one entry of B * nq tokens.
 gqa_status_t check_prefix(const gqa_desc_t* d, int max_prefix, gqa_desc_t* prefix) {
   const gqa_status_t rc = check_desc(d);

@@ -583,7 +583,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       const int first_lane = t == 1 ? p.s[it.section].shift : 0;
       const int rr = r - first_lane;                   // the row within the tile
       const bool active = rr >= lane && rr - lane < rows;  // this warp holds any of them
-      // the last key this row sees is L - 1, or (causal) L - nq + its token
+      // the last key this row sees is L - 1, or (causal) L - nq + its token; all
+      // tokens of a causal section are in one tile, and both hold that one (check_prefix)
       const int causal_cut = p.s[it.section].causal != 0 ? p.s[it.section].nq - 1 : 0;
       const int sees = it.L - causal_cut + (causal_cut != 0 ? it.tok0 + rr / p.G : 0);
       const int step = split_keys ? 2 : 1, i0 = split_keys ? t : 0;

@@ -343,3 +343,14 @@ def test_a_partial_of_nan_is_not_an_empty_one(dev):
         assert torch.isnan(out[:2]).all() and torch.isnan(l[:2]).all()
         assert (out[2] == 0).all() and l[2] == -math.inf
         assert torch.isfinite(out[3]).all() and torch.isfinite(l[3])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_own_keys_behind_a_prefix_have_one_tile_of_rows(d):
+    """The kernel's causal limit is a row's place in its tile: a second tile
+    must hold the same rows, whatever the group and the tokens."""
+    for G in range(1, 33):
+        for nq in {1, 32 // G}:
+            desc = _desc(batch=3, q_tokens=nq, q_heads=2 * G, kv_heads=2, head_dim=d, max_seqlen=700, causal=1)
+            _, _, info, _ = g.gqa_shared_keys_plan(desc, [700, 0, 3], 500, 600, 152)
+            assert info[1, 0] == nq and info[1, 1] == 1 and info[1, 2] == (d != 256)
