@@ -536,7 +536,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         if (!more) break;
       }
       if (!ok) detail::set_error(p.err_word, kErrTimeout, abort_flag);
-      // after a timeout too, so that the merge never reads what an earlier call left
+      // After a timeout too: the merge then finds places within this launch's
+      // partials, though what they hold may be an earlier call's.  Where every
+      // triple leaves partials it ignores records that name others.  The output
+      // is invalid in either case, and the error word says so.
       if (p.every_piece == 0 && p.rec != nullptr &&
           detail::write_ok(p.err_word, p.rec, p.rec_bytes, p.rec + blockIdx.x, sizeof(int2)))
         p.rec[blockIdx.x] = cut;
