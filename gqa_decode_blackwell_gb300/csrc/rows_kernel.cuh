@@ -767,7 +767,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         }
         continue;
       }
-      const int r_tok = r / p.G, tok = it.tok0 + (split_keys ? 0 : t * sec.tokens) + r_tok;
+      // (final rows are never of split or shifted tiles, which leave partials)
+      const int r_tok = r / p.G, tok = it.tok0 + t * sec.tokens + r_tok;
       const bool row_valid = r_tok < sec.tokens && tok < sec.nq;
       const long long row = (static_cast<long long>(it.b) * sec.nq + tok) * p.Hq + it.h * p.G + (r - r_tok * p.G);
       const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // a row that saw only -inf scores: 0; NaN stays NaN
