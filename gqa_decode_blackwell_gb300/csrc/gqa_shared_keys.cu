@@ -25,7 +25,8 @@ namespace {
 // tuned on whole calls, not times: only the ratios within a launch matter, and a
 // launch has blocks of at most two kinds.  (A two-tile block, 14, takes ~1.7 us;
 // one at head_dim 256, 8, ~1.4 us: both sections of such a launch have that one.)
-// Measured on GB300, us per call, with the units of a split block and item beside:
+// Measured on one GB300, us per call, with the units of a split block and item
+// beside (the first line on another: 188, 312, 140, 27.1):
 //   7, 16 (here)   128 sequences of up to 2048 keys behind 32768 (64 / 8 heads of
 //                  128) 185; 1020 of 200 behind 2000 (32 / 8) 326; 256 of 400
 //                  behind 16000 144; 32 of up to 512 behind 4000 28.1

@@ -38,8 +38,9 @@
 // The two add up rather than overlap: without exponentials, maxima and sums
 // (wrong results, to see) the kernel is only 8% faster, since a QK that shares
 // shared memory with an arriving block takes 750-950 cycles and not 516.  2048
-// tokens of 32 heads against 8192 keys, 4 of them, run at 1.4 PFLOP/s (763-790
-// us, by box).  At head_dim 256 the one tile takes its K and V, 64 bytes a
+// tokens of 32 heads against 8192 keys, 4 of them, run at 1.4 PFLOP/s (767-794
+// us, by box; 866 a call in a loop long enough for the card's power limit, which
+// takes the clock from 2070 to ~1650 MHz).  At head_dim 256 the one tile takes its K and V, 64 bytes a
 // clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of 16
 // heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
 // few, a block costs what its chain takes (~1900 cycles, split between two
@@ -136,7 +137,9 @@ constexpr uint64_t kBlockNs = 20000;  // far more than a key block of an item ta
 // last group of rows fills one tile only, which leave the items they have no
 // part in at once and then wait for the next one, or for its first scores.  So
 // every wait may take as long as that, beside its timeout.
-GQA_HD uint64_t items_in_ring_ns(int max_len) { return static_cast<uint64_t>(num_blocks(max_len)) * kItemRing * kBlockNs; }
+GQA_HD uint64_t items_in_ring_ns(int max_len) {
+  return static_cast<uint64_t>(num_blocks(max_len)) * kItemRing * kBlockNs;
+}
 
 template <int HEAD_DIM>
 struct RowsCfg {

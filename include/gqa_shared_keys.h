@@ -13,8 +13,16 @@
  *
  * per query row r over the keys j that it sees; a row that sees none yields
  * O = 0, lse = -inf.  Scores, softmax and sums are fp32, P enters the value
- * MMA in in_dtype, as in the decode kernel.  Results are bit-identical from
- * run to run.
+ * MMA in in_dtype, as in the decode kernel.  The MMA's fp32 accumulator
+ * truncates: a CTA that adds up n blocks of 128 keys leaves O up to ~5e-7 n
+ * (relative to the weighted |v|) too small, 2e-4 at 64000 keys.  Results are
+ * bit-identical from run to run.
+ *
+ * A score of NaN makes its row NaN, O and lse; one of -inf is a key that is not
+ * seen; one of +inf makes the row NaN.  V's infinities and NaN reach O of every
+ * row that sees their key, and of those from which only the causal mask hides
+ * it: their weight is 0, and 0 * NaN is NaN.  What lies past a length is never
+ * used, whatever it is.
  *
  * The conventions of gqa_decode.h hold: device pointers, caller-owned memory,
  * dense row-major tensors, asynchronous on `stream`, checked before anything
@@ -66,8 +74,9 @@ gqa_status_t gqa_cross_attn(const gqa_desc_t* desc, const void* q, const void* k
  * the keys of the prefix, [0, P), and then its own, [0, L_b) of its cache; the
  * softmax runs over both together.  desc describes the decode step as in
  * gqa_decode_attn (max_seqlen: the capacity of the sequences' own caches;
- * q_tokens * q_heads / kv_heads <= GQA_MAX_QROWS); reduction must be
- * GQA_REDUCE_AUTO.  The causal flag masks among a sequence's own keys (its nq
+ * q_tokens * q_heads / kv_heads <= GQA_MAX_QROWS, as there: the rows of a
+ * sequence's own keys are then one tile, on which the causal mask and the split
+ * of its keys rely); reduction must be GQA_REDUCE_AUTO.  The causal flag masks among a sequence's own keys (its nq
  * new tokens are the last of them; token t sees j <= L_b - nq + t); the prefix
  * is seen by every token.
  *   k_prefix, v_prefix  in_dtype [max_prefix, Hkv, d], 16-byte aligned

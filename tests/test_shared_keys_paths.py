@@ -24,7 +24,8 @@ def _sample(out, lse, q, k, v, b, tokens, L):
     """Rows of some tokens of entry b against all its L keys."""
     at = torch.tensor(tokens, device=q.device)
     sees = torch.ones(len(tokens), L, dtype=torch.bool, device=q.device)
-    want = _attend(q[b, at].double(), k[b, :L].double(), v[b, :L].double(), sees, q.shape[3] ** -0.5, q.dtype, out.dtype)
+    want = _attend(q[b, at].double(), k[b, :L].double(), v[b, :L].double(), sees, q.shape[3] ** -0.5, q.dtype,
+                   out.dtype)
     _compare(f"entry {b}", out[b:b + 1, at], lse[b:b + 1, at], [want])
 
 
@@ -80,7 +81,8 @@ CLIMBS = [  # T, H, K, S of one entry; which items the case is for
 @pytest.mark.parametrize("name,T,H,K,S", CLIMBS, ids=[c[0] for c in CLIMBS])
 def test_maxima_that_climb_within_items(dev, name, T, H, K, S, dtype, d):
     gen = torch.Generator(dev).manual_seed(d)
-    q, k, v = _rand(gen, 1, T, H, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype)
+    q = _rand(gen, 1, T, H, d, dtype=dtype)
+    k, v = _rand(gen, 1, S, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype)
     _staircase(q, k, v)
     ln = torch.tensor([S], dtype=torch.int32, device=dev)
     info, items = _items(q, k, [S])
@@ -265,10 +267,11 @@ def _expect(what, out, lse, want):
 
 def _check_seen(dev, T, d, dtype, S, call):
     """One head each: scores of -inf (some, whole blocks, all), a NaN in
-    K, in V, in one row of q, infinite V.  The other heads are as they were."""
-    K = 8
+    K, in V, in one row of q, infinite V, a score of +inf.  Another head is as it was."""
+    K = 9
     gen = torch.Generator(dev).manual_seed(d)
-    q, k, v = _rand(gen, 1, T, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype)
+    q = _rand(gen, 1, T, K, d, dtype=dtype)
+    k, v = _rand(gen, 1, S, K, d, dtype=dtype), _rand(gen, 1, S, K, d, dtype=dtype)
     ln = torch.tensor([S], dtype=torch.int32, device=dev)
     clean, clean_lse = call(q.abs(), k, v, ln)
     q = q.abs()
@@ -279,6 +282,7 @@ def _check_seen(dev, T, d, dtype, S, call):
     v[0, 77, 4, 3] = math.nan
     v[0, S - 1, 5, 4], v[0, 0, 5, 5] = math.inf, -math.inf
     q[0, T // 2, 6, 1] = math.nan
+    k[0, 1000, 8, 3] = math.inf
     out, lse = call(q, k, v, ln)
     torch.cuda.synchronize()
     assert g.gqa_decode_get_error() == g.GQA_OK
@@ -294,7 +298,7 @@ def _check_seen(dev, T, d, dtype, S, call):
         else:                              # bounds from finite stand-ins, values as they come
             zq, zk, zv = (torch.where(torch.isfinite(x), x, 0.0) for x in (qd, kd, vd))
             o, l, to, tl = _attend(zq, zk, zv, sees, d ** -0.5, dtype, dtype)
-            if h == 3:
+            if h in (3, 8):
                 o, l = torch.full_like(o, math.nan), torch.full_like(l, math.nan)
             elif h == 4:
                 o[..., 3] = math.nan
