@@ -38,8 +38,8 @@
 // The two add up rather than overlap: without exponentials, maxima and sums
 // (wrong results, to see) the kernel is only 8% faster, since a QK that shares
 // shared memory with an arriving block takes 750-950 cycles and not 516.  2048
-// tokens of 32 heads against 8192 keys, 4 of them, run at 1.4 PFLOP/s (767-794
-// us, by box; 866 a call in a loop long enough for the card's power limit, which
+// tokens of 32 heads against 8192 keys, 4 of them, run at 1.4 PFLOP/s (769-794
+// us, by box; 871 a call in a loop long enough for the card's power limit, which
 // takes the clock from 2070 to ~1650 MHz).  At head_dim 256 the one tile takes its K and V, 64 bytes a
 // clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of 16
 // heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
