@@ -1,5 +1,5 @@
-"""Python binding of the GB300 GQA decode library (``include/gqa_decode.h`` and
-``include/gqa_shared_keys.h``).
+"""Python binding of the GB300 GQA decode library (``include/gqa_decode.h``,
+``include/gqa_shared_keys.h`` and ``include/gqa_paged.h``).
 
 Argument marshalling only: every function below turns PyTorch tensors into
 the plain pointers and sizes of the C entry point of the same name and calls
@@ -16,7 +16,7 @@ import re
 import threading
 from typing import Optional
 
-from .build import HEADER, LIB, SHARED_KEYS_HEADER
+from .build import HEADER, LIB, PAGED_HEADER, SHARED_KEYS_HEADER
 
 GQA_OK = 0
 GQA_ERR_INVALID_ARG = 1
@@ -26,6 +26,7 @@ GQA_ERR_CUDA = 4
 GQA_ERR_TIMEOUT = 5
 GQA_ERR_BAD_SEQLEN = 6
 GQA_ERR_BOUNDS = 7
+GQA_ERR_BAD_INDEX = 8
 GQA_DTYPE_BF16 = 0
 GQA_DTYPE_FP32 = 1
 GQA_DTYPE_FP16 = 2
@@ -33,6 +34,9 @@ GQA_REDUCE_AUTO = 0
 GQA_REDUCE_COMBINE = 1
 GQA_REDUCE_CLUSTER = 2
 _REDUCTIONS = {"auto": GQA_REDUCE_AUTO, "combine": GQA_REDUCE_COMBINE, "cluster": GQA_REDUCE_CLUSTER}
+
+GQA_MAX_TREE_TOKENS = 256
+_ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 _lock = threading.Lock()
 _lib = None
@@ -57,6 +61,26 @@ class gqa_desc_t(ctypes.Structure):
         ("out_dtype", ctypes.c_int),
         ("in_dtype", ctypes.c_int),
         ("reduction", ctypes.c_int),
+    ]
+
+
+class gqa_pages_t(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+        ("page_stride", ctypes.c_int64),
+        ("pos_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class gqa_rotary_t(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("inverse", ctypes.c_int),
+        ("magnitude", ctypes.c_float),
     ]
 
 
@@ -112,6 +136,21 @@ def load_library(path: str) -> ctypes.CDLL:
     L.gqa_shared_keys_plan.argtypes = [D, I, I, P, I, ctypes.POINTER(I), ctypes.POINTER(I), P, P, I64,
                                        ctypes.POINTER(I64)]
     L.gqa_shared_keys_plan.restype = I
+    G, R, F64 = ctypes.POINTER(gqa_pages_t), ctypes.POINTER(gqa_rotary_t), ctypes.c_double
+    L.gqa_rotary_turns.argtypes = [I, F64, I, F64, I, F64, F64, P]
+    L.gqa_rotary_turns.restype = I
+    L.gqa_rotary_apply.argtypes = [R, P, P, I64, I, I, I, P, I64, P, I64, P]
+    L.gqa_rotary_apply.restype = I
+    L.gqa_paged_append.argtypes = [D, G, R, P, P, P, I64, P, I64, P, I64, P, P, P, P, P, P, P]
+    L.gqa_paged_append.restype = I
+    L.gqa_tree_from_parents.argtypes = [I, I, I, P, P, P, P, P, P]
+    L.gqa_tree_from_parents.restype = I
+    L.gqa_tree_workspace_size.argtypes = [D, G]
+    L.gqa_tree_workspace_size.restype = SZ
+    L.gqa_tree_attn.argtypes = [D, G, P, P, P, P, P, P, P, P, P, P, SZ, P]
+    L.gqa_tree_attn.restype = I
+    L.gqa_paged_keep.argtypes = [D, G, P, P, P, P, P, P, I, P, P, P]
+    L.gqa_paged_keep.restype = I
     return L
 
 
@@ -368,12 +407,19 @@ def _check_call(device, q, keys, lengths, out, lse, workspace, stream):
         raise ValueError("lse must be contiguous fp32 [B, nq, Hq] on q's device")
     if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != device):
         raise ValueError("workspace must be contiguous and on q's device")
+    return _raw_stream(stream, device)
+
+
+def _raw_stream(stream, device) -> int:
+    """The cudaStream_t of a call on `device` (None: torch's current stream there)."""
+    import torch
+
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
     if not hasattr(stream, "cuda_stream"):
         return int(stream)
     if stream.device.index != device:
-        raise ValueError(f"the stream is on {stream.device}, not on q's device")
+        raise ValueError(f"the stream is on {stream.device}, not on cuda:{device}")
     return stream.cuda_stream
 
 
@@ -434,16 +480,20 @@ def gqa_prefix_attn(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens
         raise GQAError(rc, "gqa_prefix_attn")
 
 
+def _torch_stream(stream, device):
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
 def _allocate(q, out_dtype, workspace_bytes, stream):
     """out, lse and a workspace of the call's own stream, so that the caching
     allocator hands none of them on while that stream still uses it."""
     import torch
 
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    elif not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=q.device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, q.device)):
         out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
         ws = torch.empty(workspace_bytes, dtype=torch.uint8, device=q.device) if workspace_bytes else None
@@ -487,3 +537,258 @@ def gqa_shared_keys_plan(desc: gqa_desc_t, kv_lens_host, prefix_len: int = 0, ma
     items = np.zeros((n.value, 9), dtype=np.int32)
     call(items, n.value)
     return nc.value, bool(every.value), info, items
+
+
+# ------------------------------------------------------- include/gqa_paged.h
+def rotary_turns(dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                 original_length: int = 0, slow: float = 1.0, fast: float = 32.0, device=None):
+    """The table the rotation turns by, int64 [dim / 2] (the bits of the C table's
+    uint64) on ``device``; scaling "none", "linear", "base" or "parts", see
+    gqa_rotary_scaling_t in ``include/gqa_paged.h``."""
+    import torch
+
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALINGS)}")
+    turns = torch.empty(max(int(dim) // 2, 1), dtype=torch.int64)
+    _check(lib().gqa_rotary_turns(int(dim), float(base), _ROTARY_SCALINGS[scaling], float(factor),
+                                  int(original_length), float(slow), float(fast), turns.data_ptr()),
+           "gqa_rotary_turns")
+    return turns if device is None else turns.to(device)
+
+
+def _on(t, device, what, dtype=None, shape=None):
+    """t, checked to be a contiguous tensor on `device` of this type and shape."""
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and on cuda:{device}")
+    return t.data_ptr()
+
+
+def _optional(t, device, what, dtype, shape):
+    return None if t is None else _on(t, device, what, dtype, shape)
+
+
+def _token_stride(t, what) -> int:
+    """Elements from token to token of t [..., tokens, heads, d]: dense heads, one stride for all tokens."""
+    heads, d = t.shape[-2:]
+    strides, sizes = t.stride(), t.shape
+    if (d > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != d):
+        raise ValueError(f"{what} must have dense heads")
+    stride, run = None, 1  # from the last token dimension outwards
+    for size, st in zip(reversed(sizes[:-2]), reversed(strides[:-2])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * run:
+            raise ValueError(f"{what} must have one stride from token to token")
+        run *= size
+    return heads * d if stride is None else stride
+
+
+def _device_of(t, what) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return device
+
+
+def _rope(turns, device, interleaved, inverse, magnitude):
+    import torch
+
+    if turns.dtype is not torch.int64 or turns.dim() != 1:
+        raise ValueError("turns must be the int64 table of rotary_turns")
+    return (gqa_rotary_t(2 * turns.shape[0], 1 if interleaved else 0, 1 if inverse else 0, float(magnitude)),
+            _on(turns, device, "turns"))
+
+
+def gqa_rotary_apply(x, positions, turns, out, *, interleaved: bool = False, inverse: bool = False,
+                     magnitude: float = 0.0, stream=None) -> None:
+    """Rotates x [..., heads, d] to positions int32 [...] into ``out`` (x itself, or
+    apart from it); see gqa_rotary_apply in ``include/gqa_paged.h``."""
+    import torch
+
+    device = _device_of(x, "x")
+    code = _type_codes().get(x.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if x.dim() < 3 or out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != device:
+        raise ValueError("x must be [..., heads, d], and out of its type and shape and on its device")
+    rope, table = _rope(turns, device, interleaved, inverse, magnitude)
+    at = _on(positions, device, "positions", torch.int32, x.shape[:-2])
+    rc = _on_device(device, lib().gqa_rotary_apply, ctypes.byref(rope), table, at, positions.numel(), x.shape[-2],
+                    x.shape[-1], code, x.data_ptr(), _token_stride(x, "x"), out.data_ptr(),
+                    _token_stride(out, "out"), _raw_stream(stream, device))
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_rotary_apply")
+
+
+def rotary(x, positions, turns, *, interleaved: bool = False, inverse: bool = False, magnitude: float = 0.0,
+           stream=None):
+    """Allocates the result with torch and calls gqa_rotary_apply."""
+    import torch
+
+    with torch.cuda.stream(_torch_stream(stream, x.device)):
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    gqa_rotary_apply(x, positions, turns, out, interleaved=interleaved, inverse=inverse, magnitude=magnitude,
+                     stream=stream)
+    return out
+
+
+def _paged(k_cache, v_cache, page_table, device, batch, dtype):
+    """Geometry of the caches [pages, page_size, kv_heads, d] (any strides but the last)."""
+    import torch
+
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("the caches must be [pages, page_size, kv_heads, d], alike in shape and strides")
+    for t in (k_cache, v_cache):
+        if t.dtype is not dtype or t.get_device() != device or t.stride(3) != 1:
+            raise ValueError("the caches must be of the inputs' type, on their device, with dense heads")
+    if page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError(f"page_table must be [{batch}, pages of a sequence]")
+    _on(page_table, device, "page_table", torch.int32)
+    pages, size, _, d = k_cache.shape
+    strides = [n if k > 1 else d for n, k in zip(k_cache.stride(), k_cache.shape)]  # (of one element: not used)
+    return gqa_pages_t(pages, size, page_table.shape[1], strides[0], strides[1], strides[2])
+
+
+def _paged_desc(batch, tokens, q_heads, k_cache, page_table, *, out_dtype=None, scale=0.0, causal=False):
+    codes = _type_codes()
+    code = codes.get(k_cache.dtype)
+    if code is None or code == GQA_DTYPE_FP32:
+        raise ValueError(f"the caches must be bf16 or fp16, not {k_cache.dtype}")
+    out_code = code if out_dtype is None else codes.get(out_dtype)
+    if out_code is None:
+        raise ValueError(f"unsupported output type {out_dtype}")
+    room = min(page_table.shape[1] * k_cache.shape[1], 1 << 30)
+    return gqa_desc_t(batch, tokens, q_heads, k_cache.shape[2], k_cache.shape[3], room, scale, 1 if causal else 0,
+                      out_code, code, GQA_REDUCE_AUTO)
+
+
+def gqa_paged_append(q, k, v, q_out, k_cache, v_cache, page_table, seqlens, *, new_lens=None, positions=None,
+                     turns=None, interleaved: bool = False, magnitude: float = 0.0, stream=None) -> None:
+    """Rotates the new tokens' q [B, nq, Hq, d] into ``q_out`` and puts k (rotated)
+    and v [B, nq, Hkv, d] into the paged caches; q, k and v may be views of one
+    tensor, q and q_out may be None, turns None rotates nothing.  See
+    gqa_paged_append in ``include/gqa_paged.h``."""
+    import torch
+
+    device = _device_of(k, "k")
+    if k.dim() != 4 or v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != device:
+        raise ValueError("k and v must be [B, nq, kv_heads, d], of one type and device")
+    B, nq, heads, d = k.shape
+    if tuple(k_cache.shape[2:]) != (heads, d):
+        raise ValueError(f"k {tuple(k.shape)} and cache {tuple(k_cache.shape)} disagree")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    geometry = _paged(k_cache, v_cache, page_table, device, B, k.dtype)
+    q_at, q_stride, out_at, q_heads = None, 0, None, heads
+    if q is not None:
+        if q.dim() != 4 or tuple(q.shape[:2]) != (B, nq) or q.shape[3] != d or q.dtype is not k.dtype \
+                or q.get_device() != device:
+            raise ValueError("q must be [B, nq, q_heads, d], of k's type and on its device")
+        q_at, q_stride, q_heads = q.data_ptr(), _token_stride(q, "q"), q.shape[2]
+        out_at = _on(q_out, device, "q_out", q.dtype, q.shape)
+    rope = table = None
+    if turns is not None:
+        rope, table = _rope(turns, device, interleaved, False, magnitude)
+        rope = ctypes.byref(rope)
+    desc = _paged_desc(B, nq, q_heads, k_cache, page_table)
+    rc = _on_device(device, lib().gqa_paged_append, ctypes.byref(desc), ctypes.byref(geometry), rope, table,
+                    _optional(positions, device, "positions", torch.int32, (B, nq)), q_at, q_stride, k.data_ptr(),
+                    _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), out_at, k_cache.data_ptr(),
+                    v_cache.data_ptr(), page_table.data_ptr(), _on(seqlens, device, "seqlens", torch.int32, (B,)),
+                    _optional(new_lens, device, "new_lens", torch.int32, (B,)), _raw_stream(stream, device))
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_paged_append")
+
+
+def gqa_tree_from_parents(parents, seqlens, tree, positions=None, *, new_lens=None, max_seqlen: int = 1 << 30,
+                          stream=None) -> None:
+    """The drafts' tree of parents int32 [B, nq] as bits, int32 [B, nq, ceil(nq / 32)],
+    and their positions int32 [B, nq]; see gqa_tree_from_parents in
+    ``include/gqa_paged.h``."""
+    import torch
+
+    device = _device_of(parents, "parents")
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, nq]")
+    B, nq = parents.shape
+    rc = _on_device(device, lib().gqa_tree_from_parents, B, nq, int(max_seqlen),
+                    _on(parents, device, "parents", torch.int32), _on(seqlens, device, "seqlens", torch.int32, (B,)),
+                    _optional(new_lens, device, "new_lens", torch.int32, (B,)),
+                    _on(tree, device, "tree", torch.int32, (B, nq, (nq + 31) // 32)),
+                    _optional(positions, device, "positions", torch.int32, (B, nq)), _raw_stream(stream, device))
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_tree_from_parents")
+
+
+def _tree_problem(q, k_cache, v_cache, page_table, out_dtype, scale=0.0, causal=False):
+    device = _device_of(q, "q")
+    if q.dim() != 4 or k_cache.dim() != 4 or q.shape[3] != k_cache.shape[3]:
+        raise ValueError(f"q {tuple(q.shape)} and cache {tuple(k_cache.shape)} disagree")
+    geometry = _paged(k_cache, v_cache, page_table, device, q.shape[0], q.dtype)
+    desc = _paged_desc(q.shape[0], q.shape[1], q.shape[2], k_cache, page_table, out_dtype=out_dtype, scale=scale,
+                       causal=causal)
+    return desc, geometry, device
+
+
+def gqa_tree_workspace_size(q, k_cache, page_table, *, out_dtype=None) -> int:
+    """Bytes gqa_tree_attn needs for q [B, nq, Hq, d] over the paged caches."""
+    desc, geometry, device = _tree_problem(q, k_cache, k_cache, page_table, out_dtype)
+    return int(_on_device(device, lib().gqa_tree_workspace_size, ctypes.byref(desc), ctypes.byref(geometry)))
+
+
+def gqa_tree_attn(q, k_cache, v_cache, page_table, seqlens, out, lse=None, workspace=None, *, new_lens=None,
+                  tree=None, causal: bool = False, scale: float = 0.0, stream=None) -> None:
+    """Attention of new tokens over the paged caches into ``out`` (and ``lse``); see
+    gqa_tree_attn in ``include/gqa_paged.h``."""
+    import torch
+
+    desc, geometry, device = _tree_problem(q, k_cache, v_cache, page_table, out.dtype, scale, causal)
+    B, nq = q.shape[:2]
+    raw = _check_call(device, q, (), ((seqlens, B),), out, lse, workspace, stream)
+    rc = _on_device(device, lib().gqa_tree_attn, ctypes.byref(desc), ctypes.byref(geometry), q.data_ptr(),
+                    k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), seqlens.data_ptr(),
+                    _optional(new_lens, device, "new_lens", torch.int32, (B,)),
+                    _optional(tree, device, "tree", torch.int32, (B, nq, (nq + 31) // 32)), out.data_ptr(),
+                    _ptr(lse), _ptr(workspace), _bytes_of(workspace), raw)
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_tree_attn")
+
+
+def tree_attention(q, k_cache, v_cache, page_table, seqlens, *, new_lens=None, tree=None, causal: bool = False,
+                   scale: float = 0.0, out_dtype=None, stream=None):
+    """Allocates out / lse / workspace with torch and calls gqa_tree_attn."""
+    ws_bytes = gqa_tree_workspace_size(q, k_cache, page_table, out_dtype=out_dtype)
+    out, lse, ws = _allocate(q, out_dtype, ws_bytes, stream)
+    gqa_tree_attn(q, k_cache, v_cache, page_table, seqlens, out, lse, ws, new_lens=new_lens, tree=tree, causal=causal,
+                  scale=scale, stream=stream)
+    return out, lse
+
+
+def gqa_paged_keep(k_cache, v_cache, page_table, seqlens, path, keep_lens, seqlens_out=None, *, tokens: int,
+                   new_lens=None, stream=None) -> None:
+    """Moves each sequence's accepted branch, path int32 [B, n] of which keep_lens
+    [B] count, together behind the positions before its new tokens (``tokens`` of
+    them, or new_lens); seqlens_out int32 [B] gets the new lengths and may be
+    seqlens.  See gqa_paged_keep in ``include/gqa_paged.h``."""
+    import torch
+
+    device = _device_of(k_cache, "k_cache")
+    if path.dim() != 2:
+        raise ValueError("path must be [B, n]")
+    B = path.shape[0]
+    geometry = _paged(k_cache, v_cache, page_table, device, B, k_cache.dtype)
+    desc = _paged_desc(B, int(tokens), k_cache.shape[2], k_cache, page_table)
+    rc = _on_device(device, lib().gqa_paged_keep, ctypes.byref(desc), ctypes.byref(geometry), k_cache.data_ptr(),
+                    v_cache.data_ptr(), page_table.data_ptr(), _on(seqlens, device, "seqlens", torch.int32, (B,)),
+                    _optional(new_lens, device, "new_lens", torch.int32, (B,)),
+                    _on(path, device, "path", torch.int32), path.shape[1],
+                    _on(keep_lens, device, "keep_lens", torch.int32, (B,)),
+                    _optional(seqlens_out, device, "seqlens_out", torch.int32, (B,)), _raw_stream(stream, device))
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_paged_keep")

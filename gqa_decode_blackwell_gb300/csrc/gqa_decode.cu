@@ -15,6 +15,7 @@
 #include "decode_kernel.cuh"
 #include "decode_launch.h"
 #include "host.h"
+#include "paged.h"
 #include "plan.cuh"
 
 namespace gqa {
@@ -93,14 +94,14 @@ static unsigned long long* g_trace_buf = nullptr;  // attached by gqa_trace_atta
 // that it was compiled to the register count (0: any) its warps share out.
 gqa_status_t ensure_smem_attr(DeviceState* st, unsigned bit, const void* fn, int bytes, int regs) {
   std::lock_guard<std::mutex> lk(g_mu);
-  if (st->attr_done & (1u << bit)) return GQA_OK;
+  if (st->attr_done & (1ull << bit)) return GQA_OK;
   if (regs != 0) {
     cudaFuncAttributes a;
     if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs != regs) return GQA_ERR_CUDA;
   }
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GQA_ERR_CUDA;
-  st->attr_done |= 1u << bit;
+  st->attr_done |= 1ull << bit;
   return GQA_OK;
 }
 
@@ -732,6 +733,7 @@ gqa_status_t gqa_decode_get_error(int clear) {
   }
   if (bits & kErrTimeout) return GQA_ERR_TIMEOUT;
   if (bits & kErrBounds) return GQA_ERR_BOUNDS;
+  if (bits & kErrBadIndex) return GQA_ERR_BAD_INDEX;
   if (bits & kErrBadSeqlen) return GQA_ERR_BAD_SEQLEN;
   return GQA_OK;
 }
@@ -745,6 +747,7 @@ const char* gqa_status_string(gqa_status_t status) {
     case GQA_ERR_CUDA: return "CUDA runtime error";
     case GQA_ERR_TIMEOUT: return "a kernel wait timed out";
     case GQA_ERR_BAD_SEQLEN: return "sequence length out of range (clamped)";
+    case GQA_ERR_BAD_INDEX: return "a page, parent, branch or number of new tokens out of range";
     case GQA_ERR_BOUNDS: return "a write or tile outside its buffer was caught (debug build)";
   }
   return "unknown status";

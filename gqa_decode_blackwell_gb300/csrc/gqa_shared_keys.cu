@@ -11,6 +11,7 @@
 
 #include "../../include/gqa_shared_keys.h"
 #include "host.h"
+#include "rows_host.h"
 #include "rows_kernel.cuh"
 #include "rows_launch.h"
 #include "rows_merge.cuh"
@@ -67,21 +68,8 @@ bool split_keys(const gqa_desc_t& d, int tiles) {
   return tiles == 2 && d.q_tokens <= tokens && (d.head_dim == 64 || d.q_tokens * G <= kTileRows / 2);
 }
 
-// One launch of the rows kernel: its sections, its plan and where each
-// section's pieces and records go.
-struct RowsLaunch {
-  int head_dim, q_heads, kv_heads, in_dtype, out_dtype;
-  float scale;
-  int n;                  // sections
-  gqa_desc_t d[2];        // each section as a problem of its own
-  struct { int tokens, groups, split_keys, shift, triples; long long pieces, part_row, rec; } s[2];
-  RowsPlan plan;
-  bool every_piece;
-  long long part_rows, records;
-  gqa_status_t status;
-};
+}  // namespace
 
-// Sections d0 and, for a prefix's launch, d1.
 RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
   RowsLaunch r;
   std::memset(&r, 0, sizeof r);
@@ -153,10 +141,6 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
   return r;
 }
 
-struct RowsWs {
-  size_t ml_off, rec_off, total;
-};
-
 RowsWs rows_ws(const RowsLaunch& r) {
   RowsWs w{0, 0, 0};
   if (r.part_rows == 0) return w;
@@ -167,26 +151,23 @@ RowsWs rows_ws(const RowsLaunch& r) {
   return w;
 }
 
-bool encode_map(EncodeTiledFn enc, const gqa_desc_t& d, CUtensorMap* m, const void* base, int heads, int positions,
-                int box_heads, int box_positions) {
+bool encode_heads_map(CUtensorMap* m, int in_dtype, const void* base, int head_dim, int heads, int positions,
+                      int outer, int64_t head_stride, int64_t pos_stride, int64_t outer_stride, int box_heads,
+                      int box_positions) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
   const CUtensorMapDataType type =
-      d.in_dtype == GQA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const cuuint64_t D = static_cast<cuuint64_t>(d.head_dim);
+      in_dtype == GQA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const cuuint32_t es[4] = {1, 1, 1, 1};
-  const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(positions),
-                              static_cast<cuuint64_t>(d.batch)};
-  const cuuint64_t strides[3] = {D * 2, D * 2 * dims[1], D * 2 * dims[1] * dims[2]};
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(positions), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[3] = {2 * static_cast<cuuint64_t>(head_stride), 2 * static_cast<cuuint64_t>(pos_stride),
+                                 2 * static_cast<cuuint64_t>(outer_stride)};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_positions), 1};
   return enc(m, type, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-struct Keys {  // a section's keys
-  const void* k;
-  const void* v;
-  const int32_t* lens;
-};
 
 gqa_status_t launch_kernel(const void* fn, dim3 grid, int threads, int smem, void* params, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
@@ -202,22 +183,35 @@ gqa_status_t launch_kernel(const void* fn, dim3 grid, int threads, int smem, voi
   return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
-// The rows kernel and, where it leaves partials, their merge; `ws` holds
-// rows_ws() bytes.
-gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys* keys, void* out, float* lse,
-                 uint8_t* ws, cudaStream_t stream) {
+gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const Keys* keys, const PagedCall* paged,
+                      void* out, float* lse, uint8_t* ws, cudaStream_t stream) {
   RowsParams p;
   std::memset(&p, 0, sizeof p);
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return GQA_ERR_CUDA;
+  if (encode_fn() == nullptr) return GQA_ERR_CUDA;
   const int G = r.q_heads / r.kv_heads;
   for (int i = 0; i < r.n; ++i) {
     const gqa_desc_t& d = r.d[i];
     RowsSection& s = p.s[i];
-    if (!encode_map(enc, d, &s.tm_q, q, d.q_heads, d.q_tokens, G, r.s[i].tokens) ||
-        !encode_map(enc, d, &s.tm_k, keys[i].k, d.kv_heads, d.max_seqlen, 1, kBlockN) ||
-        !encode_map(enc, d, &s.tm_v, keys[i].v, d.kv_heads, d.max_seqlen, 1, kBlockN))
-      return GQA_ERR_INVALID_ARG;
+    const int64_t D = d.head_dim;
+    // dense [B, positions, heads, d]
+    auto dense = [&](CUtensorMap* m, const void* base, int heads, int positions, int box_heads, int box_positions) {
+      return encode_heads_map(m, d.in_dtype, base, d.head_dim, heads, positions, d.batch, D, D * heads,
+                              D * heads * positions, box_heads, box_positions);
+    };
+    if (!dense(&s.tm_q, q, d.q_heads, d.q_tokens, G, r.s[i].tokens)) return GQA_ERR_INVALID_ARG;
+    CUtensorMap* maps[2] = {&s.tm_k, &s.tm_v};
+    const void* bases[2] = {keys[i].k, keys[i].v};
+    for (int m = 0; m < 2; ++m) {
+      bool ok;
+      if (paged != nullptr) {
+        const gqa_pages_t& g = *paged->geometry;
+        ok = encode_heads_map(maps[m], d.in_dtype, bases[m], d.head_dim, d.kv_heads, g.page_size, g.num_pages,
+                              g.head_stride, g.pos_stride, g.page_stride, 1, 1 << paged->keys.box_shift);
+      } else {
+        ok = dense(maps[m], bases[m], d.kv_heads, d.max_seqlen, 1, kBlockN);
+      }
+      if (!ok) return GQA_ERR_INVALID_ARG;
+    }
     s.lens = keys[i].lens;
     s.part_row = r.s[i].part_row;
     s.rec = r.s[i].rec;
@@ -229,6 +223,7 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
     s.causal = d.causal != 0 ? 1 : 0;
   }
   p.plan = r.plan;
+  if (paged != nullptr) p.pages = paged->keys;
   const RowsWs w = rows_ws(r);
   if (w.total > 0) {
     p.o_part = reinterpret_cast<float*>(ws);
@@ -255,8 +250,11 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
   p.timeout_ns = wait_timeout_ns() + items_in_ring_ns(longest);
   const bool f16 = r.in_dtype == GQA_DTYPE_FP16;
   const int hd = r.head_dim;
-  const KernelRef ref = hd == 64 ? rows_kernel_ref_64(f16) : hd == 256 ? rows_kernel_ref_256(f16) : rows_kernel_ref_128(f16);
-  const unsigned bit = 24u + (hd == 64 ? 0u : hd == 128 ? 2u : 4u) + (f16 ? 1u : 0u);
+  const bool pg = paged != nullptr;
+  const KernelRef ref = hd == 64    ? (pg ? rows_kernel_ref_64_1(f16) : rows_kernel_ref_64_0(f16))
+                        : hd == 256 ? (pg ? rows_kernel_ref_256_1(f16) : rows_kernel_ref_256_0(f16))
+                                    : (pg ? rows_kernel_ref_128_1(f16) : rows_kernel_ref_128_0(f16));
+  const unsigned bit = 24u + (hd == 64 ? 0u : hd == 128 ? 4u : 8u) + (f16 ? 1u : 0u) + (pg ? 2u : 0u);
   gqa_status_t rc = ensure_smem_attr(st, bit, ref.fn, ref.smem_bytes, ref.regs);
   if (rc != GQA_OK) return rc;
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
@@ -307,6 +305,8 @@ gqa_status_t run(DeviceState* st, const RowsLaunch& r, const void* q, const Keys
   return launch_kernel(fn, dim3(static_cast<unsigned>(want)), kMergeThreads, 0, &m, stream);
 }
 
+namespace {
+
 gqa_status_t check_cross(const gqa_desc_t* d) {
   const gqa_status_t rc = check_desc_any_rows(d);
   if (rc != GQA_OK) return rc;
@@ -337,6 +337,8 @@ gqa_status_t check_prefix(const gqa_desc_t* d, int max_prefix, gqa_desc_t* prefi
   return GQA_OK;
 }
 
+}  // namespace
+
 bool output_ok(const void* out, const float* lse) {
   return out != nullptr && aligned(out, 16) && (lse == nullptr || aligned(lse, 4));
 }
@@ -345,7 +347,6 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
   return need == 0 || (ws != nullptr && bytes >= need && aligned(ws, kWsAlign));
 }
 
-}  // namespace
 }  // namespace gqa
 
 using namespace gqa;
@@ -379,7 +380,7 @@ gqa_status_t gqa_cross_attn(const gqa_desc_t* desc, const void* q, const void* k
   if (r.status != GQA_OK) return r.status;
   if (!workspace_ok(workspace, workspace_bytes, rows_ws(r).total)) return GQA_ERR_WORKSPACE;
   const Keys keys[1] = {{k, v, kv_lens}};
-  return run(st, r, q, keys, out, lse, static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return run_rows(st, r, q, keys, nullptr, out, lse, static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 size_t gqa_prefix_workspace_size(const gqa_desc_t* desc, int max_prefix) {
@@ -410,7 +411,7 @@ gqa_status_t gqa_prefix_attn(const gqa_desc_t* desc, const void* q, const void* 
   if (r.status != GQA_OK) return r.status;
   if (!workspace_ok(workspace, workspace_bytes, rows_ws(r).total)) return GQA_ERR_WORKSPACE;
   const Keys keys[2] = {{k_prefix, v_prefix, prefix_len}, {k_cache, v_cache, seqlens}};
-  return run(st, r, q, keys, out, lse, static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return run_rows(st, r, q, keys, nullptr, out, lse, static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int max_prefix, const int32_t* kv_lens_host,

@@ -1,21 +1,23 @@
-// The rows kernel instantiations of one head_dim, selected when compiling:
-// -DGQA_INST_HD=<64|128|256>.  The host code reaches them through rows_launch.h.
+// The rows kernel instantiations of one head_dim, for dense or paged keys,
+// selected when compiling: -DGQA_INST_HD=<64|128|256> -DGQA_INST_PAGED=<0|1>.
+// The host code reaches them through rows_launch.h.
 #include "rows_kernel.cuh"
 #include "rows_launch.h"
 
-#if !defined(GQA_INST_HD)
-#error "compile with -DGQA_INST_HD=<64|128|256>"
+#if !defined(GQA_INST_HD) || !defined(GQA_INST_PAGED)
+#error "compile with -DGQA_INST_HD=<64|128|256> -DGQA_INST_PAGED=<0|1>"
 #endif
 
-#define GQA_ROWS_REF_NAME_(hd) rows_kernel_ref_##hd
-#define GQA_ROWS_REF_NAME(hd) GQA_ROWS_REF_NAME_(hd)
+#define GQA_ROWS_REF_NAME_(hd, paged) rows_kernel_ref_##hd##_##paged
+#define GQA_ROWS_REF_NAME(hd, paged) GQA_ROWS_REF_NAME_(hd, paged)
 
 namespace gqa {
 
-KernelRef GQA_ROWS_REF_NAME(GQA_INST_HD)(bool f16) {
+KernelRef GQA_ROWS_REF_NAME(GQA_INST_HD, GQA_INST_PAGED)(bool f16) {
   using Cfg = RowsCfg<GQA_INST_HD>;
-  const void* fn = f16 ? reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, true>)
-                       : reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, false>);
+  constexpr bool kPaged = GQA_INST_PAGED != 0;
+  const void* fn = f16 ? reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, true, kPaged>)
+                       : reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, false, kPaged>);
   return KernelRef{fn, Cfg::kSmemBytes, Cfg::kThreads, Cfg::kMoveRegs ? Cfg::kLaunchRegs : 0};
 }
 

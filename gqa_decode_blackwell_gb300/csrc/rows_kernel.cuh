@@ -59,6 +59,12 @@
 // (every_piece), leave fp32 partials (O_s, its maximum and sum) for
 // rows_merge.cuh.
 //
+// PAGED: the keys of one section of entries lie in a paged cache (paged.h), and
+// the entries' last keys are drafted tokens, of which a query token sees those
+// that its row of bits names.  A block's tiles are then fetched page by page (or
+// 128 positions of a larger one), rows of V that no page brought are zeroed with
+// those past the length, and an entry may have fewer live tokens than others.
+//
 // Every wait is bounded, as in the decode kernel, with the time that the items
 // in the ring may take on top (items_in_ring_ns).
 #pragma once
@@ -68,6 +74,7 @@
 #include <cuda_fp16.h>
 
 #include "decode_kernel.cuh"
+#include "paged.h"
 #include "rows_plan.cuh"
 #include "rows_ptx.cuh"
 
@@ -114,6 +121,7 @@ struct RowsParams {
   unsigned int* err_word;
   // byte extents of the buffers the kernel writes, checked by -DGQA_DEBUG builds
   unsigned long long out_bytes, lse_bytes, o_part_bytes, ml_part_bytes, rec_bytes;
+  PagedKeys pages;      // PAGED kernels
 };
 
 // One item of a CTA: a range of key blocks of one triple.
@@ -128,6 +136,7 @@ struct RowsItem {
   }
   int L;                  // keys of entry b
   int piece;              // where its partials go; -1: final output
+  int live;               // query tokens of entry b (PAGED: those it has; its rows behind them see nothing)
 };
 constexpr int kItemRing = 4;
 constexpr uint64_t kBlockNs = 20000;  // far more than a key block of an item takes
@@ -175,8 +184,8 @@ struct RowsCfg {
   static_assert(kStagesK % kTilesPerBlock == 0, "rings of whole blocks");
 };
 
-// IN_F16: q, k, v (and P) are fp16; otherwise bf16.
-template <int HEAD_DIM, bool IN_F16>
+// IN_F16: q, k, v (and P) are fp16; otherwise bf16.  PAGED: see the top.
+template <int HEAD_DIM, bool IN_F16, bool PAGED>
 __global__ void __launch_bounds__(RowsCfg<HEAD_DIM>::kThreads, 1)
 gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   using Cfg = RowsCfg<HEAD_DIM>;
@@ -278,7 +287,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // Q slots of an item: its row tiles that hold any token (at least one)
   auto slots_of = [&](const RowsItem& w) {
     const RowsSection& s = p.s[w.section];
-    return NT == 2 && s.split_keys == 0 && w.tok0 + s.tokens < s.nq ? 2 : 1;
+    return NT == 2 && s.split_keys == 0 && w.tok0 + s.tokens < (PAGED ? w.live : s.nq) ? 2 : 1;
   };
 
   if (warp >= kProducerWarp) {
@@ -297,15 +306,29 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           const uint32_t empty = BAR((is_v ? V_EMPTY : K_EMPTY) + static_cast<int>(stage));
           // the first pass over a ring needs no wait
           if (n >= ns && !ptx::mbar_wait_bounded(empty, ((n / ns) & 1u) ^ 1u, abort_flag, p.timeout_ns)) return false;
-          ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
           detail::check_coord(p.err_word, w.b >= 0 && w.b < p.plan.s[w.section].batch && w.h >= 0 &&
                                               (w.h + 1) * p.G <= p.Hq && blk >= 0 &&
                                               blk * kBlockN < p.plan.s[w.section].max_len);
           uint8_t* dst = (is_v ? vring : kring) + stage * Cfg::kStageBytes;
+          if constexpr (PAGED) {
+            // the boxes that hold any key of the block
+            const int box = 1 << p.pages.box_shift, first = blk * kBlockN;
+            const int held = (min(w.L - first, kBlockN) + box - 1) >> p.pages.box_shift;
+            ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(held * box * TCH * 128));
+            for (int i = 0; i < held; ++i) {
+              const int page = detail::page_of(p.pages, p.err_word, w.b, first + i * box);
 #pragma unroll
-          for (int kc = 0; kc < TCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &s.tm_v : &s.tm_k, full, (hf * TCH + kc) * 64,
-                             w.h, blk * kBlockN, w.b);
+              for (int kc = 0; kc < TCH; ++kc)
+                ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384 + i * box * 128), is_v ? &s.tm_v : &s.tm_k, full,
+                                 (hf * TCH + kc) * 64, w.h, (first + i * box) & p.pages.page_mask, page);
+            }
+          } else {
+            ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
+#pragma unroll
+            for (int kc = 0; kc < TCH; ++kc)
+              ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384), is_v ? &s.tm_v : &s.tm_k, full, (hf * TCH + kc) * 64,
+                               w.h, blk * kBlockN, w.b);
+          }
           if (is_v) ++tv; else ++tk;
         }
         return true;
@@ -510,8 +533,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         if (more) {
           const RowsSection& s = p.s[w.section];
           const int triple = w.b * p.plan.s[w.section].heads + w.hh;
-          const bool partial = p.every_piece != 0 || w.whole == 0, first_piece = w.blk_begin == 0;
-          const int n_pieces = w.blk_begin < w.blk_end ? w.n_pieces : 0;
+          const bool first_piece = w.blk_begin == 0;
           it.section = w.section;
           it.b = w.b;
           it.h = w.hh / s.groups;
@@ -520,6 +542,13 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           it.blk_end = w.blk_end;
           it.turn = w.turn;
           it.L = w.L;
+          it.live = PAGED ? detail::live_tokens(p.pages, p.err_word, w.b, w.L, s.nq) : s.nq;
+          // A group behind the entry's last token has nothing to do but to leave
+          // its rows empty: without keys, whole, wherever it was cut.
+          if (PAGED && it.tok0 >= it.live) it.blk_end = it.blk_begin;
+          const bool keys = it.blk_begin < it.blk_end;
+          const bool partial = p.every_piece != 0 || (w.whole == 0 && (!PAGED || keys));
+          const int n_pieces = keys ? w.n_pieces : 0;
           it.piece = partial ? rows_piece(p.every_piece != 0, p.plan.dealt != 0, triple, static_cast<int>(blockIdx.x),
                                           first_piece)
                              : -1;
@@ -584,16 +613,22 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       const uint32_t u0 = u;
       u += static_cast<uint32_t>(n_blk);
       const bool split_keys = NT == 2 && p.s[it.section].split_keys != 0;
-      if (!split_keys && t >= slots_of(it)) continue;
+      const bool idle = !split_keys && t >= slots_of(it);
+      // (PAGED: an idle tile may still hold rows of tokens that the entry lacks)
+      if (idle && (!PAGED || it.tok0 + t * p.s[it.section].tokens >= p.s[it.section].nq)) continue;
       const int rows = p.s[it.section].tokens * p.G;   // of a tile
       const int first_lane = t == 1 ? p.s[it.section].shift : 0;
       const int rr = r - first_lane;                   // the row within the tile
       const bool active = rr >= lane && rr - lane < rows;  // this warp holds any of them
       // the last key this row sees is L - 1, or (causal) L - nq + its token; all
       // tokens of a causal section are in one tile, and both hold that one (check_prefix)
-      const int causal_cut = p.s[it.section].causal != 0 ? p.s[it.section].nq - 1 : 0;
+      const int causal_cut = !PAGED && p.s[it.section].causal != 0 ? p.s[it.section].nq - 1 : 0;
       const int sees = it.L - causal_cut + (causal_cut != 0 ? it.tok0 + rr / p.G : 0);
-      const int step = split_keys ? 2 : 1, i0 = split_keys ? t : 0;
+      // PAGED: this row's token, and the first key that its branch may hide
+      const int tok_row = PAGED ? it.tok0 + (split_keys ? 0 : t * p.s[it.section].tokens) + rr / p.G : 0;
+      const int drafts = it.L - it.live;
+      const bool dead = PAGED && tok_row >= it.live;
+      const int step = split_keys ? 2 : 1, i0 = PAGED && idle ? n_blk : split_keys ? t : 0;
 
       float nm = kNoMax, l = 0.f;  // -max (log2 units; kNoMax while it is -inf) and the sum of this row
       for (int i = i0; i < n_blk; i += step, ++g) {
@@ -612,7 +647,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           // complete S says that every PV issued before it has landed, among
           // them the one that read the stage's V before (one tile: that is
           // PV(g-1), issued after this S, and waited for).
-          const int cap = min(p.plan.s[it.section].max_len - blk * kBlockN, kBlockN);
+          // (PAGED: nor did TMA write what no page of this entry holds)
+          const int cap = PAGED ? kBlockN : min(p.plan.s[it.section].max_len - blk * kBlockN, kBlockN);
           if ((t == 0 || split_keys) && cap > tail) {
             if constexpr (NT == 1) {
               if (g >= 1 && !wait_pv(g - 1)) break;
@@ -645,7 +681,20 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, x + 32 * c);
         ptx::tmem_wait_ld();
 
-        if ((blk + 1) * kBlockN > it.L - causal_cut) {
+        if constexpr (PAGED) {
+          if ((blk + 1) * kBlockN > (p.pages.chain != 0 || p.pages.tree != nullptr ? drafts : it.L)) {
+            const uint32_t* branch = detail::branch_of(p.pages, it.b, p.s[it.section].nq, dead ? 0 : tok_row);
+            const int seen = p.pages.chain != 0 ? min(tail, drafts + tok_row + 1 - blk * kBlockN) : tail;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+              const uint32_t vis = detail::seen_bits(seen - c) &
+                                   detail::branch_bits(branch, p.pages.tree_words, blk * kBlockN + c - drafts);
+              if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
+#pragma unroll
+              for (int j = c; j < c + 32; ++j) x[j] = (vis >> (j - c)) & 1u ? x[j] : 0xff800000u;  // -inf
+            }
+          }
+        } else if ((blk + 1) * kBlockN > it.L - causal_cut) {
           const int seen = sees - blk * kBlockN < tail ? sees - blk * kBlockN : tail;
 #pragma unroll
           for (int c = 0; c < 128; c += 32) {
@@ -741,6 +790,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       const bool partial = it.piece >= 0;
       if (n_blk == 0 && partial) continue;  // 0 pieces: the merge reads nothing of this triple
       const bool empty = i0 >= n_blk;       // this tile had no key
+      if (dead) {  // whatever its query was
+        nm = kNoMax;
+        l = 0.f;
+      }
       if (!active) continue;
       if (!empty) {
         if (!wait_pv(g - 1)) break;
