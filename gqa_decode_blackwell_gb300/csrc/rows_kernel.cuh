@@ -294,18 +294,29 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   if constexpr (Cfg::kMoveRegs) ptx::regs_dec<Cfg::kControlRegs>();
   if (warp == kProducerWarp) {
     // ============================================================= producer
-    if (lane == 0) {
+    // One thread; or (PAGED) the whole warp, converged, whose lanes each look a
+    // page up and of which one elected thread issues.
+    if (PAGED || lane == 0) {
       uint32_t tk = 0, tv = 0, tq = 0;  // ring tiles and Q slots loaded
       bool ok = true;
-      auto load_block = [&](bool is_v, const RowsItem& w, int blk) -> bool {
+      const bool issues = PAGED ? ptx::elect_one() != 0 : true;
+      auto waited = [&](int i, uint32_t parity) -> bool {
+        const bool done = ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns);
+        return PAGED ? __all_sync(0xffffffffu, done) : done;
+      };
+      // PAGED: the pages of a block's boxes, one to a lane
+      auto look_up = [&](const RowsItem& w, int blk) -> int {
+        const int pos = blk * kBlockN + (lane << p.pages.box_shift);
+        return (lane << p.pages.box_shift) < kBlockN && pos < w.L ? detail::page_of(p.pages, p.err_word, w.b, pos) : 0;
+      };
+      auto load_block = [&](bool is_v, const RowsItem& w, int blk, int page_ids) -> bool {
         const RowsSection& s = p.s[w.section];
 #pragma unroll
         for (int hf = 0; hf < TPB; ++hf) {
           const uint32_t n = is_v ? tv : tk, ns = is_v ? NSV : NSK, stage = n % ns;
           const uint32_t full = BAR((is_v ? V_FULL : K_FULL) + static_cast<int>(stage));
-          const uint32_t empty = BAR((is_v ? V_EMPTY : K_EMPTY) + static_cast<int>(stage));
           // the first pass over a ring needs no wait
-          if (n >= ns && !ptx::mbar_wait_bounded(empty, ((n / ns) & 1u) ^ 1u, abort_flag, p.timeout_ns)) return false;
+          if (n >= ns && !waited((is_v ? V_EMPTY : K_EMPTY) + static_cast<int>(stage), (n / ns) ^ 1u)) return false;
           detail::check_coord(p.err_word, w.b >= 0 && w.b < p.plan.s[w.section].batch && w.h >= 0 &&
                                               (w.h + 1) * p.G <= p.Hq && blk >= 0 &&
                                               blk * kBlockN < p.plan.s[w.section].max_len);
@@ -314,13 +325,16 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             // the boxes that hold any key of the block
             const int box = 1 << p.pages.box_shift, first = blk * kBlockN;
             const int held = (min(w.L - first, kBlockN) + box - 1) >> p.pages.box_shift;
-            ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(held * box * TCH * 128));
+            if (issues) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(held * box * TCH * 128));
             for (int i = 0; i < held; ++i) {
-              const int page = detail::page_of(p.pages, p.err_word, w.b, first + i * box);
+              const int page = __shfl_sync(0xffffffffu, page_ids, i);
+              if (issues) {
 #pragma unroll
-              for (int kc = 0; kc < TCH; ++kc)
-                ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384 + i * box * 128), is_v ? &s.tm_v : &s.tm_k, full,
-                                 (hf * TCH + kc) * 64, w.h, (first + i * box) & p.pages.page_mask, page);
+                for (int kc = 0; kc < TCH; ++kc)
+                  ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384 + i * box * 128), is_v ? &s.tm_v : &s.tm_k, full,
+                                   (hf * TCH + kc) * 64, w.h, (first + i * box) & p.pages.page_mask, page);
+              }
+              __syncwarp();
             }
           } else {
             ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
@@ -334,28 +348,36 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         return true;
       };
       RowsItem it;
-      while (next_item(it, ok, false)) {
+      while (next_item(it, ok, PAGED)) {
         if (it.blk_begin >= it.blk_end) continue;
         const RowsSection& s = p.s[it.section];
         const int nt = slots_of(it);
         for (int t = 0; t < nt; ++t, ++tq) {
           const int slot = static_cast<int>(tq % NT);
-          if (tq >= NT && !ptx::mbar_wait_bounded(BAR(Q_EMPTY + slot), ((tq / NT) & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
+          if (tq >= NT && !waited(Q_EMPTY + slot, (tq / NT) ^ 1u)) {
             ok = false;
             break;
           }
-          ptx::mbar_arrive_expect_tx(BAR(Q_FULL + slot), static_cast<uint32_t>(KCH * s.tokens * p.G * 128));
+          if (issues) {
+            ptx::mbar_arrive_expect_tx(BAR(Q_FULL + slot), static_cast<uint32_t>(KCH * s.tokens * p.G * 128));
 #pragma unroll
-          for (int kc = 0; kc < KCH; ++kc)
-            ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384 + s.shift * 128), &s.tm_q,
-                             BAR(Q_FULL + slot), kc * 64, it.h * p.G, it.tok0 + t * s.tokens, it.b);
+            for (int kc = 0; kc < KCH; ++kc)
+              ptx::tma_load_4d(ptx::smem_u32(qbuf + slot * Cfg::kQTileBytes + kc * 16384 + s.shift * 128), &s.tm_q,
+                               BAR(Q_FULL + slot), kc * 64, it.h * p.G, it.tok0 + t * s.tokens, it.b);
+          }
+          if (PAGED) __syncwarp();
         }
-        // K0, then K(i+1), V(i): at most one block of K ahead of its V
+        // K0, then K(i+1), V(i): at most one block of K ahead of its V.  (Pages
+        // are looked up a block before they are asked for.)
         const int n = it.blk_end - it.blk_begin;
-        if (ok) ok = load_block(false, it, it.block(0));
+        int ids = PAGED ? look_up(it, it.block(0)) : 0, ids1 = PAGED && n > 1 ? look_up(it, it.block(1)) : 0;
+        if (ok) ok = load_block(false, it, it.block(0), ids);
         for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n) ok = load_block(false, it, it.block(i + 1));
-          if (ok) ok = load_block(true, it, it.block(i));
+          const int ids2 = PAGED && i + 2 < n ? look_up(it, it.block(i + 2)) : 0;
+          if (i + 1 < n) ok = load_block(false, it, it.block(i + 1), ids1);
+          if (ok) ok = load_block(true, it, it.block(i), ids);
+          ids = ids1;
+          ids1 = ids2;
         }
         if (!ok) break;
       }
