@@ -260,7 +260,7 @@ size_t gqa_tree_workspace_size(const gqa_desc_t* desc, const gqa_pages_t* pages)
   int dev = 0;
   DeviceState* st = nullptr;
   if (current_device(&dev, &st) != GQA_OK) return 0;
-  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count);
+  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count, true);
   return r.status == GQA_OK ? rows_ws(r).total : 0;
 }
 
@@ -278,7 +278,7 @@ gqa_status_t gqa_tree_attn(const gqa_desc_t* desc, const gqa_pages_t* pages, con
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = current_device(&dev, &st)) != GQA_OK) return rc;
-  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count);
+  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count, true);
   if (r.status != GQA_OK) return r.status;
   if (!workspace_ok(workspace, workspace_bytes, rows_ws(r).total)) return GQA_ERR_WORKSPACE;
   PagedCall call;

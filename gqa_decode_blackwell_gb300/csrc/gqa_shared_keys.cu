@@ -38,6 +38,11 @@ namespace {
 // was then; 64 prompts of 200 tokens, 60 without keys, 35 us, 39 with zeros at 20.)
 constexpr int kTwoTileUnits = 14, kLoneTileUnits = 12, kWideUnits = 8, kItemUnits = 32, kZerosUnits = 12;
 constexpr int kSplitUnits = 7, kSplitItemUnits = 16;
+// An item of the one tile of 128-element heads over pages, against blocks of 8
+// (kWideUnits).  The calls above, at 4 / 8 / 12 / 16 / 32 units: 26 tokens 65.9 / 65.3 /
+// 65.0 / 65.6 / 66.0 us, 16 tokens 45.7 / 44.3 / 44.0 / 43.8 / 44.4, 1 token 23.4 / 23.2 /
+// 23.5 / 23.6 / 24.8.
+constexpr int kLoneItemUnits = 12;
 // Up to this many rows a merge gives each a CTA, whose warps share its pieces;
 // beyond, a warp to a row.  Measured on GB300, a whole call: 384 rows of 256
 // 28.2 us (33.3 with a warp each), 1024 rows of 128 the same both ways, 2048
@@ -45,7 +50,6 @@ constexpr int kSplitUnits = 7, kSplitItemUnits = 16;
 constexpr size_t kMergeSharedRows = 1024;
 
 int group_of(const gqa_desc_t* d) { return d->q_heads / d->kv_heads; }
-int tiles_of(int head_dim) { return head_dim == 256 ? 1 : 2; }
 
 // Few rows fit the decode kernel, which puts the keys along the MMA's M
 // dimension and streams them with a 16- or 32-column tile.  Measured on GB300
@@ -70,7 +74,7 @@ bool split_keys(const gqa_desc_t& d, int tiles) {
 
 }  // namespace
 
-RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
+RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm, bool paged) {
   RowsLaunch r;
   std::memset(&r, 0, sizeof r);
   r.head_dim = d0->head_dim;
@@ -83,7 +87,16 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
   r.n = d1 != nullptr ? 2 : 1;
   r.d[0] = *d0;
   if (d1 != nullptr) r.d[1] = *d1;
-  const int tiles = tiles_of(d0->head_dim), G = group_of(d0), most_tokens = kTileRows / G;
+  const int G = group_of(d0), most_tokens = kTileRows / G;
+  // Rows that fit one tile, over pages: one tile of 128-element heads to a CTA,
+  // whose blocks are then deeper in flight and whose items leave one piece, not two.
+  // Measured on GB300, us a call (one tile, two): 16 sequences of 1000-8192 keys,
+  // 32 / 8 heads, up to 26 tokens 65.0 and 70.1, 8 tokens 57.5 and 60.8; 32 of
+  // 300-2048, up to 16 tokens 44.0 and 48.3; 8 of 1000-4096, 1 token 23.4 and 24.6.
+  // Batches whose lengths do not fit beside its rings take two.
+  const bool lone = paged && d0->head_dim == 128 && d0->q_tokens <= most_tokens && d0->batch <= kMaxLoneEntries;
+  const int tiles = d0->head_dim == 256 || lone ? 1 : 2;
+  r.tiles = tiles;
   // Triples of rows that fit one tile all leave partials, and so do all triples
   // of a prefix's launch.
   r.every_piece = r.n == 2 || r.d[0].q_tokens <= most_tokens;
@@ -108,8 +121,9 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
                      : s.split_keys              ? kSplitUnits
                      : d.q_tokens <= most_tokens ? kLoneTileUnits
                                                  : kTwoTileUnits;
-    ps.item_units = s.split_keys ? kSplitItemUnits : kItemUnits;
+    ps.item_units = s.split_keys ? kSplitItemUnits : lone ? kLoneItemUnits : kItemUnits;
     ps.empty_units = r.every_piece ? 0 : kZerosUnits;
+    ps.block_div = rows_divisor(ps.block_units);
     entries += d.batch;
     units += static_cast<long long>(s.triples) * rows_units(ps, d.max_seqlen);
   }
@@ -127,6 +141,7 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm) {
     if (most < ctas) ctas = most < 1 ? 1 : most;
   }
   r.plan.num_ctas = static_cast<int>(ctas);
+  r.plan.ctas_div = rows_divisor(r.plan.num_ctas);
   for (int i = 0; i < r.n; ++i) {
     auto& s = r.s[i];
     if (r.every_piece) s.pieces = r.plan.dealt ? s.triples : s.triples + ctas;
@@ -251,10 +266,11 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
   const bool f16 = r.in_dtype == GQA_DTYPE_FP16;
   const int hd = r.head_dim;
   const bool pg = paged != nullptr;
-  const KernelRef ref = hd == 64    ? (pg ? rows_kernel_ref_64_1(f16) : rows_kernel_ref_64_0(f16))
-                        : hd == 256 ? (pg ? rows_kernel_ref_256_1(f16) : rows_kernel_ref_256_0(f16))
-                                    : (pg ? rows_kernel_ref_128_1(f16) : rows_kernel_ref_128_0(f16));
-  const unsigned bit = 24u + (hd == 64 ? 0u : hd == 128 ? 4u : 8u) + (f16 ? 1u : 0u) + (pg ? 2u : 0u);
+  const KernelRef ref = hd == 64    ? (pg ? rows_kernel_ref_64_1(2, f16) : rows_kernel_ref_64_0(2, f16))
+                        : hd == 256 ? (pg ? rows_kernel_ref_256_1(1, f16) : rows_kernel_ref_256_0(1, f16))
+                                    : (pg ? rows_kernel_ref_128_1(r.tiles, f16) : rows_kernel_ref_128_0(2, f16));
+  const unsigned bit = 24u + (hd == 64 ? 0u : hd == 128 ? 6u : 12u) + (f16 ? 1u : 0u) + (pg ? 2u : 0u) +
+                       (hd == 128 && r.tiles == 1 ? 2u : 0u);
   gqa_status_t rc = ensure_smem_attr(st, bit, ref.fn, ref.smem_bytes, ref.regs);
   if (rc != GQA_OK) return rc;
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
@@ -284,7 +300,22 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
   m.Hq = r.q_heads;
   m.G = G;
   m.kv_heads = r.kv_heads;
-  m.tiles = tiles_of(hd);
+  m.tiles = r.tiles;
+  // Of a paged call's few rows each gets a CTA (below), of more each a place among
+  // its tile's.
+  if (paged != nullptr && (!r.every_piece || rows > kMergeSharedRows)) {
+    const bool cut = !r.every_piece;
+    const void* fn = hd == 64    ? (cut ? reinterpret_cast<const void*>(&gqa_tile_merge_kernel<64, true>)
+                                        : reinterpret_cast<const void*>(&gqa_tile_merge_kernel<64, false>))
+                     : hd == 256 ? (cut ? reinterpret_cast<const void*>(&gqa_tile_merge_kernel<256, true>)
+                                        : reinterpret_cast<const void*>(&gqa_tile_merge_kernel<256, false>))
+                                 : (cut ? reinterpret_cast<const void*>(&gqa_tile_merge_kernel<128, true>)
+                                        : reinterpret_cast<const void*>(&gqa_tile_merge_kernel<128, false>));
+    const int per_cta = kTileMergeThreads / 32 * (hd == 256 ? kTileMergeRows<256> : kTileMergeRows<128>);
+    const int per_triple = (m.s[0].split_keys ? 1 : m.tiles) * m.s[0].tokens * G;
+    return launch_kernel(fn, dim3(static_cast<unsigned>(cut ? r.plan.num_ctas : r.s[0].triples),
+                                  (per_triple + per_cta - 1) / per_cta), kTileMergeThreads, 0, &m, stream);
+  }
   if (!r.every_piece) {
     const void* fn = hd == 64    ? reinterpret_cast<const void*>(&gqa_rows_merge_kernel<64>)
                      : hd == 256 ? reinterpret_cast<const void*>(&gqa_rows_merge_kernel<256>)
@@ -359,7 +390,7 @@ size_t gqa_cross_workspace_size(const gqa_desc_t* desc) {
   int dev = 0;
   DeviceState* st = nullptr;
   if (current_device(&dev, &st) != GQA_OK) return 0;
-  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count);
+  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count, false);
   return r.status == GQA_OK ? rows_ws(r).total : 0;
 }
 
@@ -376,7 +407,7 @@ gqa_status_t gqa_cross_attn(const gqa_desc_t* desc, const void* q, const void* k
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = current_device(&dev, &st)) != GQA_OK) return rc;
-  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count);
+  const RowsLaunch r = make_launch(desc, nullptr, st->sm_count, false);
   if (r.status != GQA_OK) return r.status;
   if (!workspace_ok(workspace, workspace_bytes, rows_ws(r).total)) return GQA_ERR_WORKSPACE;
   const Keys keys[1] = {{k, v, kv_lens}};
@@ -389,7 +420,7 @@ size_t gqa_prefix_workspace_size(const gqa_desc_t* desc, int max_prefix) {
   int dev = 0;
   DeviceState* st = nullptr;
   if (current_device(&dev, &st) != GQA_OK) return 0;
-  const RowsLaunch r = make_launch(&prefix, desc, st->sm_count);
+  const RowsLaunch r = make_launch(&prefix, desc, st->sm_count, false);
   return r.status == GQA_OK ? rows_ws(r).total : 0;
 }
 
@@ -407,7 +438,7 @@ gqa_status_t gqa_prefix_attn(const gqa_desc_t* desc, const void* q, const void* 
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = current_device(&dev, &st)) != GQA_OK) return rc;
-  const RowsLaunch r = make_launch(&prefix, desc, st->sm_count);
+  const RowsLaunch r = make_launch(&prefix, desc, st->sm_count, false);
   if (r.status != GQA_OK) return r.status;
   if (!workspace_ok(workspace, workspace_bytes, rows_ws(r).total)) return GQA_ERR_WORKSPACE;
   const Keys keys[2] = {{k_prefix, v_prefix, prefix_len}, {k_cache, v_cache, seqlens}};
@@ -430,7 +461,7 @@ gqa_status_t gqa_shared_keys_plan(const gqa_desc_t* desc, int prefix_len, int ma
   }
   if (num_items) *num_items = 0;
   if (desc->batch == 0) return GQA_OK;
-  const RowsLaunch r = with_prefix ? make_launch(&prefix, desc, sm_count) : make_launch(desc, nullptr, sm_count);
+  const RowsLaunch r = with_prefix ? make_launch(&prefix, desc, sm_count, false) : make_launch(desc, nullptr, sm_count, false);
   if (r.status != GQA_OK) return r.status;
   if (num_ctas) *num_ctas = r.plan.num_ctas;
   if (every_piece) *every_piece = r.every_piece ? 1 : 0;

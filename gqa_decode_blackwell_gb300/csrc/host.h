@@ -16,7 +16,7 @@ constexpr size_t kWsAlign = 256;
 
 struct DeviceState {
   int sm_count = 0;
-  unsigned long long attr_done = 0;  // one bit per kernel instantiation (decode: 0..23, rows: 24..35)
+  unsigned long long attr_done = 0;  // one bit per kernel instantiation (decode: 0..23, rows: 24..39)
   unsigned int* err_word = nullptr;  // device address of the library's error word
 };
 

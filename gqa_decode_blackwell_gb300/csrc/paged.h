@@ -48,23 +48,22 @@ __device__ __forceinline__ int live_tokens(const PagedKeys& k, unsigned int* err
   return n < 0 ? 0 : (n > most ? most : n);
 }
 
-// Token t's row of bits, or null.
-__device__ __forceinline__ const uint32_t* branch_of(const PagedKeys& k, int b, int nq, int t) {
-  return k.tree == nullptr ? nullptr : k.tree + (static_cast<long long>(b) * nq + t) * k.tree_words;
-}
-
 // Bits [0, n) of 32 (n of any sign).
 __device__ __forceinline__ uint32_t seen_bits(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// Of the 32 positions from `from` new tokens past the first new one on: those
-// before the first, and those the row's bits name (every one, without a row).
-__device__ __forceinline__ uint32_t branch_bits(const uint32_t* row, int words, int from) {
-  if (row == nullptr || from <= -32) return 0xffffffffu;
-  const int i = from >> 5, s = from & 31;  // (arithmetic shift: -1 for the 31 positions before)
-  const uint32_t lo = i < 0 ? 0xffffffffu : (i < words ? row[i] : 0u), hi = i + 1 < words ? row[i + 1] : 0u;
-  return __funnelshift_r(lo, hi, s);
+// Words of bits that say which positions token t of entry b sees, of the 128
+// from `from` new tokens past the first new one on: bit i of them, shifted right
+// by from modulo 32.  Positions before the first are seen, those the tree has no
+// bits for are not (and without a tree all are).
+__device__ __forceinline__ void branch_words(uint32_t (&w)[5], const PagedKeys& k, int b, int nq, int t, int from) {
+  const uint32_t* row = k.tree == nullptr ? nullptr : k.tree + (static_cast<long long>(b) * nq + t) * k.tree_words;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int at = (from >> 5) + i;  // (an arithmetic shift: below 0 for what comes before)
+    w[i] = row == nullptr || at < 0 ? 0xffffffffu : at < k.tree_words ? row[at] : 0u;
+  }
 }
 
 }  // namespace detail

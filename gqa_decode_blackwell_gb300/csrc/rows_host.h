@@ -14,6 +14,7 @@ struct RowsLaunch {
   int head_dim, q_heads, kv_heads, in_dtype, out_dtype;
   float scale;
   int n;                  // sections
+  int tiles;              // row tiles of a CTA
   gqa_desc_t d[2];        // each section as a problem of its own
   struct { int tokens, groups, split_keys, shift, triples; long long pieces, part_row, rec; } s[2];
   RowsPlan plan;
@@ -38,8 +39,8 @@ struct PagedCall {
   PagedKeys keys;
 };
 
-// Sections d0 and, for a prefix's launch, d1.
-RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm);
+// Sections d0 and, for a prefix's launch, d1.  paged: d0's keys are.
+RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm, bool paged);
 RowsWs rows_ws(const RowsLaunch& r);
 
 // The rows kernel and, where it leaves partials, their merge; `ws` holds

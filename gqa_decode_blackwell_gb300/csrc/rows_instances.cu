@@ -13,12 +13,29 @@
 
 namespace gqa {
 
-KernelRef GQA_ROWS_REF_NAME(GQA_INST_HD, GQA_INST_PAGED)(bool f16) {
-  using Cfg = RowsCfg<GQA_INST_HD>;
+namespace {
+
+template <int TILES>
+KernelRef ref(bool f16) {
+  using Cfg = RowsCfg<GQA_INST_HD, TILES>;
   constexpr bool kPaged = GQA_INST_PAGED != 0;
-  const void* fn = f16 ? reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, true, kPaged>)
-                       : reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, false, kPaged>);
+  const void* fn = f16 ? reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, TILES, true, kPaged>)
+                       : reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, TILES, false, kPaged>);
   return KernelRef{fn, Cfg::kSmemBytes, Cfg::kThreads, Cfg::kMoveRegs ? Cfg::kLaunchRegs : 0};
+}
+
+}  // namespace
+
+KernelRef GQA_ROWS_REF_NAME(GQA_INST_HD, GQA_INST_PAGED)(int tiles, bool f16) {
+#if GQA_INST_HD == 256
+  (void)tiles;
+  return ref<1>(f16);
+#elif GQA_INST_HD == 128 && GQA_INST_PAGED
+  return tiles == 1 ? ref<1>(f16) : ref<2>(f16);
+#else
+  (void)tiles;
+  return ref<2>(f16);
+#endif
 }
 
 }  // namespace gqa

@@ -31,6 +31,9 @@
 //     slots: the next block's QK runs under this block's softmax.  K and V
 //     blocks are two ring tiles each, their 128-element d-halves.
 //
+//   head_dim 128 over pages, rows that fit one tile: that form too, with two Q
+//     slots and a third block of V in flight.
+//
 // What bounds it, measured on GB300 (bf16): at head_dim 128 a step of two
 // tiles takes ~3200 cycles, in which the tensor core works for 2048, the
 // exponential units for 1024 and shared memory for ~2048 (Q and K at QK, which
@@ -124,8 +127,9 @@ struct RowsParams {
   PagedKeys pages;      // PAGED kernels
 };
 
-// One item of a CTA: a range of key blocks of one triple.
-struct RowsItem {
+// One item of a CTA: a range of key blocks of one triple.  (Copied to and from
+// shared memory 16 bytes at a time.)
+struct alignas(16) RowsItem {
   int section, b, h;
   int tok0;               // the first query token of its tiles
   int blk_begin, blk_end; // blk_begin < 0: no further item
@@ -150,18 +154,22 @@ GQA_HD uint64_t items_in_ring_ns(int max_len) {
   return static_cast<uint64_t>(num_blocks(max_len)) * kItemRing * kBlockNs;
 }
 
-template <int HEAD_DIM>
+// TILES: row tiles of a CTA (head_dim 256 has room for one).
+template <int HEAD_DIM, int TILES>
 struct RowsCfg {
-  static constexpr int kTiles = HEAD_DIM == 256 ? 1 : 2;  // row tiles of a CTA
+  static constexpr int kTiles = TILES;
   static constexpr int kChunks = HEAD_DIM / 64;           // 128-byte swizzle atoms along d
   static constexpr int kTileDim = HEAD_DIM < 128 ? HEAD_DIM : 128;
   static constexpr int kTileChunks = kTileDim / 64;
   static constexpr int kTilesPerBlock = HEAD_DIM / kTileDim;  // ring tiles of a K or V block
   static constexpr int kStageBytes = kBlockN * kTileDim * 2;
-  static constexpr int kQTileBytes = kTileRows * HEAD_DIM * 2;  // one of kTiles Q slots, taken in turn
-  static constexpr int kQBytes = kTiles * kQTileBytes;
+  static constexpr int kQTileBytes = kTileRows * HEAD_DIM * 2;  // one of the Q slots, taken in turn
+  static constexpr int kQSlots = HEAD_DIM == 256 ? 1 : 2;
+  static constexpr int kQBytes = kQSlots * kQTileBytes;
   static constexpr int kStagesK = HEAD_DIM == 64 ? 4 : 2;
-  static constexpr int kStagesV = kStagesK;
+  // One tile leaves room for a third block of V, which stays until the softmax is
+  // done with its scores.
+  static constexpr int kStagesV = HEAD_DIM == 128 && TILES == 1 ? 3 : kStagesK;
   static constexpr int kSoftmaxWarps = 4 * kTiles;
   // Two tiles: three warpgroups (softmax, softmax, and the other roles with an
   // idle warp), so that registers can move from the third to the softmax
@@ -174,23 +182,28 @@ struct RowsCfg {
   static_assert(256 * kSoftmaxRegs + 128 * kControlRegs <= 384 * kLaunchRegs, "more registers than the launch has");
   static constexpr int kRingBytes = (kStagesK + kStagesV) * kStageBytes;
   static constexpr int kItemBytes = kItemRing * static_cast<int>(sizeof(RowsItem));
-  static constexpr int kPlanBytes = 4 * (kMaxRowsEntries + 1) + 4 * kMaxRowsEntries;
-  static constexpr int kMiscBytes = 512 + kItemBytes + kPlanBytes + 12;
+  static constexpr int kMaxEntries = HEAD_DIM == 128 && TILES == 1 ? kMaxLoneEntries : kMaxRowsEntries;
+  static constexpr int kPlanBytes = 4 * (kMaxEntries + 1) + 4 * kMaxEntries;
+  static constexpr int kLiveBytes = 2 * kMaxLoneEntries;  // PAGED: their numbers of live tokens
+  static constexpr int kMiscBytes = 512 + kItemBytes + kPlanBytes + kLiveBytes + 12;
   static constexpr int kSmemBytes = 1024 + kQBytes + kRingBytes + kMiscBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 256;  // after the two S slots of 128 columns
   static_assert(kSmemBytes <= 227 * 1024, "shared memory over budget");
+  static_assert(TILES == 2 || (TILES == 1 && HEAD_DIM != 64), "configurations that are instantiated");
   static_assert(kOCol + kTiles * HEAD_DIM <= kTmemCols, "TMEM column plan");
   static_assert(kStagesK % kTilesPerBlock == 0, "rings of whole blocks");
 };
 
 // IN_F16: q, k, v (and P) are fp16; otherwise bf16.  PAGED: see the top.
-template <int HEAD_DIM, bool IN_F16, bool PAGED>
-__global__ void __launch_bounds__(RowsCfg<HEAD_DIM>::kThreads, 1)
+template <int HEAD_DIM, int TILES, bool IN_F16, bool PAGED>
+__global__ void __launch_bounds__(RowsCfg<HEAD_DIM, TILES>::kThreads, 1)
 gqa_rows_kernel(const __grid_constant__ RowsParams p) {
-  using Cfg = RowsCfg<HEAD_DIM>;
+  using Cfg = RowsCfg<HEAD_DIM, TILES>;
   constexpr int NT = Cfg::kTiles, KCH = Cfg::kChunks, TCH = Cfg::kTileChunks, TPB = Cfg::kTilesPerBlock;
   constexpr uint32_t NSK = Cfg::kStagesK, NSV = Cfg::kStagesV;
+  constexpr int NQ = Cfg::kQSlots;
+  constexpr bool HALVES = TPB == 1;  // P is handed over in two halves
   constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1, kPlanWarp = kProducerWarp + 2;
 
   extern __shared__ uint8_t smem_raw[];
@@ -202,9 +215,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   uint64_t* bar = reinterpret_cast<uint64_t*>(misc);
   RowsItem* items_ring = reinterpret_cast<RowsItem*>(misc + 512);
   uint32_t* s_pre = reinterpret_cast<uint32_t*>(misc + 512 + Cfg::kItemBytes);
-  int32_t* s_len = reinterpret_cast<int32_t*>(s_pre + kMaxRowsEntries + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_len + kMaxRowsEntries);
+  int32_t* s_len = reinterpret_cast<int32_t*>(s_pre + Cfg::kMaxEntries + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_len + Cfg::kMaxEntries);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint16_t* s_live = reinterpret_cast<uint16_t*>(tmem_slot + 2);
 
   const uint32_t bar_base = ptx::smem_u32(bar);
   auto BAR = [&](int i) -> uint32_t { return bar_base + 8u * static_cast<uint32_t>(i); };
@@ -213,14 +227,17 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // awaited one is known to be complete; with one tile, QK(g) is issued ahead
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
-                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NT, S_FULL = Q_EMPTY + NT, P_HALF = S_FULL + 2,
+                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, P_HALF = S_FULL + 2,
                 P_FULL = P_HALF + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1,
                 ITEM_EMPTY = ITEM_FULL + kItemRing, N_BARRIERS = ITEM_EMPTY + kItemRing;
   static_assert(N_BARRIERS <= 64, "barrier words");
 
   // (a shuffle tells the compiler that it is the same in all the warp)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int n0 = p.plan.s[0].batch, n_entries = n0 + p.plan.s[1].batch;
+  const int n0 = p.plan.s[0].batch, n_entries = PAGED ? n0 : n0 + p.plan.s[1].batch;
+  // (of a launch that has but one, without an index)
+  auto section = [&](int i) -> const RowsSection& { return p.s[PAGED ? 0 : i]; };
+  auto plan_section = [&](int i) -> const RowsPlanSection& { return p.plan.s[PAGED ? 0 : i]; };
 
   // ---------------------------------------------------------------- set-up
   if (warp == 0) {
@@ -241,33 +258,42 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), Cfg::kTmemCols);
     ptx::tmem_relinquish();
   }
-  // Lengths may be produced, and outputs still read, by the previous kernel.
-  ptx::griddep_wait();
-  // The next launch may set itself up; it waits for this grid before it
-  // reads or writes anything this grid touches.
-  ptx::griddep_launch_dependents();
-  for (int i = threadIdx.x; i < n_entries; i += Cfg::kThreads) {
-    const int sec = i < n0 ? 0 : 1;
-    const int raw = p.s[sec].lens[i - (sec ? n0 : 0)], L = clamp_len(raw, p.plan.s[sec].max_len);
-    if (p.plan.dealt == 0) s_len[i] = L;
-    if (raw != L && blockIdx.x == 0) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
-    if (p.plan.dealt != 0 && blockIdx.x != 0) break;  // only flagged, by one CTA
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  if (p.every_piece != 0 && p.plan.dealt == 0) {
-    // the records of entries without keys, which the plan does not list: one
-    // thread of this kernel, an item at a time, takes ~0.5 us for each
-    for (int i = blockIdx.x; i < n_entries; i += p.plan.num_ctas) {  // empty_owner
-      if (s_len[i] > 0) continue;
-      const int sec = i < n0 ? 0 : 1, heads = p.plan.s[sec].heads;
-      int2* rec = p.rec + p.s[sec].rec + static_cast<long long>(i - (sec ? n0 : 0)) * heads;
-      for (int hh = threadIdx.x; hh < heads; hh += Cfg::kThreads)
-        if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, rec + hh, sizeof(int2))) rec[hh] = make_int2(-1, 0);
+  auto stage_lengths = [&](int first, int step) {
+    for (int i = first; i < n_entries; i += step) {
+      const int sec = i < n0 ? 0 : 1;
+      const int raw = section(sec).lens[i - (sec ? n0 : 0)], L = clamp_len(raw, plan_section(sec).max_len);
+      if (p.plan.dealt == 0) s_len[i] = L;
+      if (raw != L && blockIdx.x == 0) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
+      if (p.plan.dealt != 0 && blockIdx.x != 0) break;  // only flagged, by one CTA
     }
+  };
+  // PAGED, few entries: the plan's warp stages the lengths by itself and meets
+  // the others at this barrier there, so that it need not wait for them.
+  const bool one_warp = PAGED && p.plan.dealt == 0 && n_entries <= kMaxLoneEntries;
+  uint32_t tmem_base = 0;
+  if (!one_warp || warp != kPlanWarp) {
+    // Lengths may be produced, and outputs still read, by the previous kernel.
+    ptx::griddep_wait();
+    // The next launch may set itself up; it waits for this grid before it
+    // reads or writes anything this grid touches.
+    ptx::griddep_launch_dependents();
+    if (!one_warp) stage_lengths(static_cast<int>(threadIdx.x), Cfg::kThreads);
+    ptx::tc_fence_before();
+    ptx::named_barrier_sync(1, Cfg::kThreads);
+    if (p.every_piece != 0 && p.plan.dealt == 0 && warp < kProducerWarp) {
+      // the records of entries without keys, which the plan does not list: one
+      // thread of this kernel, an item at a time, takes ~0.5 us for each
+      for (int i = blockIdx.x; i < n_entries; i += p.plan.num_ctas) {  // empty_owner
+        if (s_len[i] > 0) continue;
+        const int sec = i < n0 ? 0 : 1, heads = plan_section(sec).heads;
+        int2* rec = p.rec + section(sec).rec + static_cast<long long>(i - (sec ? n0 : 0)) * heads;
+        for (int hh = threadIdx.x; hh < heads; hh += 32 * kProducerWarp)
+          if (detail::write_ok(p.err_word, p.rec, p.rec_bytes, rec + hh, sizeof(int2))) rec[hh] = make_int2(-1, 0);
+      }
+    }
+    ptx::tc_fence_after();
+    tmem_base = *tmem_slot;
   }
-  ptx::tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
 
   // The next item of this role (one thread, or a whole warp): waits for it,
   // copies it, releases its place.  False at the end of the work, or, with
@@ -286,7 +312,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   };
   // Q slots of an item: its row tiles that hold any token (at least one)
   auto slots_of = [&](const RowsItem& w) {
-    const RowsSection& s = p.s[w.section];
+    const RowsSection& s = section(w.section);
     return NT == 2 && s.split_keys == 0 && w.tok0 + s.tokens < (PAGED ? w.live : s.nq) ? 2 : 1;
   };
 
@@ -310,16 +336,16 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         return (lane << p.pages.box_shift) < kBlockN && pos < w.L ? detail::page_of(p.pages, p.err_word, w.b, pos) : 0;
       };
       auto load_block = [&](bool is_v, const RowsItem& w, int blk, int page_ids) -> bool {
-        const RowsSection& s = p.s[w.section];
+        const RowsSection& s = section(w.section);
 #pragma unroll
         for (int hf = 0; hf < TPB; ++hf) {
           const uint32_t n = is_v ? tv : tk, ns = is_v ? NSV : NSK, stage = n % ns;
           const uint32_t full = BAR((is_v ? V_FULL : K_FULL) + static_cast<int>(stage));
           // the first pass over a ring needs no wait
           if (n >= ns && !waited((is_v ? V_EMPTY : K_EMPTY) + static_cast<int>(stage), (n / ns) ^ 1u)) return false;
-          detail::check_coord(p.err_word, w.b >= 0 && w.b < p.plan.s[w.section].batch && w.h >= 0 &&
+          detail::check_coord(p.err_word, w.b >= 0 && w.b < plan_section(w.section).batch && w.h >= 0 &&
                                               (w.h + 1) * p.G <= p.Hq && blk >= 0 &&
-                                              blk * kBlockN < p.plan.s[w.section].max_len);
+                                              blk * kBlockN < plan_section(w.section).max_len);
           uint8_t* dst = (is_v ? vring : kring) + stage * Cfg::kStageBytes;
           if constexpr (PAGED) {
             // the boxes that hold any key of the block
@@ -350,11 +376,13 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       RowsItem it;
       while (next_item(it, ok, PAGED)) {
         if (it.blk_begin >= it.blk_end) continue;
-        const RowsSection& s = p.s[it.section];
-        const int nt = slots_of(it);
+        const RowsSection& s = section(it.section);
+        const int nt = slots_of(it), n = it.blk_end - it.blk_begin;
+        // (pages are looked up a block before they are asked for)
+        int ids = PAGED ? look_up(it, it.block(0)) : 0, ids1 = PAGED && n > 1 ? look_up(it, it.block(1)) : 0;
         for (int t = 0; t < nt; ++t, ++tq) {
-          const int slot = static_cast<int>(tq % NT);
-          if (tq >= NT && !waited(Q_EMPTY + slot, (tq / NT) ^ 1u)) {
+          const int slot = static_cast<int>(tq % NQ);
+          if (tq >= NQ && !waited(Q_EMPTY + slot, (tq / NQ) ^ 1u)) {
             ok = false;
             break;
           }
@@ -367,10 +395,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           }
           if (PAGED) __syncwarp();
         }
-        // K0, then K(i+1), V(i): at most one block of K ahead of its V.  (Pages
-        // are looked up a block before they are asked for.)
-        const int n = it.blk_end - it.blk_begin;
-        int ids = PAGED ? look_up(it, it.block(0)) : 0, ids1 = PAGED && n > 1 ? look_up(it, it.block(1)) : 0;
+        // K0, then K(i+1), V(i): at most one block of K ahead of its V
         if (ok) ok = load_block(false, it, it.block(0), ids);
         for (int i = 0; i < n && ok; ++i) {
           const int ids2 = PAGED && i + 2 < n ? look_up(it, it.block(i + 2)) : 0;
@@ -388,8 +413,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         ptx::mbar_wait_bounded(BAR(K_FULL + static_cast<int>(u % NSK)), (u / NSK) & 1u, nullptr, p.timeout_ns);
       for (uint32_t u = tv > NSV ? tv - NSV : 0u; u < tv; ++u)
         ptx::mbar_wait_bounded(BAR(V_FULL + static_cast<int>(u % NSV)), (u / NSV) & 1u, nullptr, p.timeout_ns);
-      for (uint32_t u = tq > NT ? tq - NT : 0u; u < tq; ++u)
-        ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(u % NT)), (u / NT) & 1u, nullptr, p.timeout_ns);
+      for (uint32_t u = tq > NQ ? tq - NQ : 0u; u < tq; ++u)
+        ptx::mbar_wait_bounded(BAR(Q_FULL + static_cast<int>(u % NQ)), (u / NQ) & 1u, nullptr, p.timeout_ns);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -419,7 +444,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         const int n = __shfl_sync(0xffffffffu, it.blk_end - it.blk_begin, 0);
         if (n <= 0) continue;
         const int nt = __shfl_sync(0xffffffffu, slots_of(it), 0);
-        for (int t = 0; t < nt; ++t) wait(Q_FULL + static_cast<int>((uq + t) % NT), (uq + t) / NT);
+        for (int t = 0; t < nt; ++t) wait(Q_FULL + static_cast<int>((uq + t) % NQ), (uq + t) / NQ);
         // The item's steps j, each a QK and a PV of one block: with two tiles
         // of rows, tile j % 2 and block j / 2; with split keys, tile j % 2 and
         // block j; with one tile, block j (in S slot j % 2 where two are free).
@@ -429,16 +454,16 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         // first, over P(j-1), whose PV is issued already.
         const bool two = nt == 2;
         const int steps = two ? 2 * n : n;
-        const int ahead = NT == 1 ? 1 : (two || __shfl_sync(0xffffffffu, p.s[it.section].split_keys, 0) != 0 ? 2 : 1);
+        const int ahead = NT == 1 ? 1 : (two || __shfl_sync(0xffffffffu, section(it.section).split_keys, 0) != 0 ? 2 : 1);
         // (16-byte units)  Shifted rows are at `shift` in their Q slot: the second tile reads it from its start,
         // the first one from there on, each with rows of other data beside its own.
-        const uint32_t q_shift = __shfl_sync(0xffffffffu, static_cast<uint32_t>(p.s[it.section].shift), 0) * 8;
+        const uint32_t q_shift = __shfl_sync(0xffffffffu, static_cast<uint32_t>(section(it.section).shift), 0) * 8;
         auto slot_of = [&](int j) -> uint32_t {
           return NT == 1 ? (u + static_cast<uint32_t>(j)) & 1u : (ahead == 2 ? static_cast<uint32_t>(j) & 1u : 0u);
         };
         auto block_of = [&](int j) -> uint32_t { return u + static_cast<uint32_t>(two ? j >> 1 : j); };
         auto qk = [&](int j) {
-          const uint32_t slot = slot_of(j), blk = block_of(j), qs = (uq + (two ? slot : 0u)) % NT;
+          const uint32_t slot = slot_of(j), blk = block_of(j), qs = (uq + (two ? slot : 0u)) % NQ;
 #pragma unroll
           for (int hf = 0; hf < TPB; ++hf) {
             const uint32_t m = blk * TPB + hf, stage = m % NSK;
@@ -461,12 +486,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
               ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>((blk * TPB + hf) % NSK)));
           }
           if (j + 1 == steps)
-            for (int t = 0; t < nt; ++t) ptx::mma_commit_elect(leader, BAR(Q_EMPTY + static_cast<int>((uq + t) % NT)));
+            for (int t = 0; t < nt; ++t) ptx::mma_commit_elect(leader, BAR(Q_EMPTY + static_cast<int>((uq + t) % NQ)));
         };
         auto pv = [&](int j) {
           const uint32_t slot = slot_of(j), blk = block_of(j);
           const uint32_t o_tmem = tmem_base + Cfg::kOCol + (NT == 1 ? 0u : slot * HEAD_DIM);
-          constexpr int KK = kBlockN / 16, PARTS = NT == 1 ? 1 : 2;
+          constexpr int KK = kBlockN / 16, PARTS = HALVES ? 2 : 1;
           const bool first = j < (NT == 1 ? 1 : ahead);
           // (V first: it has most often arrived, and P is the one waited for)
           if (TPB == 1 && (!two || slot == 0u)) wait(V_FULL + static_cast<int>(blk % NSV), blk / NSV);
@@ -519,6 +544,25 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     __syncwarp();
   } else if (warp == kPlanWarp) {
     // ========================================================== plan walker
+    if (one_warp) {
+      // Warm L2 with what this waits for, while the previous kernel finishes (a
+      // prefetch returns no data, so it cannot observe a value that kernel still
+      // writes): the lengths, and this CTA's share of the page table's lines.
+      if (lane * 32 < n_entries) {
+        ptx::prefetch_l2(section(0).lens + lane * 32);
+        if (p.pages.news != nullptr) ptx::prefetch_l2(p.pages.news + lane * 32);
+      }
+      const long long lines = (static_cast<long long>(n_entries) * p.pages.cols + 31) / 32;
+      const long long line = static_cast<long long>(lane) * p.plan.num_ctas + blockIdx.x;
+      if (line < lines) ptx::prefetch_l2(p.pages.table + line * 32);
+      ptx::griddep_wait();
+      ptx::griddep_launch_dependents();
+      stage_lengths(lane, 32);
+      for (int i = lane; i < n_entries; i += 32)
+        s_live[i] = static_cast<uint16_t>(detail::live_tokens(p.pages, p.err_word, i, s_len[i], section(0).nq));
+      __syncwarp();
+      ptx::named_barrier_sync(1, Cfg::kThreads);
+    }
     if (p.plan.dealt == 0) {
       // exclusive prefix sums of the entries' units
       uint32_t run = 0;
@@ -526,7 +570,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         const int i = base + lane;
         uint32_t units = 0;
         if (i < n_entries) {
-          const RowsPlanSection& s = p.plan.s[i < n0 ? 0 : 1];
+          const RowsPlanSection& s = plan_section(i < n0 ? 0 : 1);
           units = static_cast<uint32_t>(s.heads) * static_cast<uint32_t>(rows_units(s, s_len[i]));
         }
         uint32_t incl = units;
@@ -544,7 +588,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     if (lane == 0) {
       bool ok = true;
       int2 cut = make_int2(-1, 0);  // the cut triple that begins in this CTA
-      RowsPlanIter iter;
+      RowsPlanIterT<PAGED> iter;
       iter.init(&p.plan, p.s[0].lens, p.s[1].lens, s_len, s_pre, static_cast<int>(blockIdx.x));
       for (uint32_t n = 0; ok; ++n) {
         RowsWork w;
@@ -553,18 +597,20 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         it.blk_begin = -1;
         it.blk_end = -1;
         if (more) {
-          const RowsSection& s = p.s[w.section];
-          const int triple = w.b * p.plan.s[w.section].heads + w.hh;
+          const RowsSection& s = section(w.section);
+          const int triple = w.b * plan_section(w.section).heads + w.hh;
           const bool first_piece = w.blk_begin == 0;
           it.section = w.section;
           it.b = w.b;
-          it.h = w.hh / s.groups;
+          it.h = s.groups == 1 ? w.hh : w.hh / s.groups;
           it.tok0 = (w.hh - it.h * s.groups) * (NT * s.tokens);
           it.blk_begin = w.blk_begin;
           it.blk_end = w.blk_end;
           it.turn = w.turn;
           it.L = w.L;
-          it.live = PAGED ? detail::live_tokens(p.pages, p.err_word, w.b, w.L, s.nq) : s.nq;
+          it.live = !PAGED     ? s.nq
+                    : one_warp ? static_cast<int>(s_live[w.b])
+                               : detail::live_tokens(p.pages, p.err_word, w.b, w.L, s.nq);
           // A group behind the entry's last token has nothing to do but to leave
           // its rows empty: without keys, whole, wherever it was cut.
           if (PAGED && it.tok0 >= it.live) it.blk_end = it.blk_begin;
@@ -634,20 +680,20 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       const int n_blk = it.blk_end - it.blk_begin;
       const uint32_t u0 = u;
       u += static_cast<uint32_t>(n_blk);
-      const bool split_keys = NT == 2 && p.s[it.section].split_keys != 0;
+      const bool split_keys = NT == 2 && section(it.section).split_keys != 0;
       const bool idle = !split_keys && t >= slots_of(it);
       // (PAGED: an idle tile may still hold rows of tokens that the entry lacks)
-      if (idle && (!PAGED || it.tok0 + t * p.s[it.section].tokens >= p.s[it.section].nq)) continue;
-      const int rows = p.s[it.section].tokens * p.G;   // of a tile
-      const int first_lane = t == 1 ? p.s[it.section].shift : 0;
+      if (idle && (!PAGED || it.tok0 + t * section(it.section).tokens >= section(it.section).nq)) continue;
+      const int rows = section(it.section).tokens * p.G;   // of a tile
+      const int first_lane = t == 1 ? section(it.section).shift : 0;
       const int rr = r - first_lane;                   // the row within the tile
       const bool active = rr >= lane && rr - lane < rows;  // this warp holds any of them
       // the last key this row sees is L - 1, or (causal) L - nq + its token; all
       // tokens of a causal section are in one tile, and both hold that one (check_prefix)
-      const int causal_cut = !PAGED && p.s[it.section].causal != 0 ? p.s[it.section].nq - 1 : 0;
+      const int causal_cut = !PAGED && section(it.section).causal != 0 ? section(it.section).nq - 1 : 0;
       const int sees = it.L - causal_cut + (causal_cut != 0 ? it.tok0 + rr / p.G : 0);
       // PAGED: this row's token, and the first key that its branch may hide
-      const int tok_row = PAGED ? it.tok0 + (split_keys ? 0 : t * p.s[it.section].tokens) + rr / p.G : 0;
+      const int tok_row = PAGED ? it.tok0 + (split_keys ? 0 : t * section(it.section).tokens) + rr / p.G : 0;
       const int drafts = it.L - it.live;
       const bool dead = PAGED && tok_row >= it.live;
       const int step = split_keys ? 2 : 1, i0 = PAGED && idle ? n_blk : split_keys ? t : 0;
@@ -658,6 +704,11 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         const uint32_t slot = NT == 2 ? static_cast<uint32_t>(t) : (g & 1u);
         const uint32_t s_addr = tmem_base + lanes + slot * kBlockN;
         const bool first = i == i0;
+        // PAGED: the words that hold the bits of this block's keys, fetched while its scores are computed
+        const bool hides = PAGED && (blk + 1) * kBlockN > (p.pages.chain != 0 || p.pages.tree != nullptr ? drafts : it.L);
+        uint32_t branch[5];
+        if (hides)
+          detail::branch_words(branch, p.pages, it.b, section(it.section).nq, dead ? 0 : tok_row, blk * kBlockN - drafts);
         if (!wait(S_FULL + static_cast<int>(slot), NT == 2 ? g : g >> 1)) break;
         const int tail = it.L - blk * kBlockN;  // keys of this block
         if (tail < kBlockN) {
@@ -670,7 +721,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           // them the one that read the stage's V before (one tile: that is
           // PV(g-1), issued after this S, and waited for).
           // (PAGED: nor did TMA write what no page of this entry holds)
-          const int cap = PAGED ? kBlockN : min(p.plan.s[it.section].max_len - blk * kBlockN, kBlockN);
+          const int cap = PAGED ? kBlockN : min(plan_section(it.section).max_len - blk * kBlockN, kBlockN);
           if ((t == 0 || split_keys) && cap > tail) {
             if constexpr (NT == 1) {
               if (g >= 1 && !wait_pv(g - 1)) break;
@@ -693,7 +744,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         }
         if (!active) {  // no row of this warp is read: whatever its lanes hold may stand for P
           __syncwarp();
-          if (NT == 2 && lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
+          if (HALVES && lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
           if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + static_cast<int>(slot)));
           continue;
         }
@@ -704,13 +755,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         ptx::tmem_wait_ld();
 
         if constexpr (PAGED) {
-          if ((blk + 1) * kBlockN > (p.pages.chain != 0 || p.pages.tree != nullptr ? drafts : it.L)) {
-            const uint32_t* branch = detail::branch_of(p.pages, it.b, p.s[it.section].nq, dead ? 0 : tok_row);
+          if (hides) {
             const int seen = p.pages.chain != 0 ? min(tail, drafts + tok_row + 1 - blk * kBlockN) : tail;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
-              const uint32_t vis = detail::seen_bits(seen - c) &
-                                   detail::branch_bits(branch, p.pages.tree_words, blk * kBlockN + c - drafts);
+              const uint32_t vis =
+                  detail::seen_bits(seen - c) & __funnelshift_r(branch[c / 32], branch[c / 32 + 1], blk * kBlockN - drafts);
               if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
 #pragma unroll
               for (int j = c; j < c + 32; ++j) x[j] = (vis >> (j - c)) & 1u ? x[j] : 0xff800000u;  // -inf
@@ -783,7 +833,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           exps(c);
-          if (NT == 2 && c == 6) {  // the first half's stores, up to columns 79 by now, have had time
+          if (HALVES && c == 6) {  // the first half's stores, up to columns 79 by now, have had time
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
@@ -821,7 +871,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         if (!wait_pv(g - 1)) break;
         ptx::tc_fence_after();
       }
-      const RowsSection& sec = p.s[it.section];
+      const RowsSection& sec = section(it.section);
       if (partial) {
         // O as it stands, with its maximum and sum: the merge normalises.  Rows
         // of tokens past the last one have a place too, which nothing reads.

@@ -264,4 +264,85 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
   detail::write_row<HEAD_DIM>(sum[0], p.out, p.lse, p.out_dtype, row);
 }
 
+// The rows of a launch of one section whose triples hold many, a triple to
+// blockIdx.x (CUT: the cut triple, if any, that begins in that CTA of the launch)
+// and a group of its rows to blockIdx.y.  A warp takes R rows, whose pieces are the
+// same number of the same places, and has R x kBatch of them in flight: the two
+// kernels above have as many for one row or two, wait as long for each, and take
+// as many more waves of CTAs (whole calls over pages, us: 16 x 8 tiles of 104 rows of
+// 128 elements 63.7, not 65.6; 32 x 8 of 64 rows 41.8, not 43.7; 48 of 128 rows of 256
+// elements 58.9, not 60.3).
+constexpr int kTileMergeThreads = 128;
+template <int HEAD_DIM>
+constexpr int kTileMergeRows = HEAD_DIM == 256 ? 2 : 4;
+
+template <int HEAD_DIM, bool CUT>
+__global__ void __launch_bounds__(kTileMergeThreads)
+gqa_tile_merge_kernel(const RowsMergeParams p) {
+  constexpr int VEC = HEAD_DIM / 32, R = kTileMergeRows<HEAD_DIM>, kBatch = 2;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const RowsMergeSection& s = p.s[0];
+  const int lane = threadIdx.x & 31;
+  const int2 rec = p.rec[s.rec + blockIdx.x];
+  const int tile_rows = s.tokens * p.G, own_tiles = s.split_keys ? 1 : p.tiles;  // tiles with rows of their own
+  const long long piece_rows = static_cast<long long>(p.tiles) * tile_rows;
+  int triple = static_cast<int>(blockIdx.x), n = 0;
+  long long first, next, stride;
+  if constexpr (CUT) {
+    triple = rec.x;
+    if (rec.x < 0 || rec.y <= 0 || 2 * (static_cast<int>(blockIdx.x) + rec.y) > s.pieces) return;
+    n = rec.y;
+    first = (2ll * blockIdx.x + 1) * piece_rows;
+    next = 2ll * (blockIdx.x + 1) * piece_rows;
+    stride = 2ll * piece_rows;
+  } else {
+    const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
+    n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
+    first = s.part_row + rec.x * piece_rows;
+    stride = s.split_keys ? tile_rows : piece_rows;
+    next = first + stride;
+  }
+  const int rows = own_tiles * tile_rows;
+  const int i0 = (static_cast<int>(blockIdx.y) * (kTileMergeThreads / 32) + static_cast<int>(threadIdx.x >> 5)) * R;
+  if (i0 >= rows) return;
+  const int i = i0 + R <= rows ? i0 : (rows >= R ? rows - R : 0);  // (past the last row: the last again)
+  detail::RowSum<VEC> sum[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) sum[r].clear();
+  for (int j0 = 0; j0 < n; j0 += kBatch) {
+    float2 ml[kBatch][R];
+    float v[kBatch][R][VEC];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      if (j0 + q >= n) break;
+      const long long at = (j0 + q == 0 ? first : next + (j0 + q - 1) * stride) + i;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const long long row = at + (i + r < rows ? r : 0);
+        ml[q][r] = p.ml_part[row];
+        detail::load_vec<VEC>(p.o_part + row * HEAD_DIM + lane * VEC, v[q][r]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      if (j0 + q >= n) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) sum[r].add(ml[q][r], v[q][r]);
+    }
+  }
+  const int per_batch = p.kv_heads * s.groups;
+  const int b = triple / per_batch, hg = triple - b * per_batch;
+  const int h = hg / s.groups, grp = hg - h * s.groups;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (i + r >= rows) break;
+    const int t = (i + r) / tile_rows, in_tile = i + r - t * tile_rows;
+    const int tok = (grp * own_tiles + t) * s.tokens + in_tile / p.G;
+    if (tok >= s.nq) continue;
+    const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + in_tile % p.G;
+    detail::write_row<HEAD_DIM>(sum[r], p.out, p.lse, p.out_dtype, row);
+  }
+}
+
 }  // namespace gqa

@@ -30,6 +30,35 @@
 namespace gqa {
 
 constexpr int kMaxRowsEntries = 4096;  // batch entries whose lengths are staged in shared memory
+// The same with one tile at head_dim 128, whose rings take the place of the rest;
+// and so few that the plan's warp stages them alone.
+constexpr int kMaxLoneEntries = 128;
+
+// x / d for a divisor that a launch keeps: a multiplication by 2^32 / d, rounded
+// up, is too large by x / 2^32 at most, and so the quotient by one.  (A division
+// is some 35 dependent instructions, and a CTA's first K load waits for six.)
+struct RowsDivisor {
+  uint32_t d, m;
+};
+GQA_HD RowsDivisor rows_divisor(int d) {
+  return RowsDivisor{static_cast<uint32_t>(d), d == 1 ? 0u : static_cast<uint32_t>((1ull << 32) / static_cast<uint32_t>(d)) + 1u};
+}
+GQA_HD uint32_t div_by(uint32_t x, const RowsDivisor& by) {  // x below 2^31
+  if (by.d == 1) return x;
+  const uint32_t q = static_cast<uint32_t>((static_cast<uint64_t>(x) * by.m) >> 32);
+  return q * by.d > x ? q - 1 : q;
+}
+// x / d for quotients below 2^20, in fp32: off by one at most, before it is put right.
+GQA_HD uint32_t div_small(uint32_t x, uint32_t d) {
+#ifdef __CUDA_ARCH__
+  uint32_t q = static_cast<uint32_t>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+  if (q * d > x) --q;
+  if (x - q * d >= d) ++q;
+  return q;
+#else
+  return x / d;
+#endif
+}
 
 struct RowsPlanSection {
   int batch;        // entries (0: no such section)
@@ -39,12 +68,14 @@ struct RowsPlanSection {
   int item_units;
   int empty_units;  // of a triple without blocks; 0: such triples are not listed
   int groups;       // triples that share an entry's keys of one KV head
+  RowsDivisor block_div;  // block_units
 };
 
 struct RowsPlan {
   RowsPlanSection s[2];
   int num_ctas;
   int dealt;        // whole triples in turn, instead of equal ranges
+  RowsDivisor ctas_div;  // num_ctas
 };
 
 struct RowsWork {
@@ -61,8 +92,13 @@ GQA_HD int rows_units(const RowsPlanSection& s, int L) {
   return nblk > 0 ? nblk * s.block_units + s.item_units : s.empty_units;
 }
 
-struct RowsPlanIter {
+// ONE: the plan has one section, whose numbers then stay in registers (a CTA's
+// first K load waits for this code, and reading them through a pointer, one after
+// another, was half of its time).
+template <bool ONE>
+struct RowsPlanIterT {
   const RowsPlan* rp;
+  RowsPlanSection one;
   const int32_t* lens;     // clamped lengths of both sections' entries (dealt: unused)
   const uint32_t* pre;     // entries + 1 prefix sums of their units
   const int32_t* raw0;     // each section's lengths
@@ -76,30 +112,47 @@ struct RowsPlanIter {
   GQA_HD uint32_t start(uint32_t c) const { return c * q + (c < rem ? c : rem); }
   GQA_HD int owner(uint32_t u) const {
     const uint32_t split = rem * (q + 1);
-    return static_cast<int>(u < split ? u / (q + 1) : rem + (u - split) / q);
+    return static_cast<int>(u < split ? div_small(u, q + 1) : rem + div_small(u - split, q));  // below num_ctas
   }
   // The first entry from `a` on that holds units past u (the number of entries if none does).
   GQA_HD int reaching(uint32_t u, int a) const {
-    int z = rp->s[0].batch + rp->s[1].batch;
+    int z = entries();
     while (a < z) {
       const int mid = (a + z) / 2;
       if (pre[mid + 1] > u) z = mid; else a = mid + 1;
     }
     return a;
   }
-  GQA_HD const RowsPlanSection& section(int entry) const { return rp->s[entry < rp->s[0].batch ? 0 : 1]; }
+  GQA_HD int entries() const {
+    if constexpr (ONE) return one.batch;
+    else return rp->s[0].batch + rp->s[1].batch;
+  }
+  GQA_HD int section_of(int entry) const {
+    if constexpr (ONE) return 0;
+    else return entry < rp->s[0].batch ? 0 : 1;
+  }
+  GQA_HD const RowsPlanSection& section(int entry) const {
+    if constexpr (ONE) return one;
+    else return rp->s[section_of(entry)];
+  }
 
   GQA_HD void init(const RowsPlan* plan, const int32_t* lens0, const int32_t* lens1, const int32_t* clamped,
                    const uint32_t* prefix, int c) {
     rp = plan; lens = clamped; pre = prefix; raw0 = lens0; raw1 = lens1; cta = c;
     next_triple = c;
+    if constexpr (ONE) one = plan->s[0];
     if (rp->dealt) return;
-    const int E = rp->s[0].batch + rp->s[1].batch;
+    const int E = entries();
     U = pre[E];
-    const uint32_t w0 = static_cast<uint32_t>(rp->s[0].block_units), w1 = static_cast<uint32_t>(rp->s[1].block_units);
-    const uint32_t most = U / (w0 > w1 ? w0 : w1);  // ranges at least a block long
-    C = most < 1 ? 1 : (most < static_cast<uint32_t>(rp->num_ctas) ? most : static_cast<uint32_t>(rp->num_ctas));
-    q = U / C;
+    uint32_t w = static_cast<uint32_t>(rp->s[0].block_units);
+    if constexpr (!ONE) w = w > static_cast<uint32_t>(rp->s[1].block_units) ? w : static_cast<uint32_t>(rp->s[1].block_units);
+    C = static_cast<uint32_t>(rp->num_ctas);
+    q = div_by(U, rp->ctas_div);
+    if (q < w) {  // ranges at least a block long
+      const uint32_t most = U / w;
+      C = most < 1 ? 1 : most;
+      q = U / C;
+    }
     rem = U - q * C;
     hh = 0;
     if (static_cast<uint32_t>(c) >= C) {  // this CTA owns nothing
@@ -111,10 +164,14 @@ struct RowsPlanIter {
     hi = start(static_cast<uint32_t>(c) + 1);
     e = reaching(lo, 0);
     if (e < E && pre[e] < lo)
-      hh = static_cast<int>((lo - pre[e]) / static_cast<uint32_t>(rows_units(section(e), lens[e])));
+      hh = static_cast<int>(div_heads(lo - pre[e], static_cast<uint32_t>(rows_units(section(e), lens[e])), section(e)));
+  }
+  // the triple that holds an entry's unit x: one of its heads
+  GQA_HD static uint32_t div_heads(uint32_t x, uint32_t units, const RowsPlanSection& s) {
+    return s.heads < (1 << 20) ? div_small(x, units) : x / units;
   }
   GQA_HD void emit(RowsWork& w, int blk_begin, int blk_end, int whole, int pieces) {
-    w.section = e < rp->s[0].batch ? 0 : 1;
+    w.section = section_of(e);
     w.b = e - (w.section ? rp->s[0].batch : 0);
     w.hh = hh;
     w.L = lens[e];
@@ -144,7 +201,7 @@ struct RowsPlanIter {
   }
   GQA_HD bool next(RowsWork& w) {
     if (rp->dealt) return next_dealt(w);
-    const int E = rp->s[0].batch + rp->s[1].batch;
+    const int E = entries();
     while (e < E) {
       const RowsPlanSection& s = section(e);
       const uint32_t u = static_cast<uint32_t>(rows_units(s, lens[e]));
@@ -165,8 +222,8 @@ struct RowsPlanIter {
         const uint32_t bu = static_cast<uint32_t>(s.block_units);
         const uint32_t first = v + static_cast<uint32_t>(s.item_units);  // where block 0 begins
         const uint32_t last = first + (nblk - 1) * bu;                    // and the last one
-        const uint32_t from = lo > first ? (lo - first + bu - 1) / bu : 0;
-        const uint32_t upto = hi > last ? nblk : (hi > first ? (hi - first + bu - 1) / bu : 0);
+        const uint32_t from = lo > first ? div_by(lo - first + bu - 1, s.block_div) : 0;
+        const uint32_t upto = hi > last ? nblk : (hi > first ? div_by(hi - first + bu - 1, s.block_div) : 0);
         if (from < upto) {
           const bool whole = from == 0 && upto == nblk;
           emit(w, static_cast<int>(from), static_cast<int>(upto), whole,
@@ -189,6 +246,8 @@ struct RowsPlanIter {
     return false;
   }
 };
+
+using RowsPlanIter = RowsPlanIterT<false>;
 
 // The CTA that records the triples of entry e (of both sections) that has no
 // keys, in launches that do not list those.
