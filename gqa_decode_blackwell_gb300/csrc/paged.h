@@ -12,6 +12,9 @@
 #include <cstdint>
 
 #include "plan.cuh"
+#ifdef __CUDACC__
+#include "sm103_ptx.cuh"
+#endif
 
 namespace gqa {
 
@@ -37,6 +40,54 @@ __device__ __forceinline__ int page_of(const PagedKeys& k, unsigned int* err_wor
   if (static_cast<unsigned>(page) < static_cast<unsigned>(k.num_pages)) return page;
   atomicOr(err_word, kErrBadIndex);
   return k.num_pages;
+}
+
+// This lane's page of block blk of entry b, which has L positions: that of the
+// block's box `lane`, if it has one that holds any.
+__device__ __forceinline__ int lane_page(const PagedKeys& k, unsigned int* err_word, int b, int blk, int L, int lane) {
+  const int in_block = lane << k.box_shift, pos = blk * kBlockN + in_block;
+  return in_block < kBlockN && pos < L ? page_of(k, err_word, b, pos) : 0;
+}
+
+// The boxes of block blk of KV head h that hold any of the entry's L positions,
+// into a tile at shared address dst: `chunks` of 64 elements, 16 KB apart, from
+// element `elem` on.  Their bytes are expected at `bar`.  The whole warp calls it,
+// with the block's pages (lane_page), and the thread that `issues` issues.  (Pages
+// are handed over four at a time: one by one, boxes of 16 positions bound wide
+// heads, 68 us a call of eight trees of 40 tokens, 63 so.)
+template <int CHUNKS>
+__device__ __forceinline__ void load_pages(const PagedKeys& k, const void* map, uint32_t bar, uint32_t dst, int blk,
+                                           int L, int h, int elem, int pages, bool issues, uint64_t policy) {
+  const int box = 1 << k.box_shift, first = blk * kBlockN;
+  const int held = (min(L - first, kBlockN) + box - 1) >> k.box_shift;
+  if (issues) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(held * box * CHUNKS * 128));
+#pragma unroll 1
+  for (int i0 = 0; i0 < held; i0 += 4) {
+    int page[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) page[i] = __shfl_sync(0xffffffffu, pages, i0 + i);
+    if (issues) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= held) break;
+        const int at = (i0 + i) << k.box_shift;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+          ptx::tma_load_4d_hint(dst + c * 16384 + at * 128, map, bar, elem + c * 64, h, (first + at) & k.page_mask, page[i],
+                                policy);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Warms L2 with one of `ctas` CTAs' share of the page table's lines (as far as a
+// warp's lanes reach).  A prefetch returns no data, so it may run before the
+// previous kernel has finished.
+__device__ __forceinline__ void prefetch_table(const PagedKeys& k, int entries, int ctas, int lane) {
+  const long long lines = (static_cast<long long>(entries) * k.cols + 31) / 32;
+  const long long line = static_cast<long long>(lane) * ctas + blockIdx.x;
+  if (line < lines) ptx::prefetch_l2(k.table + line * 32);
 }
 
 // New tokens of entry b, which has L positions: at most nq, and at most L.

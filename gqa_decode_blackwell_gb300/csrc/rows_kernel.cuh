@@ -326,14 +326,15 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       uint32_t tk = 0, tv = 0, tq = 0;  // ring tiles and Q slots loaded
       bool ok = true;
       const bool issues = PAGED ? ptx::elect_one() != 0 : true;
+      // PAGED: keys that only one tile group reads are read once, and then need not
+      // push partials out of L2 (16 trees of 26 tokens 60 us a call, 63 without)
+      const uint64_t policy = PAGED && p.s[0].groups == 1 ? ptx::l2_policy_evict_first() : ptx::l2_policy_evict_normal();
       auto waited = [&](int i, uint32_t parity) -> bool {
         const bool done = ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns);
         return PAGED ? __all_sync(0xffffffffu, done) : done;
       };
-      // PAGED: the pages of a block's boxes, one to a lane
-      auto look_up = [&](const RowsItem& w, int blk) -> int {
-        const int pos = blk * kBlockN + (lane << p.pages.box_shift);
-        return (lane << p.pages.box_shift) < kBlockN && pos < w.L ? detail::page_of(p.pages, p.err_word, w.b, pos) : 0;
+      auto look_up = [&](const RowsItem& w, int blk) {
+        return detail::lane_page(p.pages, p.err_word, w.b, blk, w.L, lane);
       };
       auto load_block = [&](bool is_v, const RowsItem& w, int blk, int page_ids) -> bool {
         const RowsSection& s = section(w.section);
@@ -348,20 +349,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
                                               blk * kBlockN < plan_section(w.section).max_len);
           uint8_t* dst = (is_v ? vring : kring) + stage * Cfg::kStageBytes;
           if constexpr (PAGED) {
-            // the boxes that hold any key of the block
-            const int box = 1 << p.pages.box_shift, first = blk * kBlockN;
-            const int held = (min(w.L - first, kBlockN) + box - 1) >> p.pages.box_shift;
-            if (issues) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(held * box * TCH * 128));
-            for (int i = 0; i < held; ++i) {
-              const int page = __shfl_sync(0xffffffffu, page_ids, i);
-              if (issues) {
-#pragma unroll
-                for (int kc = 0; kc < TCH; ++kc)
-                  ptx::tma_load_4d(ptx::smem_u32(dst + kc * 16384 + i * box * 128), is_v ? &s.tm_v : &s.tm_k, full,
-                                   (hf * TCH + kc) * 64, w.h, (first + i * box) & p.pages.page_mask, page);
-              }
-              __syncwarp();
-            }
+            detail::load_pages<TCH>(p.pages, is_v ? &s.tm_v : &s.tm_k, full, ptx::smem_u32(dst), blk, w.L, w.h,
+                                    hf * TCH * 64, page_ids, issues, policy);
           } else {
             ptx::mbar_arrive_expect_tx(full, Cfg::kStageBytes);
 #pragma unroll
@@ -552,9 +541,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         ptx::prefetch_l2(section(0).lens + lane * 32);
         if (p.pages.news != nullptr) ptx::prefetch_l2(p.pages.news + lane * 32);
       }
-      const long long lines = (static_cast<long long>(n_entries) * p.pages.cols + 31) / 32;
-      const long long line = static_cast<long long>(lane) * p.plan.num_ctas + blockIdx.x;
-      if (line < lines) ptx::prefetch_l2(p.pages.table + line * 32);
+      detail::prefetch_table(p.pages, n_entries, p.plan.num_ctas, lane);
       ptx::griddep_wait();
       ptx::griddep_launch_dependents();
       stage_lengths(lane, 32);

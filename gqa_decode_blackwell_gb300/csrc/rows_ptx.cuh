@@ -39,6 +39,13 @@ __device__ __forceinline__ uint32_t elect_one() {
   return p;
 }
 
+// L2 policy of data that is read again (beside l2_policy_evict_first).
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
 // MMAs issued by the elected thread of a warp that stays converged, so that
 // descriptors and addresses live in uniform registers: issued by one thread
 // of a diverged warp, whose operands must be moved there one by one, an MMA
