@@ -15,13 +15,14 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "decode_kernel.cuh"
 #include "paged.h"
 
 namespace gqa {
 
-constexpr int kRotaryThreads = 128;
+constexpr int kRotaryThreads = 256;  // of a CTA, at most
 constexpr int kMaxPairs = 128;  // of a head: head_dim / 2
 
 // Tokens' heads to rotate or copy: `heads` of each token, dense, `stride`
@@ -68,26 +69,63 @@ __device__ __forceinline__ float2 turn_of(uint64_t turns, int position, int inve
   return make_float2(r.x * magnitude, r.y * magnitude);
 }
 
-// 8 consecutive elements, as fp32 and as they are in memory.
-template <typename T>
-struct Eight {
-  uint4 raw[sizeof(T) / 2];
+// N consecutive elements (N * sizeof(T) bytes, aligned to as many or to 16), two
+// to a word where they are of 16 bits.
+template <typename T, int N>
+struct Run {
+  static constexpr int kBytes = N * static_cast<int>(sizeof(T)), kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
   __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x; w[1] = v.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
+    }
   }
   __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kBytes == 2) {
+      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = raw[i];
+      for (int i = 0; i < kWords; i += 4)
+        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
   }
-  __device__ __forceinline__ float get(int e) const { return to_f32(reinterpret_cast<const T*>(raw)[e]); }
-  __device__ __forceinline__ void set(int e, float v) { from_f32(reinterpret_cast<T*>(raw)[e], v); }
-  static __device__ __forceinline__ float to_f32(float v) { return v; }
-  static __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-  static __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ void from_f32(float& d, float v) { d = v; }
-  static __device__ __forceinline__ void from_f32(__half& d, float v) { d = __float2half_rn(v); }
-  static __device__ __forceinline__ void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[e]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      return __half2float(__ushort_as_half(static_cast<unsigned short>(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu)));
+    } else {
+      return __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+  }
+  // elements e and e + 1 (e even); the second is lost in a run of one
+  __device__ __forceinline__ void set2(int e, float lo, float hi) {
+    if constexpr (sizeof(T) == 4) {
+      w[e] = __float_as_uint(lo);
+      if constexpr (N > 1) w[e + 1] = __float_as_uint(hi);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 v = __floats2half2_rn(lo, hi);
+      w[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+      w[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
 };
 
 __device__ __forceinline__ void turn(float2 cs, float a, float b, float& ra, float& rb) {
@@ -95,115 +133,86 @@ __device__ __forceinline__ void turn(float2 cs, float a, float b, float& ra, flo
   rb = a * cs.y + b * cs.x;
 }
 
-// Where 16 elements of a head that one thread takes begin: its i-th of
-// head_dim / 16.  Pairs of halves: two runs of 8 that are each other's partners
-// as long as there are any, then 16 in a row; else 16 in a row.
-template <bool INTERLEAVED>
+// Where the two runs of N elements that one thread takes of a head begin, its
+// i-th pair of them.  Pairs of halves: each other's partners as long as there are
+// any, then 2 N in a row; else 2 N in a row.
+template <bool INTERLEAVED, int N>
 __device__ __forceinline__ int2 runs_of(int i, int pairs) {
-  if (!INTERLEAVED && 8 * i < pairs) return make_int2(8 * i, pairs + 8 * i);
-  return make_int2(16 * i, 16 * i + 8);
+  if (!INTERLEAVED && N * i < pairs) return make_int2(N * i, pairs + N * i);
+  return make_int2(2 * N * i, 2 * N * i + N);
 }
 
-template <typename T, bool INTERLEAVED>
-__device__ __forceinline__ void turn_runs(Eight<T>& a, Eight<T>& b, const float2* table, int i, int pairs) {
+template <typename T, bool INTERLEAVED, int N>
+__device__ __forceinline__ void turn_runs(Run<T, N>& a, Run<T, N>& b, const float2* table, int i, int pairs) {
   if constexpr (INTERLEAVED) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      Eight<T>& v = e < 4 ? a : b;
-      if (8 * i + e >= pairs) continue;
+    for (int e = 0; e < N; ++e) {
+      Run<T, N>& v = e < N / 2 ? a : b;
+      constexpr int H = N / 2;
+      if (N * i + e >= pairs) continue;
       float ra, rb;
-      turn(table[8 * i + e], v.get(2 * (e & 3)), v.get(2 * (e & 3) + 1), ra, rb);
-      v.set(2 * (e & 3), ra);
-      v.set(2 * (e & 3) + 1, rb);
+      turn(table[N * i + e], v.get(2 * (e % H)), v.get(2 * (e % H) + 1), ra, rb);
+      v.set2(2 * (e % H), ra, rb);
     }
   } else {
-    if (8 * i >= pairs) return;
+    if (N * i >= pairs) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float ra, rb;
-      turn(table[8 * i + e], a.get(e), b.get(e), ra, rb);
-      a.set(e, ra);
-      b.set(e, rb);
+    for (int e = 0; e < N; e += 2) {
+      float ra[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 2 && e + k < N; ++k) turn(table[N * i + e + k], a.get(e + k), b.get(e + k), ra[k], rb[k]);
+      a.set2(e, ra[0], ra[1]);
+      b.set2(e, rb[0], rb[1]);
     }
   }
 }
 
-// The rows of one CTA: head r of them is at src(r) and goes to dst(r); those
-// with rotated(r) are rotated by the table, of which `ready` waits once.
-// VEC: 16 elements a thread at a time, where partners are whole runs of 8 apart
-// (interleaved, or halves of a multiple of 8 pairs); else a pair at a time, which
-// takes any even number of rotated elements (20 of 64, 12 heads: as fast at 77
-// tokens, a third of the rate at 8192).
-template <typename T, bool INTERLEAVED, bool VEC, typename Src, typename Dst, typename Rotated, typename Ready>
-__device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, const float2* table, int part,
-                                           int parts, const Src& src, const Dst& dst, const Rotated& rotated,
-                                           const Ready& ready) {
-  const int per_row = head_dim / (VEC ? 16 : 2), n = n_rows * per_row, step = parts * kRotaryThreads;
-  int u = part * kRotaryThreads + static_cast<int>(threadIdx.x);
-  if constexpr (VEC) {
-    Eight<T> a, b;
-    int r = 0, i = 0;
-    auto load = [&] {
-      r = u / per_row;
-      i = u - r * per_row;
-      const int2 at = runs_of<INTERLEAVED>(i, rotated(r) ? pairs : 0);
-      const T* from = src(r);
-      a.load(from + at.x);
-      b.load(from + at.y);
-    };
-    if (u < n) load();
-    ready();  // with the first loads under way
-    while (u < n) {
-      const bool turns = rotated(r);
-      if (turns) turn_runs<T, INTERLEAVED>(a, b, table, i, pairs);
-      T* to = dst(r);
-      if (to != nullptr) {
-        const int2 at = runs_of<INTERLEAVED>(i, turns ? pairs : 0);
-        a.store(to + at.x);
-        b.store(to + at.y);
-      }
-      if ((u += step) < n) load();
+// The rows of one CTA: head r of them is at src(r) and goes to dst(r) (nowhere, if
+// that is null); those with rotated(r) are rotated by the table, which `ready`
+// fills while the first loads are under way.  (The next two runs loaded ahead cost
+// registers, and so CTAs: prompts 24.0 us, 19.7 without.)
+template <typename T, bool INTERLEAVED, int N, typename Src, typename Dst, typename Rotated, typename Ready>
+__device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, const float2* table, const Src& src,
+                                           const Dst& dst, const Rotated& rotated, const Ready& ready) {
+  // units of a row: a power of two, as head_dim and N are
+  const int row_shift = 31 - __clz(head_dim / (2 * N)), n = n_rows << row_shift;
+  const int step = static_cast<int>(gridDim.y * blockDim.x);
+  int u = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x);
+  Run<T, N> a, b;
+  int r = 0, i = 0;
+  auto load = [&] {
+    r = u >> row_shift;
+    i = u - (r << row_shift);
+    const int2 at = runs_of<INTERLEAVED, N>(i, rotated(r) ? pairs : 0);
+    const T* from = src(r);
+    a.load(from + at.x);
+    b.load(from + at.y);
+  };
+  if (u < n) load();
+  ready();
+  while (u < n) {
+    const bool turns = rotated(r);
+    if (turns) turn_runs<T, INTERLEAVED, N>(a, b, table, i, pairs);
+    T* to = dst(r);
+    if (to != nullptr) {
+      const int2 at = runs_of<INTERLEAVED, N>(i, turns ? pairs : 0);
+      a.store(to + at.x);
+      b.store(to + at.y);
     }
-  } else {
-    T a, b;
-    int r = 0, lo = 0, hi = 0;
-    bool turns = false;
-    int i = 0;
-    auto load = [&] {
-      r = u / per_row;
-      i = u - r * per_row;
-      turns = rotated(r) && i < pairs;  // (else two elements past the pairs, as they are; only halves come here)
-      lo = turns ? i : 2 * i;
-      hi = turns ? i + pairs : 2 * i + 1;
-      a = src(r)[lo];
-      b = src(r)[hi];
-    };
-    if (u < n) load();
-    ready();
-    while (u < n) {
-      if (turns) {
-        float ra, rb;
-        turn(table[i], Eight<T>::to_f32(a), Eight<T>::to_f32(b), ra, rb);
-        Eight<T>::from_f32(a, ra);
-        Eight<T>::from_f32(b, rb);
-      }
-      T* to = dst(r);
-      if (to != nullptr) {
-        to[lo] = a;
-        to[hi] = b;
-      }
-      if ((u += step) < n) load();
-    }
+    if ((u += step) < n) load();
   }
 }
 
 }  // namespace detail
 
-// A token to blockIdx.x, of whose heads blockIdx.y takes its part.
-template <typename T, bool INTERLEAVED, bool VEC>
+// A token to blockIdx.x, of whose heads blockIdx.y takes its part.  N: the longest
+// run, of 8, 4, 2 or 1, that pairs of halves come apart into; 8 where neighbours
+// are pairs.  Measured on GB300: 1264 tokens of 36 heads of 64, of which 16, 24, 20 and
+// 6 elements turn (runs of 8, 4, 2, 1), 5.2, 6.1, 8.1 and 10.7 us.
+template <typename T, bool INTERLEAVED, int N>
 __global__ void __launch_bounds__(kRotaryThreads)
 gqa_rotary_kernel(const RotaryParams p) {
-  __shared__ float2 table[kMaxPairs];
+  __shared__ alignas(16) float2 table[kMaxPairs];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long token = blockIdx.x;
@@ -212,22 +221,23 @@ gqa_rotary_kernel(const RotaryParams p) {
   const uint64_t turns = tid < p.pairs ? p.turns[tid] : 0;
   const T* src = static_cast<const T*>(p.x.src) + token * p.x.src_stride;
   T* dst = static_cast<T*>(p.x.dst) + token * p.x.dst_stride;
-  detail::turn_heads<T, INTERLEAVED, VEC>(
-      p.x.heads, p.head_dim, p.pairs, table, static_cast<int>(blockIdx.y), static_cast<int>(gridDim.y),
+  detail::turn_heads<T, INTERLEAVED, N>(
+      p.x.heads, p.head_dim, p.pairs, table,
       [&](int r) { return src + static_cast<long long>(r) * p.head_dim; },
       [&](int r) { return dst + static_cast<long long>(r) * p.head_dim; }, [](int) { return true; },
       [&] {
-        if (tid < p.pairs) table[tid] = detail::turn_of(turns, position, p.inverse, p.magnitude);
+        for (int i = tid; i < p.pairs; i += static_cast<int>(blockDim.x))
+          table[i] = detail::turn_of(i == tid ? turns : p.turns[i], position, p.inverse, p.magnitude);
         __syncthreads();
       });
 }
 
 // The same for a batch's new tokens: queries into x.dst, keys and values into
 // the page that holds the token's place.
-template <typename T, bool INTERLEAVED, bool VEC>
+template <typename T, bool INTERLEAVED, int N>
 __global__ void __launch_bounds__(kRotaryThreads)
 gqa_append_kernel(const RotaryParams p) {
-  __shared__ float2 table[kMaxPairs];
+  __shared__ alignas(16) float2 table[kMaxPairs];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long token = blockIdx.x;
@@ -241,30 +251,36 @@ gqa_append_kernel(const RotaryParams p) {
   if (t >= n) return;
   const int place = L - n + t;
   const int position = p.positions != nullptr ? p.positions[token] : place;
-  const int page = detail::page_of(p.pages, p.err_word, b, place);
-  const bool there = page < p.pages.num_pages;
-  const long long at = page * p.page_stride + (place & p.pages.page_mask) * p.pos_stride;
+  const int page = p.pages.table[static_cast<long long>(b) * p.pages.cols + (place >> p.pages.page_shift)];
   const T* q = static_cast<const T*>(p.x.src) + token * p.x.src_stride;
   const T* k = static_cast<const T*>(p.k.src) + token * p.k.src_stride;
   const T* v = static_cast<const T*>(p.v.src) + token * p.v.src_stride;
   T* q_out = static_cast<T*>(p.x.dst) + token * p.x.dst_stride;
-  T* k_to = static_cast<T*>(p.k_cache) + at;
-  T* v_to = static_cast<T*>(p.v_cache) + at;
+  // (where they go is not known before the page is: the first loads need not wait for it)
+  T *k_to = nullptr, *v_to = nullptr;
   const int hq = p.x.heads, hk = p.k.heads;
-  detail::turn_heads<T, INTERLEAVED, VEC>(
-      hq + 2 * hk, p.head_dim, p.pairs, table, static_cast<int>(blockIdx.y), static_cast<int>(gridDim.y),
+  detail::turn_heads<T, INTERLEAVED, N>(
+      hq + 2 * hk, p.head_dim, p.pairs, table,
       [&](int r) {
         const long long d = p.head_dim;
         return r < hq ? q + r * d : r < hq + hk ? k + (r - hq) * d : v + (r - hq - hk) * d;
       },
       [&](int r) -> T* {
         if (r < hq) return q_out + static_cast<long long>(r) * p.head_dim;
-        if (!there) return nullptr;
+        if (k_to == nullptr) return nullptr;
         return r < hq + hk ? k_to + (r - hq) * p.head_stride : v_to + (r - hq - hk) * p.head_stride;
       },
       [&](int r) { return r < hq + hk && p.pairs > 0; },
       [&] {
-        if (tid < p.pairs) table[tid] = detail::turn_of(turns, position, 0, p.magnitude);
+        for (int i = tid; i < p.pairs; i += static_cast<int>(blockDim.x))
+          table[i] = detail::turn_of(i == tid ? turns : p.turns[i], position, 0, p.magnitude);
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.pages.num_pages)) {
+          const long long at = page * p.page_stride + (place & p.pages.page_mask) * p.pos_stride;
+          k_to = static_cast<T*>(p.k_cache) + at;
+          v_to = static_cast<T*>(p.v_cache) + at;
+        } else if (tid == 0) {
+          atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
+        }
         __syncthreads();
       });
 }
