@@ -203,6 +203,13 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int NT = Cfg::kTiles, KCH = Cfg::kChunks, TCH = Cfg::kTileChunks, TPB = Cfg::kTilesPerBlock;
   constexpr uint32_t NSK = Cfg::kStagesK, NSV = Cfg::kStagesV;
   constexpr int NQ = Cfg::kQSlots;
+  // head_dim 64 over pages: O takes a quarter of TMEM, so that there is room for a
+  // third S slot.  Steps take the slots in turn, and two QKs run ahead of the PV at
+  // hand, where a tile with one slot waits for its PV and its next QK after every
+  // block (16 sequences of 32768 keys, 32 / 8 heads, 26 tokens: XXX us, 268 so).
+  constexpr bool THREE = PAGED && HEAD_DIM == 64;
+  constexpr uint32_t OCOL = THREE ? 3 * kBlockN : Cfg::kOCol;
+  static_assert(OCOL + NT * HEAD_DIM <= Cfg::kTmemCols, "TMEM column plan");
   constexpr bool HALVES = TPB == 1;  // P is handed over in two halves
   constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1, kPlanWarp = kProducerWarp + 2;
 
@@ -226,9 +233,14 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // block's parity.  A parity wait is sound only while the phase before the
   // awaited one is known to be complete; with one tile, QK(g) is issued ahead
   // of PV(g-1), so S(g) complete says that PV(g-2) has landed, no later one.
+  // (THREE: they are a tile's, three of each in turn, so that its warps, which may
+  // leave an item at once, only have their own steps to count.  A tile alone has QKs
+  // of two steps complete before its warps look at the first: with two barriers in
+  // turn, the third would complete the first's next phase under their eyes.)
+  constexpr int SETS = THREE ? 6 : 2;
   constexpr int K_FULL = 0, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK, V_EMPTY = V_FULL + NSV,
-                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, P_HALF = S_FULL + 2,
-                P_FULL = P_HALF + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 2, ITEM_FULL = DRAIN + 1,
+                Q_FULL = V_EMPTY + NSV, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, P_HALF = S_FULL + SETS,
+                P_FULL = P_HALF + SETS, O_FULL = P_FULL + SETS, DRAIN = O_FULL + SETS, ITEM_FULL = DRAIN + 1,
                 ITEM_EMPTY = ITEM_FULL + kItemRing, N_BARRIERS = ITEM_EMPTY + kItemRing;
   static_assert(N_BARRIERS <= 64, "barrier words");
 
@@ -243,7 +255,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   if (warp == 0) {
     for (int i = lane; i < N_BARRIERS; i += 32) {
       uint32_t arrivals = 1;
-      if (i >= P_HALF && i < P_FULL + 2) arrivals = 4;         // the softmax warps of a tile
+      if (i >= P_HALF && i < O_FULL) arrivals = 4;             // the softmax warps of a tile
       if (i >= ITEM_EMPTY) arrivals = Cfg::kSoftmaxWarps + 2;  // softmax warps, producer, issuer
       ptx::mbar_init(BAR(i), arrivals);
     }
@@ -424,7 +436,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       bool ok = true;
       uint32_t u = 0;            // K/V blocks
       uint32_t uq = 0;           // Q slots
-      uint32_t g[2] = {0u, 0u};  // value MMAs of each S slot
+      uint32_t g[2] = {0u, 0u};  // value MMAs of each S slot (THREE: of each tile)
+      uint32_t us = 0;           // THREE: steps
       auto wait = [&](int i, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns));
       };
@@ -447,19 +460,31 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         // (16-byte units)  Shifted rows are at `shift` in their Q slot: the second tile reads it from its start,
         // the first one from there on, each with rows of other data beside its own.
         const uint32_t q_shift = __shfl_sync(0xffffffffu, static_cast<uint32_t>(section(it.section).shift), 0) * 8;
+        auto tile_of = [&](int j) -> uint32_t {
+          return NT == 1 || ahead == 1 ? 0u : static_cast<uint32_t>(j) & 1u;
+        };
         auto slot_of = [&](int j) -> uint32_t {
-          return NT == 1 ? (u + static_cast<uint32_t>(j)) & 1u : (ahead == 2 ? static_cast<uint32_t>(j) & 1u : 0u);
+          return NT == 1 ? (u + static_cast<uint32_t>(j)) & 1u
+                 : THREE ? (us + static_cast<uint32_t>(j)) % 3u
+                         : tile_of(j);
+        };
+        // the S and P barriers of step j, and (THREE) which of its tile's steps it is
+        auto count_of = [&](int j) -> uint32_t {
+          return g[tile_of(j)] + static_cast<uint32_t>(ahead == 2 ? j >> 1 : j);
+        };
+        auto set_of = [&](int j) -> int {
+          return static_cast<int>(THREE ? 3u * tile_of(j) + count_of(j) % 3u : slot_of(j));
         };
         auto block_of = [&](int j) -> uint32_t { return u + static_cast<uint32_t>(two ? j >> 1 : j); };
         auto qk = [&](int j) {
-          const uint32_t slot = slot_of(j), blk = block_of(j), qs = (uq + (two ? slot : 0u)) % NQ;
+          const uint32_t slot = slot_of(j), tile = tile_of(j), blk = block_of(j), qs = (uq + (two ? tile : 0u)) % NQ;
 #pragma unroll
           for (int hf = 0; hf < TPB; ++hf) {
             const uint32_t m = blk * TPB + hf, stage = m % NSK;
-            if (!two || slot == 0u) wait(K_FULL + static_cast<int>(stage), m / NSK);
+            if (!two || tile == 0u) wait(K_FULL + static_cast<int>(stage), m / NSK);
             if (!ok) return;
             ptx::tc_fence_after();
-            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4) + (slot == 0u ? q_shift : 0u);
+            const uint32_t qd = q_lo + ((qs * Cfg::kQTileBytes) >> 4) + (tile == 0u ? q_shift : 0u);
             const uint32_t kd = k_lo + ((stage * Cfg::kStageBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < Cfg::kTileDim / 16; ++kk) {
@@ -468,8 +493,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
                                     kd + (kk >> 2) * 1024 + (kk & 3) * 2, k_hi, idesc_qk, k > 0 ? 1u : 0u);
             }
           }
-          ptx::mma_commit_elect(leader, BAR(S_FULL + static_cast<int>(slot)));
-          if (!two || slot == 1u) {  // the block's last use
+          ptx::mma_commit_elect(leader, BAR(S_FULL + set_of(j)));
+          if (!two || tile == 1u) {  // the block's last use
 #pragma unroll
             for (int hf = 0; hf < TPB; ++hf)
               ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>((blk * TPB + hf) % NSK)));
@@ -478,19 +503,21 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             for (int t = 0; t < nt; ++t) ptx::mma_commit_elect(leader, BAR(Q_EMPTY + static_cast<int>((uq + t) % NQ)));
         };
         auto pv = [&](int j) {
-          const uint32_t slot = slot_of(j), blk = block_of(j);
-          const uint32_t o_tmem = tmem_base + Cfg::kOCol + (NT == 1 ? 0u : slot * HEAD_DIM);
+          const uint32_t slot = slot_of(j), tile = tile_of(j), blk = block_of(j);
+          const int set = set_of(j);
+          const uint32_t p_phase = THREE ? count_of(j) / 3u : g[slot];
+          const uint32_t o_tmem = tmem_base + OCOL + tile * HEAD_DIM;
           constexpr int KK = kBlockN / 16, PARTS = HALVES ? 2 : 1;
           const bool first = j < (NT == 1 ? 1 : ahead);
           // (V first: it has most often arrived, and P is the one waited for)
-          if (TPB == 1 && (!two || slot == 0u)) wait(V_FULL + static_cast<int>(blk % NSV), blk / NSV);
+          if (TPB == 1 && (!two || tile == 0u)) wait(V_FULL + static_cast<int>(blk % NSV), blk / NSV);
           // P comes in two halves, so that the first one's MMAs run under the
           // last exponentials: 4 x 2048 tokens of 32 heads against 8192 keys
           // 766 us and not 797, a batch behind 32768 keys 194 and not 199
           // (thirds at 1/2 and 3/4: 812, 205).  One tile waits for V, not P.
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
-            wait((part + 1 < PARTS ? P_HALF : P_FULL) + static_cast<int>(slot), g[slot]);
+            wait((part + 1 < PARTS ? P_HALF : P_FULL) + set, p_phase);
 #pragma unroll
             for (int hf = 0; hf < TPB; ++hf) {
               const uint32_t m = blk * TPB + hf, stage = m % NSV;
@@ -504,23 +531,28 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
                                       vd + kk * (2048 >> 4), v_hi, idesc_pv, (kk > 0 || !first) ? 1u : 0u);
             }
           }
-          ++g[slot];
-          ptx::mma_commit_elect(leader, BAR(O_FULL + static_cast<int>(slot)));
-          if (!two || slot == 1u) {
+          if constexpr (!THREE) ++g[slot];
+          ptx::mma_commit_elect(leader, BAR(O_FULL + set));
+          if (!two || tile == 1u) {
 #pragma unroll
             for (int hf = 0; hf < TPB; ++hf)
               ptx::mma_commit_elect(leader, BAR(V_EMPTY + static_cast<int>((blk * TPB + hf) % NSV)));
           }
         };
 #pragma unroll 1
-        for (int j = -ahead; j < steps && ok; ++j) {
-          if constexpr (NT == 1) {
-            if (j + 1 < steps) qk(j + 1);
+        for (int j = THREE ? -2 : -ahead; j < steps && ok; ++j) {
+          if constexpr (NT == 1 || THREE) {
+            if (j + (THREE ? 2 : 1) < steps) qk(j + (THREE ? 2 : 1));
             if (j >= 0 && ok) pv(j);
           } else {
             if (j >= 0) pv(j);
             if (ok && j + ahead < steps) qk(j + ahead);
           }
+        }
+        if constexpr (THREE) {
+          g[0] = count_of(ahead == 2 ? 2 * ((steps + 1) / 2) : steps);
+          if (ahead == 2) g[1] = count_of(2 * (steps / 2) + 1);
+          us += static_cast<uint32_t>(steps);
         }
         u += static_cast<uint32_t>(n);
         uq += static_cast<uint32_t>(nt);
@@ -639,10 +671,11 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     const int t = warp >> 2;                        // this warp's row tile
     const int r = (warp & 3) * 32 + lane;           // its TMEM lane: a row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_addr = tmem_base + lanes + Cfg::kOCol + static_cast<uint32_t>(t * HEAD_DIM);
+    const uint32_t o_addr = tmem_base + lanes + OCOL + static_cast<uint32_t>(t * HEAD_DIM);
     const uint64_t scale2 = ptx::pack_f32x2(p.scale_log2, p.scale_log2);
     uint32_t g = 0;  // blocks of this tile
     uint32_t u = 0;  // K/V blocks of the items before
+    uint32_t us = 0; // THREE: and their steps
     bool ok = true;
     auto pack16 = [](float lo, float hi) -> uint32_t {
       if constexpr (IN_F16) {
@@ -659,6 +692,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     };
 
     auto wait_pv = [&](uint32_t blk_g) {  // the value MMA of this tile's block blk_g has landed
+      if (THREE) return wait(O_FULL + 3 * t + static_cast<int>(blk_g % 3u), blk_g / 3u);
       return NT == 2 ? wait(O_FULL + t, blk_g) : wait(O_FULL + static_cast<int>(blk_g & 1u), blk_g >> 1);
     };
 
@@ -669,6 +703,9 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       u += static_cast<uint32_t>(n_blk);
       const bool split_keys = NT == 2 && section(it.section).split_keys != 0;
       const bool idle = !split_keys && t >= slots_of(it);
+      const bool two = THREE && !split_keys && slots_of(it) == 2;
+      const uint32_t us0 = us;
+      if constexpr (THREE) us += static_cast<uint32_t>(two ? 2 * n_blk : n_blk);
       // (PAGED: an idle tile may still hold rows of tokens that the entry lacks)
       if (idle && (!PAGED || it.tok0 + t * section(it.section).tokens >= section(it.section).nq)) continue;
       const int rows = section(it.section).tokens * p.G;   // of a tile
@@ -688,7 +725,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       float nm = kNoMax, l = 0.f;  // -max (log2 units; kNoMax while it is -inf) and the sum of this row
       for (int i = i0; i < n_blk; i += step, ++g) {
         const int blk = it.block(i);
-        const uint32_t slot = NT == 2 ? static_cast<uint32_t>(t) : (g & 1u);
+        const uint32_t slot = THREE     ? (us0 + static_cast<uint32_t>(two ? 2 * i + t : i)) % 3u
+                              : NT == 2 ? static_cast<uint32_t>(t)
+                                        : (g & 1u);
+        const int set = static_cast<int>(THREE ? 3u * static_cast<uint32_t>(t) + g % 3u : slot);
         const uint32_t s_addr = tmem_base + lanes + slot * kBlockN;
         const bool first = i == i0;
         // PAGED: the words that hold the bits of this block's keys, fetched while its scores are computed
@@ -696,7 +736,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         uint32_t branch[5];
         if (hides)
           detail::branch_words(branch, p.pages, it.b, section(it.section).nq, dead ? 0 : tok_row, blk * kBlockN - drafts);
-        if (!wait(S_FULL + static_cast<int>(slot), NT == 2 ? g : g >> 1)) break;
+        if (!wait(S_FULL + set, THREE ? g / 3u : NT == 2 ? g : g >> 1)) break;
         const int tail = it.L - blk * kBlockN;  // keys of this block
         if (tail < kBlockN) {
           // V rows past the end hold whatever the buffer holds there; zero
@@ -731,8 +771,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         }
         if (!active) {  // no row of this warp is read: whatever its lanes hold may stand for P
           __syncwarp();
-          if (HALVES && lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
-          if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + static_cast<int>(slot)));
+          if (HALVES && lane == 0) ptx::mbar_arrive(BAR(P_HALF + set));
+          if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + set));
           continue;
         }
         ptx::tc_fence_after();
@@ -824,7 +864,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(BAR(P_HALF + static_cast<int>(slot)));
+            if (lane == 0) ptx::mbar_arrive(BAR(P_HALF + set));
           }
           if (c > 0) put_p(c - 1);  // under the next exponentials, whose unit then does not wait for it
         }
@@ -832,7 +872,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + static_cast<int>(slot)));
+        if (lane == 0) ptx::mbar_arrive(BAR(P_FULL + set));
 
         // the sum, from the unrounded p, under the value MMA
         uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
