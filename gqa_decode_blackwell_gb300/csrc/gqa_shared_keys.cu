@@ -168,7 +168,7 @@ RowsWs rows_ws(const RowsLaunch& r) {
 
 bool encode_heads_map(CUtensorMap* m, int in_dtype, const void* base, int head_dim, int heads, int positions,
                       int outer, int64_t head_stride, int64_t pos_stride, int64_t outer_stride, int box_heads,
-                      int box_positions) {
+                      int box_positions, CUtensorMapL2promotion l2) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
   const CUtensorMapDataType type =
@@ -180,7 +180,7 @@ bool encode_heads_map(CUtensorMap* m, int in_dtype, const void* base, int head_d
                                  2 * static_cast<cuuint64_t>(outer_stride)};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_positions), 1};
   return enc(m, type, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_SWIZZLE_128B, l2,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -220,8 +220,12 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
       bool ok;
       if (paged != nullptr) {
         const gqa_pages_t& g = *paged->geometry;
+        // A head's row of 64 elements is 128 bytes, and twice as many would bring
+        // another head's, which may be gone before it is asked for (16 sequences of
+        // 32768 keys of 8 heads of 64: 248 us with 256-byte fetches, 207 with these).
         ok = encode_heads_map(maps[m], d.in_dtype, bases[m], d.head_dim, d.kv_heads, g.page_size, g.num_pages,
-                              g.head_stride, g.pos_stride, g.page_stride, 1, 1 << paged->keys.box_shift);
+                              g.head_stride, g.pos_stride, g.page_stride, 1, 1 << paged->keys.box_shift,
+                              d.head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
       } else {
         ok = dense(maps[m], bases[m], d.kv_heads, d.max_seqlen, 1, kBlockN);
       }

@@ -52,7 +52,7 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
 // [outer, positions, heads, d] with the given strides (in elements).
 bool encode_heads_map(CUtensorMap* m, int in_dtype, const void* base, int head_dim, int heads, int positions,
                       int outer, int64_t head_stride, int64_t pos_stride, int64_t outer_stride, int box_heads,
-                      int box_positions);
+                      int box_positions, CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 gqa_status_t launch_kernel(const void* fn, dim3 grid, int threads, int smem, void* params, cudaStream_t s);
 bool output_ok(const void* out, const float* lse);

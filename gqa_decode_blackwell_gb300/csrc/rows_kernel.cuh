@@ -206,11 +206,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // head_dim 64 over pages: O takes a quarter of TMEM, so that there is room for a
   // third S slot.  Steps take the slots in turn, and two QKs run ahead of the PV at
   // hand, where a tile with one slot waits for its PV and its next QK after every
-  // block (16 sequences of 32768 keys, 32 / 8 heads, 26 tokens: XXX us, 268 so).
+  // block (16 sequences of 32768 keys, 32 / 8 heads, us a call with three slots and
+  // two: 64 tokens 305 and 334, 26 tokens, whose keys are split, 222 and 223).
   constexpr bool THREE = PAGED && HEAD_DIM == 64;
   constexpr uint32_t OCOL = THREE ? 3 * kBlockN : Cfg::kOCol;
   static_assert(OCOL + NT * HEAD_DIM <= Cfg::kTmemCols, "TMEM column plan");
-  constexpr bool HALVES = TPB == 1;  // P is handed over in two halves
+  constexpr bool HALVES = TPB == 1 && !THREE;  // P is handed over in two halves
   constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1, kPlanWarp = kProducerWarp + 2;
 
   extern __shared__ uint8_t smem_raw[];
@@ -436,8 +437,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       bool ok = true;
       uint32_t u = 0;            // K/V blocks
       uint32_t uq = 0;           // Q slots
-      uint32_t g[2] = {0u, 0u};  // value MMAs of each S slot (THREE: of each tile)
-      uint32_t us = 0;           // THREE: steps
+      uint32_t g[2] = {0u, 0u};  // value MMAs of each S slot
+      uint32_t us = 0, g0 = 0, g1 = 0;  // THREE: steps, and those of each tile
       auto wait = [&](int i, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(BAR(i), parity & 1u, abort_flag, p.timeout_ns));
       };
@@ -470,7 +471,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         };
         // the S and P barriers of step j, and (THREE) which of its tile's steps it is
         auto count_of = [&](int j) -> uint32_t {
-          return g[tile_of(j)] + static_cast<uint32_t>(ahead == 2 ? j >> 1 : j);
+          return (tile_of(j) != 0u ? g1 : g0) + static_cast<uint32_t>(ahead == 2 ? j >> 1 : j);
         };
         auto set_of = [&](int j) -> int {
           return static_cast<int>(THREE ? 3u * tile_of(j) + count_of(j) % 3u : slot_of(j));
@@ -550,8 +551,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           }
         }
         if constexpr (THREE) {
-          g[0] = count_of(ahead == 2 ? 2 * ((steps + 1) / 2) : steps);
-          if (ahead == 2) g[1] = count_of(2 * (steps / 2) + 1);
+          g0 += static_cast<uint32_t>(ahead == 2 ? (steps + 1) / 2 : steps);
+          g1 += static_cast<uint32_t>(ahead == 2 ? steps / 2 : 0);
           us += static_cast<uint32_t>(steps);
         }
         u += static_cast<uint32_t>(n);

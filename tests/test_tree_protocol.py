@@ -24,7 +24,7 @@ class Paged(Cta):
         self.o_turn = 1 if mistake == "one barrier for O" else self.turn
         self.q_full, self.q_empty = [Bar() for _ in range(self.nq)], [Bar() for _ in range(self.nq)]
         self.stage["Q"] = [dict(holds=None, loading=False, readers=0, zeroed=True) for _ in range(self.nq)]
-        self.halves = form.shape.tpb == 1
+        self.halves = form.shape.tpb == 1 and not form.three
         if self.three:
             n = self.turn * self.nt
             self.s_full, self.o_full = [Bar() for _ in range(n)], [Bar() for _ in range(self.o_turn * self.nt)]
