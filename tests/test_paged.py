@@ -208,6 +208,12 @@ def test_header_is_plain_c_and_exported(tmp_path):
                    check=True)
 
 
+def test_status_of_an_index_out_of_range():
+    assert g.GQA_ERR_BAD_INDEX == 8
+    assert "out of range" in g.gqa_status_string(g.GQA_ERR_BAD_INDEX)
+    assert g.gqa_status_string(g.GQA_ERR_BAD_INDEX) != g.gqa_status_string(g.GQA_ERR_BAD_SEQLEN)
+
+
 def test_python_checks_tensors():
     """Refused before anything reaches the library (these are CPU tensors, the last of whose faults that is)."""
     k = torch.zeros(2, 5, 2, 64, dtype=BF16)
@@ -624,6 +630,11 @@ TREE = [  # lens, news, T, H, K, d, page, dtype, out dtype, heads first
     ([700, 650], [3, 2], 3, 100, 1, 128, 1024, FP16, None, False),                           # G = 100: a token a tile
     ([300] * 40 + [0] * 60, [9] * 40 + [0] * 60, 9, 12, 12, 64, 16, BF16, None, False),      # a padded batch
     ([(i * 29) % 300 for i in range(300)], None, 30, 8, 2, 64, 16, BF16, None, False),       # fewer positions than tokens
+    ([3000, 2000, 1, 700], [70, 33, 1, 0], 70, 8, 2, 64, 32, BF16, None, False),             # a group of two tiles, then one alone
+    ([5000, 130], None, 50, 16, 2, 64, 16, FP16, None, False),                               # the same, cut many times
+    ([(i * 97) % 700 for i in range(200)], [i % 10 for i in range(200)], 9, 32, 8, 128, 16, BF16, None, False),  # more
+    ([(i * 97) % 300 for i in range(140)], None, 40, 8, 2, 128, 32, FP16, None, False),      # entries than one warp stages
+    ([(i * 97) % 400 for i in range(150)], [i % 20 for i in range(150)], 19, 8, 1, 256, 16, BF16, None, False),
     ([(i * 29) % 150 for i in range(4100)], None, 20, 2, 2, 64, 16, BF16, None, False),      # more entries than are staged
     ([(i * 29) % 150 for i in range(4100)], [(i * 7) % 70 for i in range(4100)], 70, 4, 1, 64, 32, FP16, None, False),
 ]
@@ -980,6 +991,39 @@ def test_graph_of_a_step_follows_its_inputs(dev):
     torch.cuda.synchronize()
     s.check()
     assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
+def test_capacity_far_beyond_the_lengths(dev):
+    """A table for 2^24 positions of each sequence, of which they have a few thousand."""
+    for T in (1, 20):
+        c = Case(dev, [3000, 40, 0, 777], None, T, 16, 4, 128, 16, seed=96)
+        wide = torch.full((4, 1 << 20), -1, dtype=torch.int32, device=dev)
+        wide[:, : c.table.shape[1]] = c.table
+        c.table = wide
+        out, lse = c.run(causal=True)
+        _compare("capacity", out, lse, c.want(lambda b: torch.ones(c.n[b], c.n[b]).tril().bool()))
+    assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
+def test_steps_back_to_back_without_waiting(dev):
+    """Twenty steps in a row on one cache, each reading what the one before has just written: the results of the
+    same steps with the GPU waited for after every call."""
+    def many(wait):
+        s = Step(dev, *STEPS[1], seed=97)
+        outs = []
+        for i in range(20):
+            s.qkv.copy_(_randn(dev, *s.qkv.shape, seed=200 + i))
+            s.run()
+            if wait:
+                torch.cuda.synchronize()
+            outs.append((s.out.clone(), s.lse.clone(), s.c.k.clone()))
+        torch.cuda.synchronize()
+        return outs
+
+    for a, b in zip(many(True), many(False)):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 @gpu
