@@ -568,7 +568,9 @@ class _Handles:
 
         self.int32, self.int64, self.fp32 = torch.int32, torch.int64, torch.float32
         self.current_stream, self.current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        self.lib = lib()
+        self.lib = L = lib()
+        self.rotary_apply, self.paged_append, self.paged_keep = L.gqa_rotary_apply, L.gqa_paged_append, L.gqa_paged_keep
+        self.tree_from_parents, self.tree_attn = L.gqa_tree_from_parents, L.gqa_tree_attn
 
 
 _handles = None
@@ -581,13 +583,12 @@ def _hot() -> _Handles:
     return _handles
 
 
-def _call(h, name, device, stream, *args):
-    """The C function `name` on `device`, in `stream`, the last of its arguments."""
+def _call(h, fn, device, stream, *args):
+    """The C function `fn` on `device`, in `stream`, the last of its arguments."""
     raw = h.current_stream(device) if stream is None else _raw_stream(stream, device)
-    fn = getattr(h.lib, name)
     rc = fn(*args, raw) if h.current_device() == device else _on_device(device, fn, *args, raw)
-    if rc != GQA_OK:
-        raise GQAError(rc, name)
+    if rc:
+        raise GQAError(rc, fn.__name__)
 
 
 def _need(t, what, device, dtype=None, shape=None):
@@ -603,6 +604,7 @@ def _need(t, what, device, dtype=None, shape=None):
 
 
 def _ints(t, device, int32, shape) -> bool:
+    """Whether t, if there is one, is a contiguous tensor on `device` of this type and shape."""
     return t is None or (t.dtype is int32 and t.shape == shape and t.get_device() == device and t.is_contiguous())
 
 
@@ -693,8 +695,9 @@ def gqa_rotary_apply(x, positions, turns, out, *, interleaved: bool = False, inv
         raise ValueError("x must be [..., heads, d], and out of its type and shape and on its device")
     if not _ints(positions, device, h.int32, shape[:-2]) or positions is None:
         raise ValueError(f"positions must be contiguous int32 {tuple(shape[:-2])} on x's device")
-    _need(turns, "turns (of rotary_turns)", device, h.int64)
-    _call(h, "gqa_rotary_apply", device, stream, _rope(turns.numel(), interleaved, inverse, magnitude),
+    if not _ints(turns, device, h.int64, turns.shape):
+        _need(turns, "turns (of rotary_turns)", device, h.int64)
+    _call(h, h.rotary_apply, device, stream, _rope(turns.numel(), interleaved, inverse, magnitude),
           turns.data_ptr(), positions.data_ptr(), positions.numel(), shape[-2], shape[-1], code, x.data_ptr(),
           _strides_of_tokens(shape, x.stride(), "x"), out.data_ptr(),
           _strides_of_tokens(shape, out.stride(), "out"))
@@ -732,8 +735,10 @@ def gqa_paged_append(q, k, v, q_out, k_cache, v_cache, page_table, seqlens, *, n
         raise ValueError(f"k {tuple(shape)} and cache {tuple(k_cache.shape)} disagree")
     if not _caches_agree(k_cache, v_cache, page_table, device, dtype, h.int32):
         _refuse_caches(k_cache, v_cache, page_table, device, dtype)
-    if seqlens is None or not (_ints(seqlens, device, h.int32, batch) and _ints(new_lens, device, h.int32, batch)
-                               and _ints(positions, device, h.int32, tokens)):
+    int32 = h.int32
+    if not (seqlens is not None and _ints(seqlens, device, int32, batch)
+            and (new_lens is None or _ints(new_lens, device, int32, batch))
+            and (positions is None or _ints(positions, device, int32, tokens))):
         raise ValueError("seqlens and new_lens must be int32 [B], positions int32 [B, nq], contiguous on k's device")
     q_at, q_stride, out_at = None, 0, None
     if q is not None:
@@ -744,9 +749,10 @@ def gqa_paged_append(q, k, v, q_out, k_cache, v_cache, page_table, seqlens, *, n
         q_at, q_stride, out_at = q.data_ptr(), _strides_of_tokens(q.shape, q.stride(), "q"), q_out.data_ptr()
     rope = table = None
     if turns is not None:
-        _need(turns, "turns (of rotary_turns)", device, h.int64)
-        rope, table = _rope(turns.numel(), interleaved, False, magnitude), turns.data_ptr()
-    _call(h, "gqa_paged_append", device, stream, desc, geometry, rope, table, _ptr(positions), q_at, q_stride,
+        if not _ints(turns, device, h.int64, turns.shape):
+            _need(turns, "turns (of rotary_turns)", device, h.int64)
+        rope, table = _rope(turns.shape[0], interleaved, False, magnitude), turns.data_ptr()
+    _call(h, h.paged_append, device, stream, desc, geometry, rope, table, _ptr(positions), q_at, q_stride,
           k.data_ptr(), _strides_of_tokens(shape, k.stride(), "k"), v.data_ptr(),
           _strides_of_tokens(shape, v.stride(), "v"), out_at, k_cache.data_ptr(), v_cache.data_ptr(),
           page_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens))
@@ -766,7 +772,7 @@ def gqa_tree_from_parents(parents, seqlens, tree, positions=None, *, new_lens=No
                           (tree, "tree", (B, nq, (nq + 31) // 32)), (positions, "positions", shape)):
         if not _ints(t, device, h.int32, size):
             _need(t, what, device, h.int32, size)
-    _call(h, "gqa_tree_from_parents", device, stream, B, nq, int(max_seqlen), parents.data_ptr(), seqlens.data_ptr(),
+    _call(h, h.tree_from_parents, device, stream, B, nq, int(max_seqlen), parents.data_ptr(), seqlens.data_ptr(),
           _ptr(new_lens), tree.data_ptr(), _ptr(positions))
 
 
@@ -792,8 +798,10 @@ def gqa_tree_attn(q, k_cache, v_cache, page_table, seqlens, out, lse=None, works
                                                          page_table.shape, out.dtype, scale, causal)
     if not _caches_agree(k_cache, v_cache, page_table, device, dtype, h.int32):
         _refuse_caches(k_cache, v_cache, page_table, device, dtype)
-    if seqlens is None or not (_ints(seqlens, device, h.int32, batch) and _ints(new_lens, device, h.int32, batch)
-                               and _ints(tree, device, h.int32, bits)):
+    int32 = h.int32
+    if not (seqlens is not None and _ints(seqlens, device, int32, batch)
+            and (new_lens is None or _ints(new_lens, device, int32, batch))
+            and (tree is None or _ints(tree, device, int32, bits))):
         raise ValueError("seqlens and new_lens must be int32 [B], tree int32 [B, nq, ceil(nq / 32)], contiguous on q's "
                          "device")
     if not (q.is_contiguous() and out.shape == shape and out.is_contiguous() and out.get_device() == device):
@@ -806,7 +814,7 @@ def gqa_tree_attn(q, k_cache, v_cache, page_table, seqlens, out, lse=None, works
         if not workspace.is_contiguous() or workspace.get_device() != device:
             raise ValueError("workspace must be contiguous and on q's device")
         ws, ws_bytes = workspace.data_ptr(), _bytes_of(workspace)
-    _call(h, "gqa_tree_attn", device, stream, desc, geometry, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call(h, h.tree_attn, device, stream, desc, geometry, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           page_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), _ptr(tree), out.data_ptr(), _ptr(lse), ws,
           ws_bytes)
 
@@ -839,6 +847,6 @@ def gqa_paged_keep(k_cache, v_cache, page_table, seqlens, path, keep_lens, seqle
                           (keep_lens, "keep_lens", batch), (seqlens_out, "seqlens_out", batch)):
         if not _ints(t, device, h.int32, size):
             _need(t, what, device, h.int32, size)
-    _call(h, "gqa_paged_keep", device, stream, desc, geometry, k_cache.data_ptr(), v_cache.data_ptr(),
+    _call(h, h.paged_keep, device, stream, desc, geometry, k_cache.data_ptr(), v_cache.data_ptr(),
           page_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), path.data_ptr(), shape[1], keep_lens.data_ptr(),
           _ptr(seqlens_out))
