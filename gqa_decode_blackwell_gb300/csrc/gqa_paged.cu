@@ -89,16 +89,16 @@ const void* rotary_fn(bool interleaved, int run) {
 
 // Few tokens are spread over CTAs of a unit (two runs) a thread, up to a GPU full
 // of them; of many each has one CTA, which computes the token's angles once, of
-// 128 threads up to 512 units and 256 beyond.  Measured on GB300 (128, 256): 8192
-// places of 384 units 19.4 and 22.4 us, 8192 of 256 21.3 and 21.6, 2048 of 1280 21.8
-// and 16.6, 2048 of 512 in fp32 26.3 and 25.4.
+// 256 threads where they have two units or more each or all of them one, and else of
+// 128.  Measured on GB300 (128, 256): 8192 places of 384 units 18.5 and 20.4 us, 8192
+// of 256 21.1 and 21.0, 2048 of 1280 20.2 and 16.5, 2048 of 512 in fp32 25.5 and 24.2.
 gqa_status_t launch_rotary(const void* fn, RotaryParams& p, long long tokens, int rows, int run, int sm,
                            cudaStream_t s) {
   const long long units = static_cast<long long>(rows) * (p.head_dim / (2 * run));
   long long threads = 128, parts = (units + threads - 1) / threads;
   const long long spread = 16LL * sm / tokens;
   if (spread < parts) {
-    threads = units <= 512 ? 128 : kRotaryThreads;
+    threads = units > 2 * kRotaryThreads || units % kRotaryThreads == 0 ? kRotaryThreads : 128;
     parts = spread > 1 ? spread : 1;
   }
   return launch_kernel(fn, dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(parts < 65535 ? parts : 65535)),

@@ -128,9 +128,25 @@ struct Run {
   }
 };
 
-__device__ __forceinline__ void turn(float2 cs, float a, float b, float& ra, float& rb) {
-  ra = a * cs.x - b * cs.y;
-  rb = a * cs.y + b * cs.x;
+__device__ __forceinline__ void turn(float c, float s, float a, float b, float& ra, float& rb) {
+  ra = a * c - b * s;
+  rb = a * s + b * c;
+}
+
+// A token's angles in shared memory: two pairs to a word, (cos, cos, sin, sin), in
+// the order in which a unit's threads ask for them -- pairs 2 k and 2 k + 1 of all
+// units side by side, so that 8 threads read 128 bytes without a bank conflict
+// (pairs one after another: 19.4 us a prompt's append, 18.5 so).
+template <int N>
+__device__ __forceinline__ int angle_at(int i, int k, int pairs) {
+  return k * ((pairs + N - 1) / N) + i;
+}
+template <int N>
+__device__ __forceinline__ void put_angle(float4* table, int pair, int pairs, float2 cs) {
+  const int i = pair / N, e = pair - i * N;
+  float* w = reinterpret_cast<float*>(table + angle_at<N>(i, e / 2, pairs)) + e % 2;
+  w[0] = cs.x;
+  w[2] = cs.y;
 }
 
 // Where the two runs of N elements that one thread takes of a head begin, its
@@ -143,24 +159,29 @@ __device__ __forceinline__ int2 runs_of(int i, int pairs) {
 }
 
 template <typename T, bool INTERLEAVED, int N>
-__device__ __forceinline__ void turn_runs(Run<T, N>& a, Run<T, N>& b, const float2* table, int i, int pairs) {
+__device__ __forceinline__ void turn_runs(Run<T, N>& a, Run<T, N>& b, const float4* table, int i, int pairs) {
   if constexpr (INTERLEAVED) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int e = 0; e < N; e += 2) {
       Run<T, N>& v = e < N / 2 ? a : b;
       constexpr int H = N / 2;
       if (N * i + e >= pairs) continue;
+      const float4 cs = table[angle_at<N>(i, e / 2, pairs)];
       float ra, rb;
-      turn(table[N * i + e], v.get(2 * (e % H)), v.get(2 * (e % H) + 1), ra, rb);
+      turn(cs.x, cs.z, v.get(2 * (e % H)), v.get(2 * (e % H) + 1), ra, rb);
       v.set2(2 * (e % H), ra, rb);
+      if (N * i + e + 1 >= pairs) continue;
+      turn(cs.y, cs.w, v.get(2 * (e % H) + 2), v.get(2 * (e % H) + 3), ra, rb);
+      v.set2(2 * (e % H) + 2, ra, rb);
     }
   } else {
     if (N * i >= pairs) return;
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
+      const float4 cs = table[angle_at<N>(i, e / 2, pairs)];
       float ra[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 2 && e + k < N; ++k) turn(table[N * i + e + k], a.get(e + k), b.get(e + k), ra[k], rb[k]);
+      turn(cs.x, cs.z, a.get(e), b.get(e), ra[0], rb[0]);
+      if constexpr (N > 1) turn(cs.y, cs.w, a.get(e + 1), b.get(e + 1), ra[1], rb[1]);
       a.set2(e, ra[0], ra[1]);
       b.set2(e, rb[0], rb[1]);
     }
@@ -170,9 +191,9 @@ __device__ __forceinline__ void turn_runs(Run<T, N>& a, Run<T, N>& b, const floa
 // The rows of one CTA: head r of them is at src(r) and goes to dst(r) (nowhere, if
 // that is null); those with rotated(r) are rotated by the table, which `ready`
 // fills while the first loads are under way.  (The next two runs loaded ahead cost
-// registers, and so CTAs: prompts 24.0 us, 19.7 without.)
+// registers, and so CTAs: prompts 24.0 us, then 19.7 without.)
 template <typename T, bool INTERLEAVED, int N, typename Src, typename Dst, typename Rotated, typename Ready>
-__device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, const float2* table, const Src& src,
+__device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, const float4* table, const Src& src,
                                            const Dst& dst, const Rotated& rotated, const Ready& ready) {
   // units of a row: a power of two, as head_dim and N are
   const int row_shift = 31 - __clz(head_dim / (2 * N)), n = n_rows << row_shift;
@@ -208,11 +229,12 @@ __device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, 
 // A token to blockIdx.x, of whose heads blockIdx.y takes its part.  N: the longest
 // run, of 8, 4, 2 or 1, that pairs of halves come apart into; 8 where neighbours
 // are pairs.  Measured on GB300: 1264 tokens of 36 heads of 64, of which 16, 24, 20 and
-// 6 elements turn (runs of 8, 4, 2, 1), 5.2, 6.1, 8.1 and 10.7 us.
+// 6 elements turn (runs of 8, 4, 2, 1), 5.3, 6.2, 8.0 and 10.8 us.  32 registers let an
+// SM hold 2048 threads (40: 2048 tokens of 80 heads of 256 18.8 us, 16.5 so).
 template <typename T, bool INTERLEAVED, int N>
-__global__ void __launch_bounds__(kRotaryThreads)
+__global__ void __launch_bounds__(kRotaryThreads, sizeof(T) == 4 ? 6 : 8)
 gqa_rotary_kernel(const RotaryParams p) {
-  __shared__ alignas(16) float2 table[kMaxPairs];
+  __shared__ float4 table[kMaxPairs];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long token = blockIdx.x;
@@ -227,7 +249,8 @@ gqa_rotary_kernel(const RotaryParams p) {
       [&](int r) { return dst + static_cast<long long>(r) * p.head_dim; }, [](int) { return true; },
       [&] {
         for (int i = tid; i < p.pairs; i += static_cast<int>(blockDim.x))
-          table[i] = detail::turn_of(i == tid ? turns : p.turns[i], position, p.inverse, p.magnitude);
+          detail::put_angle<N>(table, i, p.pairs,
+                               detail::turn_of(i == tid ? turns : p.turns[i], position, p.inverse, p.magnitude));
         __syncthreads();
       });
 }
@@ -235,9 +258,9 @@ gqa_rotary_kernel(const RotaryParams p) {
 // The same for a batch's new tokens: queries into x.dst, keys and values into
 // the page that holds the token's place.
 template <typename T, bool INTERLEAVED, int N>
-__global__ void __launch_bounds__(kRotaryThreads)
+__global__ void __launch_bounds__(kRotaryThreads, sizeof(T) == 4 ? 6 : 8)
 gqa_append_kernel(const RotaryParams p) {
-  __shared__ alignas(16) float2 table[kMaxPairs];
+  __shared__ float4 table[kMaxPairs];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long token = blockIdx.x;
@@ -273,7 +296,8 @@ gqa_append_kernel(const RotaryParams p) {
       [&](int r) { return r < hq + hk && p.pairs > 0; },
       [&] {
         for (int i = tid; i < p.pairs; i += static_cast<int>(blockDim.x))
-          table[i] = detail::turn_of(i == tid ? turns : p.turns[i], position, 0, p.magnitude);
+          detail::put_angle<N>(table, i, p.pairs,
+                               detail::turn_of(i == tid ? turns : p.turns[i], position, 0, p.magnitude));
         if (static_cast<unsigned>(page) < static_cast<unsigned>(p.pages.num_pages)) {
           const long long at = page * p.page_stride + (place & p.pages.page_mask) * p.pos_stride;
           k_to = static_cast<T*>(p.k_cache) + at;
