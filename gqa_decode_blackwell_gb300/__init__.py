@@ -3,7 +3,8 @@
 
 Argument marshalling only: every function below turns PyTorch tensors into
 the plain pointers and sizes of the C entry point of the same name and calls
-it.  All computation happens in the sm_103a kernels of
+it (those of ``include/gqa_paged.h`` by way of ``csrc/paged_binding.cpp``).
+All computation happens in the sm_103a kernels of
 ``libgqa_decode_sm103.so``; there is no fallback.  If the library has not
 been built, the first call raises ``RuntimeError`` (build it with
 ``gqa_decode_blackwell_gb300.build.build()``).
@@ -11,13 +12,14 @@ been built, the first call raises ``RuntimeError`` (build it with
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
 from typing import Optional
 
-from .build import HEADER, LIB, PAGED_HEADER, SHARED_KEYS_HEADER
+from .build import HEADER, LIB, PAGED_HEADER, SHARED_KEYS_HEADER, binding_path
 
 GQA_OK = 0
 GQA_ERR_INVALID_ARG = 1
@@ -541,9 +543,8 @@ def gqa_shared_keys_plan(desc: gqa_desc_t, kv_lens_host, prefix_len: int = 0, ma
 
 
 # ------------------------------------------------------- include/gqa_paged.h
-# A step of a few tokens is shorter on the GPU than its calls are here, so these
-# functions keep what follows from shapes, strides and types alone (the C
-# structures, and that they agree), and look at each tensor for the rest once.
+# A step of a few tokens is shorter on the GPU than calls marshalled here would be,
+# so what follows goes through csrc/paged_binding.cpp, which looks at the tensors.
 def rotary_turns(dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
                  original_length: int = 0, slow: float = 1.0, fast: float = 32.0, device=None):
     """The table the rotation turns by, int64 [dim / 2] (the bits of the C table's
@@ -560,147 +561,40 @@ def rotary_turns(dim: int, base: float = 10000.0, *, scaling: str = "none", fact
     return turns if device is None else turns.to(device)
 
 
-class _Handles:
-    """What every call needs of torch and of the library, looked up once."""
-
-    def __init__(self):
-        import torch
-
-        self.int32, self.int64, self.fp32 = torch.int32, torch.int64, torch.float32
-        self.current_stream, self.current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        self.lib = L = lib()
-        self.rotary_apply, self.paged_append, self.paged_keep = L.gqa_rotary_apply, L.gqa_paged_append, L.gqa_paged_keep
-        self.tree_from_parents, self.tree_attn = L.gqa_tree_from_parents, L.gqa_tree_attn
+_binding, _bound = None, None
 
 
-_handles = None
+def _paged():
+    """csrc/paged_binding.cpp, calling the loaded library."""
+    global _binding, _bound
+    if _bound is None or _bound is not _lib:
+        with _lock:
+            if _binding is None:
+                import torch  # noqa: F401  (whose libraries it is linked against)
 
-
-def _hot() -> _Handles:
-    global _handles
-    if _handles is None or _handles.lib is not _lib:
-        _handles = _Handles()
-    return _handles
-
-
-def _call(h, fn, device, stream, *args):
-    """The C function `fn` on `device`, in `stream`, the last of its arguments."""
-    raw = h.current_stream(device) if stream is None else _raw_stream(stream, device)
-    rc = fn(*args, raw) if h.current_device() == device else _on_device(device, fn, *args, raw)
-    if rc:
-        raise GQAError(rc, fn.__name__)
-
-
-def _need(t, what, device, dtype=None, shape=None):
-    """Raises unless t is a contiguous tensor on `device` of this type and shape (None: no tensor is fine too)."""
-    if t is None:
-        return
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {tuple(shape)}, not {tuple(t.shape)}")
-    if t.get_device() != device or device < 0 or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous and on the call's CUDA device")
-
-
-def _ints(t, device, int32, shape) -> bool:
-    """Whether t, if there is one, is a contiguous tensor on `device` of this type and shape."""
-    return t is None or (t.dtype is int32 and t.shape == shape and t.get_device() == device and t.is_contiguous())
-
-
-def _token_stride(t, what) -> int:
-    """Elements from token to token of t [..., tokens, heads, d]: dense heads, one stride for all tokens."""
-    return _strides_of_tokens(t.shape, t.stride(), what)
-
-
-@functools.lru_cache(maxsize=1024)
-def _strides_of_tokens(sizes, strides, what) -> int:
-    heads, d = sizes[-2:]
-    if (d > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != d):
-        raise ValueError(f"{what} must have dense heads")
-    stride, run = None, 1  # from the last token dimension outwards
-    for size, st in zip(reversed(sizes[:-2]), reversed(strides[:-2])):
-        if size == 1:
-            continue
-        if stride is None:
-            stride = st
-        elif st != stride * run:
-            raise ValueError(f"{what} must have one stride from token to token")
-        run *= size
-    return heads * d if stride is None else stride
-
-
-@functools.lru_cache(maxsize=256)
-def _rope(pairs, interleaved, inverse, magnitude):
-    return ctypes.byref(gqa_rotary_t(2 * pairs, 1 if interleaved else 0, 1 if inverse else 0, float(magnitude)))
-
-
-@functools.lru_cache(maxsize=1024)
-def _paged_layout(batch, tokens, q_heads, d, dtype, cache_shape, cache_strides, table_shape, out_dtype, scale, causal):
-    """The C descriptions of a batch and of caches [pages, page_size, kv_heads, d] (any strides but the last), and
-    the shapes of what belongs to the batch."""
-    codes = _type_codes()
-    code = codes.get(dtype)
-    if code is None or code == GQA_DTYPE_FP32:
-        raise ValueError(f"tensors and caches must be bf16 or fp16, not {dtype}")
-    out_code = code if out_dtype is None else codes.get(out_dtype)
-    if out_code is None:
-        raise ValueError(f"unsupported output type {out_dtype}")
-    if len(cache_shape) != 4 or cache_shape[3] != d or cache_strides[3] != 1:
-        raise ValueError(f"the caches must be [pages, page_size, kv_heads, {d}] with dense heads, not {tuple(cache_shape)}")
-    if len(table_shape) != 2 or table_shape[0] != batch:
-        raise ValueError(f"page_table must be [{batch}, pages of a sequence], not {tuple(table_shape)}")
-    pages, size, kv_heads, _ = cache_shape
-    strides = [n if k > 1 else d for n, k in zip(cache_strides, cache_shape)]  # (of one element: not used)
-    geometry = gqa_pages_t(pages, size, table_shape[1], strides[0], strides[1], strides[2])
-    desc = gqa_desc_t(batch, tokens, q_heads, kv_heads, d, min(table_shape[1] * size, 1 << 30), scale,
-                      1 if causal else 0, out_code, code, GQA_REDUCE_AUTO)
-    return (ctypes.byref(desc), ctypes.byref(geometry), (batch,), (batch, tokens),
-            (batch, tokens, (tokens + 31) // 32), (batch, tokens, q_heads))
-
-
-def _caches_agree(k_cache, v_cache, page_table, device, dtype, int32) -> bool:
-    return (k_cache.dtype is dtype and v_cache.dtype is dtype and v_cache.shape == k_cache.shape
-            and v_cache.stride() == k_cache.stride() and k_cache.get_device() == device
-            and v_cache.get_device() == device and page_table.dtype is int32 and page_table.get_device() == device
-            and page_table.is_contiguous())
-
-
-def _refuse_caches(k_cache, v_cache, page_table, device, dtype):
-    _need(page_table, "page_table", device, _hot().int32)
-    for t in (k_cache, v_cache):
-        if t.dtype is not dtype or t.get_device() != device:
-            raise ValueError("the caches must be of the inputs' type and on their device")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
-        raise ValueError("the caches must be alike in shape and strides")
-
-
-def _device_of(t, what) -> int:
-    device = t.get_device()
-    if device < 0:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    return device
+                path = binding_path()
+                if not os.path.exists(path):
+                    raise RuntimeError(f"binding of the paged calls not built ({path}); run "
+                                       "gqa_decode_blackwell_gb300.build.build() or __graft_entry__.build()")
+                loader = importlib.machinery.ExtensionFileLoader("_paged_binding", path)
+                _binding = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_binding", loader))
+        L = lib()
+        _binding.use(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.gqa_rotary_apply, L.gqa_paged_append, L.gqa_tree_from_parents, L.gqa_tree_workspace_size, L.gqa_tree_attn,
+            L.gqa_paged_keep)))
+        _bound = L
+    return _binding
 
 
 def gqa_rotary_apply(x, positions, turns, out, *, interleaved: bool = False, inverse: bool = False,
                      magnitude: float = 0.0, stream=None) -> None:
     """Rotates x [..., heads, d] to positions int32 [...] into ``out`` (x itself, or
     apart from it); see gqa_rotary_apply in ``include/gqa_paged.h``."""
-    device = _device_of(x, "x")
-    h, shape = _hot(), x.shape
-    code = _type_codes().get(x.dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    if len(shape) < 3 or out.dtype is not x.dtype or out.shape != shape or out.get_device() != device:
-        raise ValueError("x must be [..., heads, d], and out of its type and shape and on its device")
-    if not _ints(positions, device, h.int32, shape[:-2]) or positions is None:
-        raise ValueError(f"positions must be contiguous int32 {tuple(shape[:-2])} on x's device")
-    if not _ints(turns, device, h.int64, turns.shape):
-        _need(turns, "turns (of rotary_turns)", device, h.int64)
-    _call(h, h.rotary_apply, device, stream, _rope(turns.numel(), interleaved, inverse, magnitude),
-          turns.data_ptr(), positions.data_ptr(), positions.numel(), shape[-2], shape[-1], code, x.data_ptr(),
-          _strides_of_tokens(shape, x.stride(), "x"), out.data_ptr(),
-          _strides_of_tokens(shape, out.stride(), "out"))
+    if stream is not None:
+        stream = _raw_stream(stream, x.get_device())
+    rc = _paged().rotary_apply(x, positions, turns, out, interleaved, inverse, magnitude, stream)
+    if rc:
+        raise GQAError(rc, "gqa_rotary_apply")
 
 
 def rotary(x, positions, turns, *, interleaved: bool = False, inverse: bool = False, magnitude: float = 0.0,
@@ -708,7 +602,8 @@ def rotary(x, positions, turns, *, interleaved: bool = False, inverse: bool = Fa
     """Allocates the result with torch and calls gqa_rotary_apply."""
     import torch
 
-    _device_of(x, "x")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
     with torch.cuda.stream(_torch_stream(stream, x.device)):
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     gqa_rotary_apply(x, positions, turns, out, interleaved=interleaved, inverse=inverse, magnitude=magnitude,
@@ -722,40 +617,12 @@ def gqa_paged_append(q, k, v, q_out, k_cache, v_cache, page_table, seqlens, *, n
     and v [B, nq, Hkv, d] into the paged caches; q, k and v may be views of one
     tensor, q and q_out may be None, turns None rotates nothing.  See
     gqa_paged_append in ``include/gqa_paged.h``."""
-    device = _device_of(k, "k")
-    h, dtype, shape = _hot(), k.dtype, k.shape
-    if len(shape) != 4 or v.shape != shape or v.dtype is not dtype or v.get_device() != device:
-        raise ValueError("k and v must be [B, nq, kv_heads, d], of one type and device")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    heads = shape[2] if q is None else q.shape[-2]
-    desc, geometry, batch, tokens, _, _ = _paged_layout(shape[0], shape[1], heads, shape[3], dtype, k_cache.shape,
-                                                        k_cache.stride(), page_table.shape, None, 0.0, False)
-    if k_cache.shape[2] != shape[2]:
-        raise ValueError(f"k {tuple(shape)} and cache {tuple(k_cache.shape)} disagree")
-    if not _caches_agree(k_cache, v_cache, page_table, device, dtype, h.int32):
-        _refuse_caches(k_cache, v_cache, page_table, device, dtype)
-    int32 = h.int32
-    if not (seqlens is not None and _ints(seqlens, device, int32, batch)
-            and (new_lens is None or _ints(new_lens, device, int32, batch))
-            and (positions is None or _ints(positions, device, int32, tokens))):
-        raise ValueError("seqlens and new_lens must be int32 [B], positions int32 [B, nq], contiguous on k's device")
-    q_at, q_stride, out_at = None, 0, None
-    if q is not None:
-        if (q.shape != (*tokens, heads, shape[3]) or q.dtype is not dtype or q.get_device() != device
-                or q_out.shape != q.shape or q_out.dtype is not dtype or q_out.get_device() != device
-                or not q_out.is_contiguous()):
-            raise ValueError("q must be [B, nq, q_heads, d], of k's type and on its device, and q_out so and contiguous")
-        q_at, q_stride, out_at = q.data_ptr(), _strides_of_tokens(q.shape, q.stride(), "q"), q_out.data_ptr()
-    rope = table = None
-    if turns is not None:
-        if not _ints(turns, device, h.int64, turns.shape):
-            _need(turns, "turns (of rotary_turns)", device, h.int64)
-        rope, table = _rope(turns.shape[0], interleaved, False, magnitude), turns.data_ptr()
-    _call(h, h.paged_append, device, stream, desc, geometry, rope, table, _ptr(positions), q_at, q_stride,
-          k.data_ptr(), _strides_of_tokens(shape, k.stride(), "k"), v.data_ptr(),
-          _strides_of_tokens(shape, v.stride(), "v"), out_at, k_cache.data_ptr(), v_cache.data_ptr(),
-          page_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens))
+    if stream is not None:
+        stream = _raw_stream(stream, k.get_device())
+    rc = _paged().paged_append(q, k, v, q_out, k_cache, v_cache, page_table, seqlens, new_lens, positions, turns,
+                               interleaved, magnitude, stream)
+    if rc:
+        raise GQAError(rc, "gqa_paged_append")
 
 
 def gqa_tree_from_parents(parents, seqlens, tree, positions=None, *, new_lens=None, max_seqlen: int = 1 << 30,
@@ -763,60 +630,29 @@ def gqa_tree_from_parents(parents, seqlens, tree, positions=None, *, new_lens=No
     """The drafts' tree of parents int32 [B, nq] as bits, int32 [B, nq, ceil(nq / 32)],
     and their positions int32 [B, nq]; see gqa_tree_from_parents in
     ``include/gqa_paged.h``."""
-    device = _device_of(parents, "parents")
-    h, shape = _hot(), parents.shape
-    if len(shape) != 2:
-        raise ValueError("parents must be [B, nq]")
-    B, nq = shape
-    for t, what, size in ((parents, "parents", shape), (seqlens, "seqlens", (B,)), (new_lens, "new_lens", (B,)),
-                          (tree, "tree", (B, nq, (nq + 31) // 32)), (positions, "positions", shape)):
-        if not _ints(t, device, h.int32, size):
-            _need(t, what, device, h.int32, size)
-    _call(h, h.tree_from_parents, device, stream, B, nq, int(max_seqlen), parents.data_ptr(), seqlens.data_ptr(),
-          _ptr(new_lens), tree.data_ptr(), _ptr(positions))
+    if stream is not None:
+        stream = _raw_stream(stream, parents.get_device())
+    rc = _paged().tree_from_parents(parents, seqlens, tree, positions, new_lens, max_seqlen, stream)
+    if rc:
+        raise GQAError(rc, "gqa_tree_from_parents")
 
 
 def gqa_tree_workspace_size(q, k_cache, page_table, *, out_dtype=None) -> int:
     """Bytes gqa_tree_attn needs for q [B, nq, Hq, d] over the paged caches."""
-    device = _device_of(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, nq, q_heads, d]")
-    desc, geometry = _paged_layout(*q.shape, q.dtype, k_cache.shape, k_cache.stride(), page_table.shape, out_dtype, 0.0,
-                                   False)[:2]
-    return int(_on_device(device, lib().gqa_tree_workspace_size, desc, geometry))
+    code = -1 if out_dtype is None else _dtype_code(out_dtype, (GQA_DTYPE_BF16, GQA_DTYPE_FP32, GQA_DTYPE_FP16))
+    return _paged().tree_workspace_size(q, k_cache, page_table, code)
 
 
 def gqa_tree_attn(q, k_cache, v_cache, page_table, seqlens, out, lse=None, workspace=None, *, new_lens=None,
                   tree=None, causal: bool = False, scale: float = 0.0, stream=None) -> None:
     """Attention of new tokens over the paged caches into ``out`` (and ``lse``); see
     gqa_tree_attn in ``include/gqa_paged.h``."""
-    device = _device_of(q, "q")
-    h, dtype, shape = _hot(), q.dtype, q.shape
-    if len(shape) != 4:
-        raise ValueError("q must be [B, nq, q_heads, d]")
-    desc, geometry, batch, _, bits, rows = _paged_layout(*shape, dtype, k_cache.shape, k_cache.stride(),
-                                                         page_table.shape, out.dtype, scale, causal)
-    if not _caches_agree(k_cache, v_cache, page_table, device, dtype, h.int32):
-        _refuse_caches(k_cache, v_cache, page_table, device, dtype)
-    int32 = h.int32
-    if not (seqlens is not None and _ints(seqlens, device, int32, batch)
-            and (new_lens is None or _ints(new_lens, device, int32, batch))
-            and (tree is None or _ints(tree, device, int32, bits))):
-        raise ValueError("seqlens and new_lens must be int32 [B], tree int32 [B, nq, ceil(nq / 32)], contiguous on q's "
-                         "device")
-    if not (q.is_contiguous() and out.shape == shape and out.is_contiguous() and out.get_device() == device):
-        raise ValueError("q and out must be contiguous, of one shape and on one device")
-    if lse is not None and not (lse.dtype is h.fp32 and lse.shape == rows and lse.is_contiguous()
-                                and lse.get_device() == device):
-        raise ValueError("lse must be contiguous fp32 [B, nq, Hq] on q's device")
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.get_device() != device:
-            raise ValueError("workspace must be contiguous and on q's device")
-        ws, ws_bytes = workspace.data_ptr(), _bytes_of(workspace)
-    _call(h, h.tree_attn, device, stream, desc, geometry, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          page_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), _ptr(tree), out.data_ptr(), _ptr(lse), ws,
-          ws_bytes)
+    if stream is not None:
+        stream = _raw_stream(stream, q.get_device())
+    rc = _paged().tree_attn(q, k_cache, v_cache, page_table, seqlens, out, lse, workspace, new_lens, tree, causal, scale,
+                            stream)
+    if rc:
+        raise GQAError(rc, "gqa_tree_attn")
 
 
 def tree_attention(q, k_cache, v_cache, page_table, seqlens, *, new_lens=None, tree=None, causal: bool = False,
@@ -835,18 +671,8 @@ def gqa_paged_keep(k_cache, v_cache, page_table, seqlens, path, keep_lens, seqle
     [B] count, together behind the positions before its new tokens (``tokens`` of
     them, or new_lens); seqlens_out int32 [B] gets the new lengths and may be
     seqlens.  See gqa_paged_keep in ``include/gqa_paged.h``."""
-    device = _device_of(k_cache, "k_cache")
-    h, shape, cache = _hot(), path.shape, k_cache.shape
-    if len(shape) != 2 or len(cache) != 4:
-        raise ValueError("path must be [B, n], and the caches [pages, page_size, kv_heads, d]")
-    desc, geometry, batch = _paged_layout(shape[0], int(tokens), cache[2], cache[3], k_cache.dtype, cache,
-                                          k_cache.stride(), page_table.shape, None, 0.0, False)[:3]
-    if not _caches_agree(k_cache, v_cache, page_table, device, k_cache.dtype, h.int32):
-        _refuse_caches(k_cache, v_cache, page_table, device, k_cache.dtype)
-    for t, what, size in ((seqlens, "seqlens", batch), (new_lens, "new_lens", batch), (path, "path", shape),
-                          (keep_lens, "keep_lens", batch), (seqlens_out, "seqlens_out", batch)):
-        if not _ints(t, device, h.int32, size):
-            _need(t, what, device, h.int32, size)
-    _call(h, h.paged_keep, device, stream, desc, geometry, k_cache.data_ptr(), v_cache.data_ptr(),
-          page_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), path.data_ptr(), shape[1], keep_lens.data_ptr(),
-          _ptr(seqlens_out))
+    if stream is not None:
+        stream = _raw_stream(stream, k_cache.get_device())
+    rc = _paged().paged_keep(k_cache, v_cache, page_table, seqlens, path, keep_lens, seqlens_out, new_lens, tokens, stream)
+    if rc:
+        raise GQAError(rc, "gqa_paged_keep")

@@ -1,14 +1,17 @@
 """Builds the sm_103a shared library in-tree with nvcc.
 
 The library is a plain C-ABI ``.so`` (see ``include/gqa_decode.h``,
-``include/gqa_shared_keys.h`` and ``include/gqa_paged.h``); nothing here links
-against PyTorch.
+``include/gqa_shared_keys.h`` and ``include/gqa_paged.h``); nothing in it links
+against PyTorch.  Beside it stands the native binding of the paged calls
+(``csrc/paged_binding.cpp``, g++), which does, and only marshals tensors.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +29,7 @@ DEBUG_LIB = os.path.join(PKG, "libgqa_decode_sm103_debug.so")
 # (-DGQA_TRACE): gqa_trace_attach() names a device buffer that the following
 # launches stamp per CTA, role and block.  For measurement only.
 TRACE_LIB = os.path.join(PKG, "libgqa_decode_sm103_trace.so")
+BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -39,6 +43,33 @@ def _nvcc() -> str:
 def sources():
     return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))] + [
         HEADER, SHARED_KEYS_HEADER, PAGED_HEADER]
+
+
+def binding_path() -> str:
+    """Where the binding for the present Python and PyTorch is: it holds for no others."""
+    import torch
+
+    return os.path.join(PKG, f"_paged_binding-{sys.implementation.cache_tag}-torch{torch.__version__}.so")
+
+
+def _start_binding(out: str) -> subprocess.Popen:
+    import torch
+
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    includes = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+                os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    return subprocess.Popen([
+        shutil.which("g++") or "g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-w",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in includes),
+        BINDING_SOURCE, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+        "-o", out])
+
+
+def _binding_up_to_date(out: str) -> bool:
+    if not os.path.exists(out):
+        return False
+    return all(os.path.getmtime(s) <= os.path.getmtime(out) for s in (BINDING_SOURCE, HEADER, PAGED_HEADER))
 
 
 def up_to_date(out: str = LIB) -> bool:
@@ -71,7 +102,23 @@ def _units(build_dir: str):
 
 def build(force: bool = False, out: str = LIB, extra_flags=(), verbose: bool = False) -> str:
     """Compile the csrc translation units for sm_103a (in parallel) and link
-    them into ``out`` (skipped if current)."""
+    them into ``out``, and for the library itself the binding beside it (each
+    skipped if current)."""
+    binding = binding_path() if out == LIB else None
+    if binding is None or (not force and _binding_up_to_date(binding)):
+        return _build_library(force, out, extra_flags, verbose)
+    temporary = f"{binding}.{os.getpid()}.tmp"
+    process = _start_binding(temporary)
+    try:
+        return _build_library(force, out, extra_flags, verbose)
+    finally:
+        if process.wait() == 0:
+            os.replace(temporary, binding)
+        else:
+            raise subprocess.CalledProcessError(process.returncode, "g++ (paged_binding.cpp)")
+
+
+def _build_library(force: bool, out: str, extra_flags, verbose: bool) -> str:
     if not force and up_to_date(out):
         return out
     build_dir = os.path.join(os.path.dirname(os.path.abspath(out)), "_build",

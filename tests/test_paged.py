@@ -242,9 +242,9 @@ def test_python_checks_tensors():
 def test_one_stride_for_all_tokens(t, stride):
     if stride is None:
         with pytest.raises(ValueError):
-            g._token_stride(t, "t")
+            g._paged().stride_of(t)
     else:
-        assert g._token_stride(t, "t") == stride
+        assert g._paged().stride_of(t) == stride
 
 
 # ------------------------------------------------------- the rotation's table
@@ -990,6 +990,56 @@ def test_graph_of_a_step_follows_its_inputs(dev):
         graph.replay()
     torch.cuda.synchronize()
     s.check()
+    assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
+def test_tensors_that_do_not_fit_are_refused(dev):
+    """Types, shapes, strides and devices, each wrong by itself; nothing is launched, and nothing changes."""
+    c = Case(dev, [40, 90], None, 6, 8, 2, 64, 16, seed=98)
+    k = _randn(dev, 2, 6, 2, 64, seed=99)
+    parents, tree, at = _ints(dev, [[-1] * 6] * 2), torch.zeros(2, 6, 1, dtype=torch.int32, device=dev), _ints(dev, [[0] * 6] * 2)
+    turns, path = g.rotary_turns(64, device=dev), _ints(dev, [[0, 2]] * 2)
+    keep, news = _ints(dev, [2, 2]), _ints(dev, [6, 5])
+    out, lse = torch.zeros_like(c.q), torch.zeros(2, 6, 8, device=dev)
+    ws = torch.zeros(max(g.gqa_tree_workspace_size(c.q, c.k, c.table), 1), dtype=torch.uint8, device=dev)
+    calls = {
+        "apply": (g.gqa_rotary_apply, dict(x=c.q, positions=at, turns=turns, out=c.q.clone())),
+        "append": (g.gqa_paged_append, dict(q=c.q, k=k, v=k, q_out=out, k_cache=c.k, v_cache=c.v, page_table=c.table,
+                                            seqlens=c.ln, new_lens=news, positions=at, turns=turns)),
+        "parents": (g.gqa_tree_from_parents, dict(parents=parents, seqlens=c.ln, tree=tree, positions=at, new_lens=news)),
+        "attn": (g.gqa_tree_attn, dict(q=c.q, k_cache=c.k, v_cache=c.v, page_table=c.table, seqlens=c.ln, out=out, lse=lse,
+                                       workspace=ws, new_lens=news, tree=tree)),
+        "keep": (g.gqa_paged_keep, dict(k_cache=c.k, v_cache=c.v, page_table=c.table, seqlens=c.ln, path=path,
+                                        keep_lens=keep, seqlens_out=c.ln.clone(), new_lens=news, tokens=6)),
+    }
+    for name, (fn, args) in calls.items():
+        fn(**args)                                                     # as they are, they do fit
+        torch.cuda.synchronize()
+        held = {n: t.clone() for n, t in args.items() if isinstance(t, torch.Tensor)}
+        for n, t in args.items():
+            if not isinstance(t, torch.Tensor):
+                continue
+            wrong = [t.cpu(), t.to(torch.float64), t[:1] if n != "turns" else t[None], t[..., None]]
+            if n == "workspace":
+                wrong = [t.cpu(), torch.cat([t, t])[::2]]
+            elif n != "turns":
+                wrong.append(torch.cat([t, t], dim=-1)[..., ::2])
+            for w in wrong:
+                with pytest.raises(ValueError):
+                    fn(**{**args, n: w})
+            with pytest.raises(TypeError):
+                fn(**{**args, n: "a tensor"})
+            if n not in ("q", "q_out", "lse", "workspace", "new_lens", "turns", "tree", "positions", "seqlens_out"):
+                with pytest.raises(ValueError):
+                    fn(**{**args, n: None})
+        torch.cuda.synchronize()
+        for n, t in held.items():
+            assert torch.equal(args[n], t), (name, n)
+    with pytest.raises(ValueError):
+        g.gqa_paged_append(c.q, k, k, None, c.k, c.v, c.table, c.ln)   # q without a place for it
+    with pytest.raises(TypeError):
+        g.gqa_tree_attn(**{**calls["attn"][1], "scale": "a number"})
     assert g.gqa_decode_get_error() == g.GQA_OK
 
 
