@@ -107,7 +107,8 @@ def build(force: bool = False, out: str = LIB, extra_flags=(), verbose: bool = F
     binding = binding_path() if out == LIB else None
     if binding is None or (not force and _binding_up_to_date(binding)):
         return _build_library(force, out, extra_flags, verbose)
-    temporary = f"{binding}.{os.getpid()}.tmp"
+    os.makedirs(os.path.join(PKG, "_build"), exist_ok=True)
+    temporary = os.path.join(PKG, "_build", f"{os.path.basename(binding)}.{os.getpid()}")
     process = _start_binding(temporary)
     try:
         return _build_library(force, out, extra_flags, verbose)

@@ -72,19 +72,23 @@ int run_of(bool interleaved, int pairs) {
 }
 
 template <typename T, bool APPEND, bool INTERLEAVED, int N>
-const void* rotary_instance() {
-  if constexpr (APPEND) return reinterpret_cast<const void*>(&gqa_append_kernel<T, INTERLEAVED, N>);
-  else return reinterpret_cast<const void*>(&gqa_rotary_kernel<T, INTERLEAVED, N>);
+const void* rotary_instance(bool grouped) {
+  if constexpr (APPEND)
+    return grouped ? reinterpret_cast<const void*>(&gqa_append_kernel<T, INTERLEAVED, N, true>)
+                   : reinterpret_cast<const void*>(&gqa_append_kernel<T, INTERLEAVED, N, false>);
+  else
+    return grouped ? reinterpret_cast<const void*>(&gqa_rotary_kernel<T, INTERLEAVED, N, true>)
+                   : reinterpret_cast<const void*>(&gqa_rotary_kernel<T, INTERLEAVED, N, false>);
 }
 
 // The rotation kernel for a type, a layout and a run.
 template <typename T, bool APPEND>
-const void* rotary_fn(bool interleaved, int run) {
-  if (interleaved) return rotary_instance<T, APPEND, true, 8>();
-  return run == 8   ? rotary_instance<T, APPEND, false, 8>()
-         : run == 4 ? rotary_instance<T, APPEND, false, 4>()
-         : run == 2 ? rotary_instance<T, APPEND, false, 2>()
-                    : rotary_instance<T, APPEND, false, 1>();
+const void* rotary_fn(bool interleaved, int run, bool grouped) {
+  if (interleaved) return rotary_instance<T, APPEND, true, 8>(grouped);
+  return run == 8   ? rotary_instance<T, APPEND, false, 8>(grouped)
+         : run == 4 ? rotary_instance<T, APPEND, false, 4>(grouped)
+         : run == 2 ? rotary_instance<T, APPEND, false, 2>(grouped)
+                    : rotary_instance<T, APPEND, false, 1>(grouped);
 }
 
 // Few tokens are spread over CTAs of a unit (two runs) a thread, up to a GPU full
@@ -92,16 +96,34 @@ const void* rotary_fn(bool interleaved, int run) {
 // 256 threads where they have two units or more each or all of them one, and else of
 // 128.  Measured on GB300 (128, 256): 8192 places of 384 units 18.5 and 20.4 us, 8192
 // of 256 21.1 and 21.0, 2048 of 1280 20.2 and 16.5, 2048 of 512 in fp32 25.5 and 24.2.
-gqa_status_t launch_rotary(const void* fn, RotaryParams& p, long long tokens, int rows, int run, int sm,
+// Many tokens of few units share CTAs.
+template <bool APPEND>
+gqa_status_t launch_rotary(int dtype, bool interleaved, RotaryParams& p, long long tokens, int rows, int sm,
                            cudaStream_t s) {
+  const int run = run_of(interleaved, p.pairs);
   const long long units = static_cast<long long>(rows) * (p.head_dim / (2 * run));
   long long threads = 128, parts = (units + threads - 1) / threads;
   const long long spread = 16LL * sm / tokens;
-  if (spread < parts) {
+  const bool grouped = spread < 1 && units <= kGroupUnits;
+  if (grouped) {
+    p.group = static_cast<int>(kGroupThreads / units);
+    threads = kGroupThreads;
+    parts = 1;
+  } else if (spread < parts) {
     threads = units > 2 * kRotaryThreads || units % kRotaryThreads == 0 ? kRotaryThreads : 128;
     parts = spread > 1 ? spread : 1;
   }
-  return launch_kernel(fn, dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(parts < 65535 ? parts : 65535)),
+  p.tokens = tokens;
+  const void* fn;
+  if (dtype == GQA_DTYPE_FP16) {
+    fn = rotary_fn<__half, APPEND>(interleaved, run, grouped);
+  } else if (APPEND || dtype == GQA_DTYPE_BF16) {
+    fn = rotary_fn<__nv_bfloat16, APPEND>(interleaved, run, grouped);
+  } else {
+    if constexpr (!APPEND) fn = rotary_fn<float, APPEND>(interleaved, run, grouped);
+  }
+  const long long ctas = grouped ? (tokens + p.group - 1) / p.group : tokens;
+  return launch_kernel(fn, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(parts < 65535 ? parts : 65535)),
                        static_cast<int>(threads), 0, &p, s);
 }
 
@@ -176,12 +198,8 @@ gqa_status_t gqa_rotary_apply(const gqa_rotary_t* rope, const uint64_t* turns, c
   p.pairs = rope->dim / 2;
   p.inverse = rope->inverse != 0 ? 1 : 0;
   p.magnitude = rope->magnitude > 0.f ? rope->magnitude : 1.f;
-  const bool il = rope->interleaved != 0;
-  const int run = run_of(il, p.pairs);
-  const void* fn = dtype == GQA_DTYPE_FP32   ? rotary_fn<float, false>(il, run)
-                   : dtype == GQA_DTYPE_FP16 ? rotary_fn<__half, false>(il, run)
-                                             : rotary_fn<__nv_bfloat16, false>(il, run);
-  return launch_rotary(fn, p, tokens, heads, run, st->sm_count, static_cast<cudaStream_t>(stream));
+  return launch_rotary<false>(dtype, rope->interleaved != 0, p, tokens, heads, st->sm_count,
+                              static_cast<cudaStream_t>(stream));
 }
 
 gqa_status_t gqa_paged_append(const gqa_desc_t* desc, const gqa_pages_t* pages, const gqa_rotary_t* rope,
@@ -233,12 +251,8 @@ gqa_status_t gqa_paged_append(const gqa_desc_t* desc, const gqa_pages_t* pages, 
   p.pairs = rope != nullptr ? rope->dim / 2 : 0;
   p.magnitude = rope != nullptr && rope->magnitude > 0.f ? rope->magnitude : 1.f;
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
-  const bool il = rope != nullptr && rope->interleaved != 0;
-  const int run = run_of(il, p.pairs);
-  const void* fn = desc->in_dtype == GQA_DTYPE_FP16 ? rotary_fn<__half, true>(il, run)
-                                                    : rotary_fn<__nv_bfloat16, true>(il, run);
-  return launch_rotary(fn, p, tokens, p.x.heads + 2 * desc->kv_heads, run, st->sm_count,
-                       static_cast<cudaStream_t>(stream));
+  return launch_rotary<true>(desc->in_dtype, rope != nullptr && rope->interleaved != 0, p, tokens,
+                             p.x.heads + 2 * desc->kv_heads, st->sm_count, static_cast<cudaStream_t>(stream));
 }
 
 gqa_status_t gqa_tree_from_parents(int batch, int q_tokens, int max_seqlen, const int32_t* parents,

@@ -24,6 +24,9 @@ namespace gqa {
 
 constexpr int kRotaryThreads = 256;  // of a CTA, at most
 constexpr int kMaxPairs = 128;  // of a head: head_dim / 2
+// Tokens of at most this many units (two runs of a head) share a CTA of
+// kGroupThreads, a unit to a thread.
+constexpr int kGroupUnits = 64, kGroupThreads = 2 * kGroupUnits;
 
 // Tokens' heads to rotate or copy: `heads` of each token, dense, `stride`
 // elements from token to token.
@@ -49,6 +52,8 @@ struct RotaryParams {
   int head_dim, pairs;
   int inverse;
   float magnitude;
+  int group;                 // tokens of a CTA (kernels of groups)
+  long long tokens;
   unsigned int* err_word;
 };
 
@@ -224,6 +229,27 @@ __device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, 
   }
 }
 
+// A group's tokens: this thread's among them and its unit, and the tokens there
+// are.  Their angles lie one token's behind the other's, 128 threads' units of 8 pairs
+// at most: 512 words, for tokens of one head.
+constexpr int kGroupAngles = kGroupThreads * 4;
+struct Member {
+  int sub, unit, count, angles;
+  bool here;
+};
+template <int N>
+__device__ __forceinline__ Member member_of(const RotaryParams& p, int n_rows) {
+  const int units = n_rows << (31 - __clz(p.head_dim / (2 * N))), tid = static_cast<int>(threadIdx.x);
+  Member m;
+  m.sub = tid / units;
+  m.unit = tid - m.sub * units;
+  const long long left = p.tokens - static_cast<long long>(blockIdx.x) * p.group;
+  m.count = left < p.group ? static_cast<int>(left) : p.group;
+  m.angles = (N > 1 ? N / 2 : 1) * ((p.pairs + N - 1) / N);
+  m.here = m.sub < m.count;
+  return m;
+}
+
 }  // namespace detail
 
 // A token to blockIdx.x, of whose heads blockIdx.y takes its part.  N: the longest
@@ -231,12 +257,41 @@ __device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, 
 // are pairs.  Measured on GB300: 1264 tokens of 36 heads of 64, of which 16, 24, 20 and
 // 6 elements turn (runs of 8, 4, 2, 1), 5.3, 6.2, 8.0 and 10.8 us.  32 registers let an
 // SM hold 2048 threads (40: 2048 tokens of 80 heads of 256 18.8 us, 16.5 so).
-template <typename T, bool INTERLEAVED, int N>
-__global__ void __launch_bounds__(kRotaryThreads, sizeof(T) == 4 ? 6 : 8)
+// GROUPED: p.group tokens of few heads to a CTA, a unit to a thread; a CTA to each
+// would be bound by the CTAs an SM can start (44931 tokens of 8 heads of 64 45.5 us, 16.0
+// so, at HBM rate 13.6; 10935 of them 11.4 and 5.6).
+template <typename T, bool INTERLEAVED, int N, bool GROUPED>
+__global__ void __launch_bounds__(GROUPED ? kGroupThreads : kRotaryThreads, GROUPED ? 12 : sizeof(T) == 4 ? 6 : 8)
 gqa_rotary_kernel(const RotaryParams p) {
-  __shared__ float4 table[kMaxPairs];
+  __shared__ float4 table[GROUPED ? detail::kGroupAngles : kMaxPairs];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if constexpr (GROUPED) {
+    const detail::Member m = detail::member_of<N>(p, p.x.heads);
+    const long long first = static_cast<long long>(blockIdx.x) * p.group;
+    const int row_shift = 31 - __clz(p.head_dim / (2 * N)), head = m.unit >> row_shift;
+    const int i = m.unit - (head << row_shift);
+    const int2 at = detail::runs_of<INTERLEAVED, N>(i, p.pairs);
+    const long long in_token = static_cast<long long>(head) * p.head_dim, token = first + m.sub;
+    detail::Run<T, N> a, b;
+    if (m.here) {
+      const T* from = static_cast<const T*>(p.x.src) + token * p.x.src_stride + in_token;
+      a.load(from + at.x);
+      b.load(from + at.y);
+    }
+    for (int j = static_cast<int>(threadIdx.x); j < m.count * p.pairs; j += kGroupThreads) {
+      const int s = j / p.pairs, pair = j - s * p.pairs;
+      detail::put_angle<N>(table + s * m.angles, pair, p.pairs,
+                           detail::turn_of(p.turns[pair], p.positions[first + s], p.inverse, p.magnitude));
+    }
+    __syncthreads();
+    if (!m.here) return;
+    detail::turn_runs<T, INTERLEAVED, N>(a, b, table + m.sub * m.angles, i, p.pairs);
+    T* to = static_cast<T*>(p.x.dst) + token * p.x.dst_stride + in_token;
+    a.store(to + at.x);
+    b.store(to + at.y);
+    return;
+  }
   const long long token = blockIdx.x;
   const int tid = static_cast<int>(threadIdx.x);
   const int position = p.positions[token];
@@ -257,12 +312,66 @@ gqa_rotary_kernel(const RotaryParams p) {
 
 // The same for a batch's new tokens: queries into x.dst, keys and values into
 // the page that holds the token's place.
-template <typename T, bool INTERLEAVED, int N>
-__global__ void __launch_bounds__(kRotaryThreads, sizeof(T) == 4 ? 6 : 8)
+template <typename T, bool INTERLEAVED, int N, bool GROUPED>
+__global__ void __launch_bounds__(GROUPED ? kGroupThreads : kRotaryThreads, GROUPED ? 12 : sizeof(T) == 4 ? 6 : 8)
 gqa_append_kernel(const RotaryParams p) {
-  __shared__ float4 table[kMaxPairs];
+  __shared__ float4 table[GROUPED ? detail::kGroupAngles : kMaxPairs];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if constexpr (GROUPED) {
+    __shared__ int positions[kGroupThreads];
+    const int hq = p.x.heads, hk = p.k.heads, d = p.head_dim;
+    const detail::Member m = detail::member_of<N>(p, hq + 2 * hk);
+    const long long token = static_cast<long long>(blockIdx.x) * p.group + m.sub;
+    const int row_shift = 31 - __clz(d / (2 * N)), r = m.unit >> row_shift, i = m.unit - (r << row_shift);
+    const int pairs = r < hq + hk ? p.pairs : 0;
+    const int2 at = detail::runs_of<INTERLEAVED, N>(i, pairs);
+    detail::Run<T, N> a, b;
+    bool there = false;
+    int place = 0, page = -1;
+    if (m.here) {
+      const int e = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(p.nq));
+      const int t = static_cast<int>(token) - e * p.nq;
+      const int raw = p.seqlens[e], L = clamp_len(raw, p.max_seqlen);
+      if (raw != L && t == 0 && m.unit == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadSeqlen));
+      const int n = detail::live_tokens(p.pages, p.err_word, e, L, p.nq);
+      there = t < n;
+      place = L - n + t;
+      if (there) {
+        const T* from = r < hq        ? static_cast<const T*>(p.x.src) + token * p.x.src_stride + r * d
+                        : r < hq + hk ? static_cast<const T*>(p.k.src) + token * p.k.src_stride + (r - hq) * d
+                                      : static_cast<const T*>(p.v.src) + token * p.v.src_stride + (r - hq - hk) * d;
+        a.load(from + at.x);
+        b.load(from + at.y);
+        page = p.pages.table[static_cast<long long>(e) * p.pages.cols + (place >> p.pages.page_shift)];
+      }
+      if (m.unit == 0) positions[m.sub] = p.positions != nullptr && there ? p.positions[token] : place;
+    }
+    __syncthreads();
+    for (int j = static_cast<int>(threadIdx.x); j < m.count * p.pairs; j += kGroupThreads) {
+      const int s = j / p.pairs, pair = j - s * p.pairs;
+      detail::put_angle<N>(table + s * m.angles, pair, p.pairs,
+                           detail::turn_of(p.turns[pair], positions[s], 0, p.magnitude));
+    }
+    __syncthreads();
+    if (!there) return;
+    if (pairs > 0) detail::turn_runs<T, INTERLEAVED, N>(a, b, table + m.sub * m.angles, i, pairs);
+    T* to;
+    if (r < hq) {
+      to = static_cast<T*>(p.x.dst) + token * p.x.dst_stride + r * d;
+    } else {
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages.num_pages)) {
+        atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
+        return;
+      }
+      const int h = r < hq + hk ? r - hq : r - hq - hk;
+      to = static_cast<T*>(r < hq + hk ? p.k_cache : p.v_cache) + page * p.page_stride +
+           (place & p.pages.page_mask) * p.pos_stride + h * p.head_stride;
+    }
+    a.store(to + at.x);
+    b.store(to + at.y);
+    return;
+  }
   const long long token = blockIdx.x;
   const int tid = static_cast<int>(threadIdx.x);
   const int b = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.nq));

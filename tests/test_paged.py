@@ -349,6 +349,28 @@ def test_rotary_matches_the_definition(dev, T, H, d, dim, interleaved, dtype, kw
 
 
 @gpu
+@pytest.mark.parametrize("T,H,d,dim,interleaved,dtype", [
+    (2700, 1, 64, 64, False, BF16), (2701, 3, 64, 20, False, FP16), (2702, 8, 64, 18, True, BF16), (2703, 9, 64, 64, True, FP32),
+    (2704, 5, 128, 24, False, FP32), (2705, 8, 128, 128, False, BF16), (2706, 3, 256, 256, False, BF16),
+    (2707, 4, 256, 250, True, FP16), (2708, 1, 64, 18, False, BF16), (2709, 2, 64, 2, False, FP32)])
+def test_rotary_of_many_tokens_of_few_heads(dev, T, H, d, dim, interleaved, dtype):
+    """Tokens that share a CTA, the last one's not full; out of a view and into one."""
+    wide = _randn(dev, T, H + 2, d, dtype=dtype, seed=T)
+    into = torch.full((T, H + 1, d), 7.0, dtype=dtype, device=dev)
+    x, out = wide[:, 1: H + 1], into[:, 1:]
+    positions = torch.randint(-2 ** 31, 2 ** 31 - 1, (T,), device=dev, generator=torch.Generator(dev).manual_seed(T)).to(torch.int32)
+    turns = g.rotary_turns(dim, 10000.0, device=dev)
+    for inverse in (False, True):
+        g.gqa_rotary_apply(x, positions, turns, out, interleaved=interleaved, inverse=inverse, magnitude=0.5)
+        _check_turned(out, _turned(x, positions, turns, interleaved, inverse, 0.5))
+        assert torch.equal(out[..., dim:], x[..., dim:]) and (into[:, 0] == 7).all()
+    before = wide.clone()
+    g.gqa_rotary_apply(x, positions, turns, x, interleaved=interleaved, inverse=True, magnitude=0.5)
+    assert torch.equal(x, out)
+    assert torch.equal(wide[:, 0], before[:, 0]) and torch.equal(wide[:, H + 1:], before[:, H + 1:])
+
+
+@gpu
 @pytest.mark.parametrize("dim,interleaved", [(64, False), (20, False), (20, True)])
 def test_rotary_of_views_keeps_what_is_around(dev, dim, interleaved):
     """Heads out of one projection's output, into part of another tensor; elements that are not rotated pass
@@ -528,6 +550,10 @@ APPEND = [  # lens, news, T, H, K, d, page, dtype, heads first, dim, interleaved
     ([700, 300], None, 40, 10, 2, 256, 256, FP16, False, 256, True),
     ([9, 3], None, 12, 4, 4, 64, 16, BF16, False, 0, False),          # more tokens than positions, nothing rotated
     ([70000], [4], 4, 3, 3, 128, 65536, BF16, False, 96, False),
+    ([2000, 0, 900, 1300], [900, 0, 1, 877], 900, 8, 1, 64, 16, BF16, False, 64, False),   # many tokens of few heads, some dead
+    ([1500, 1300], None, 1300, 2, 1, 128, 32, FP16, True, 50, True),
+    ([1299, 1300, 5], None, 1300, 1, 1, 64, 16, BF16, False, 0, False),
+    ([1299, 1300, 5], None, 1300, 2, 2, 64, 16, BF16, True, 20, False),
 ]
 
 
@@ -605,6 +631,20 @@ def test_append_to_bad_pages_and_lengths(dev):
         g.gqa_paged_append(None, k, k, None, c.k, c.v, c.table, c.ln)
         assert g.gqa_decode_get_error() == g.GQA_ERR_BAD_INDEX
         assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v)
+    # many tokens of few heads, of which those of one page are lost
+    c = Case(dev, [2000, 1500], None, 1400, 4, 2, 64, 16, seed=4)
+    many = _randn(dev, 2, 1400, 2, 64, seed=8)
+    lost = int(c.table[0, 60])
+    c.table[0, 60] = -5                                              # positions 960 to 975
+    want_k, want_v = c.k.clone(), c.v.clone()
+    for b, L in enumerate(c.lens):
+        there = [j for j in range(L - 1400, L) if b == 1 or not 960 <= j < 976]
+        at, off = c.table[b].long()[torch.tensor(there, device=dev) // 16], torch.tensor(there, device=dev) % 16
+        new = torch.tensor(there, device=dev) - (L - 1400)
+        want_k[at, off] = want_v[at, off] = many[b, new]
+    g.gqa_paged_append(None, many, many, None, c.k, c.v, c.table, c.ln)
+    assert g.gqa_decode_get_error() == g.GQA_ERR_BAD_INDEX
+    assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v) and lost >= 0
     c = Case(dev, [48, 0], None, 20, 4, 2, 64, 16, seed=4)
     before = c.k.clone()
     g.gqa_paged_append(None, k, k, None, c.k, c.v, c.table, _ints(dev, [999, -5]))
