@@ -44,8 +44,8 @@
 // tokens of 32 heads against 8192 keys, 4 of them, run at 1.4 PFLOP/s (769-794
 // us, by box; 871 a call in a loop long enough for the card's power limit, which
 // takes the clock from 2070 to ~1650 MHz).  At head_dim 256 the one tile takes its K and V, 64 bytes a
-// clock, from L2, which gives ~50: a block takes ~2600 cycles, 333 tokens of 16
-// heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
+// clock, from L2, which gives ~37: a block takes ~3900 cycles, and 3500 of them with
+// nothing but its loads; 333 tokens of 16 heads against 5001 keys, 2 of them, 50 us.  Where a section's rows are
 // few, a block costs what its chain takes (~1900 cycles, split between two
 // tiles) and an item ~4600 more: its QK, softmax, PV and epilogue follow one
 // another, with little to run under them.  A CTA starts its first K load after
@@ -212,6 +212,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr uint32_t OCOL = THREE ? 3 * kBlockN : Cfg::kOCol;
   static_assert(OCOL + NT * HEAD_DIM <= Cfg::kTmemCols, "TMEM column plan");
   constexpr bool HALVES = TPB == 1 && !THREE;  // P is handed over in two halves
+  // head_dim 256 over pages: a half block is given back when its own MMAs are done, not
+  // with the block's others (trees of 40 tokens, three tiles that share K and V, 1.98
+  // and 1.86 us a block; a tile alone, at HBM rate, 2.68 and 2.64)
+  constexpr bool BY_HALF = PAGED && TPB == 2;
   constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1, kPlanWarp = kProducerWarp + 2;
 
   extern __shared__ uint8_t smem_raw[];
@@ -493,9 +497,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
               ptx::mma_f16_ss_elect(leader, tmem_base + slot * kBlockN, qd + (k >> 2) * 1024 + (k & 3) * 2, q_hi,
                                     kd + (kk >> 2) * 1024 + (kk & 3) * 2, k_hi, idesc_qk, k > 0 ? 1u : 0u);
             }
+            if (BY_HALF) ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>(stage)));
           }
           ptx::mma_commit_elect(leader, BAR(S_FULL + set_of(j)));
-          if (!two || tile == 1u) {  // the block's last use
+          if (!BY_HALF && (!two || tile == 1u)) {  // the block's last use
 #pragma unroll
             for (int hf = 0; hf < TPB; ++hf)
               ptx::mma_commit_elect(leader, BAR(K_EMPTY + static_cast<int>((blk * TPB + hf) % NSK)));
@@ -530,11 +535,12 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
               for (int kk = part * (KK / PARTS); kk < (part + 1) * (KK / PARTS); ++kk)
                 ptx::mma_f16_ts_elect(leader, o_tmem + hf * Cfg::kTileDim, tmem_base + slot * kBlockN + kk * 8,
                                       vd + kk * (2048 >> 4), v_hi, idesc_pv, (kk > 0 || !first) ? 1u : 0u);
+              if (BY_HALF) ptx::mma_commit_elect(leader, BAR(V_EMPTY + static_cast<int>(stage)));
             }
           }
           if constexpr (!THREE) ++g[slot];
           ptx::mma_commit_elect(leader, BAR(O_FULL + set));
-          if (!two || tile == 1u) {
+          if (!BY_HALF && (!two || tile == 1u)) {
 #pragma unroll
             for (int hf = 0; hf < TPB; ++hf)
               ptx::mma_commit_elect(leader, BAR(V_EMPTY + static_cast<int>((blk * TPB + hf) % NSV)));

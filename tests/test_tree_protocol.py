@@ -3,7 +3,9 @@
 What differs from test_rows_protocol, whose checks these are: at head_dim 64 three
 S slots that the steps take in turn, with two QKs ahead of the PV at hand and the
 barriers of a tile's steps three in turn; at head_dim 128, where the rows fit one
-tile, one tile with two S slots, two Q slots and three stages of V.
+tile, one tile with two S slots, two Q slots and three stages of V; at head_dim 256
+halves of K's and V's blocks given back each after its own MMAs.  There the block that
+ends inside is any one of an item's, as items may take their blocks from the middle on.
 """
 import random
 from collections import namedtuple
@@ -19,7 +21,8 @@ FORMS = {64: Form(Shape(2, 1, 4, 4), 2, True), 128: Form(Shape(1, 1, 2, 3), 2, F
 class Paged(Cta):
     def __init__(self, form, items, rng, give_up_at=None, mistake=None):
         super().__init__(form.shape, items, rng, give_up_at, mistake)
-        self.nq, self.three = form.nq, form.three
+        self.nq, self.three, self.by_half = form.nq, form.three, form.shape.tpb == 2
+        self.tails = [rng.randrange(it.n) if it.n and it.tail else -1 for it in items]
         self.turn = 2 if mistake == "two barriers in turn" else 3
         self.o_turn = 1 if mistake == "one barrier for O" else self.turn
         self.q_full, self.q_empty = [Bar() for _ in range(self.nq)], [Bar() for _ in range(self.nq)]
@@ -30,6 +33,12 @@ class Paged(Cta):
             self.s_full, self.o_full = [Bar() for _ in range(n)], [Bar() for _ in range(self.o_turn * self.nt)]
             self.p_half, self.p_full = [Bar(WARPS) for _ in range(n)], [Bar(WARPS) for _ in range(n)]
             self.scores = [dict(unread=0, p_pending=False) for _ in range(3)]
+
+    def reads(self, kind, slot, content):
+        st = self.stage[kind][slot]
+        if self.by_half and kind == "V":  # (the base has it that the last block ends inside)
+            st["zeroed"] = content[1] != self.tails[content[0]] or st.get("zeros") == WARPS
+        return super().reads(kind, slot, content)
 
     def producer(self):
         sh, t = self.shape, dict(K=0, V=0, Q=0)
@@ -100,10 +109,22 @@ class Paged(Cta):
                 def set_of(j):
                     return self.turn * tile_of(j) + count_of(j) % self.turn if three else slot_of(j)
 
+                def halves(kind, full, empty, ns, i, last):
+                    """The MMAs of a block's halves; `last` goes with the second's."""
+                    for hf in range(sh.tpb):
+                        m = (u + i) * sh.tpb + hf
+                        yield from self.wait(full[m % ns], m // ns, f"issuer {kind}")
+                        st = self.reads(kind, m % ns, (n, i, hf))
+                        self.mma.append(("read", [st] + (last if hf + 1 == sh.tpb else [])))
+                        if self.mistake == "given back by the warp" and kind == "V":
+                            empty[m % ns].arrive()
+                        else:
+                            self.mma.append(("arrive", empty[m % ns]))
+
                 def qk(j):
                     slot, tile, i = slot_of(j), tile_of(j), j >> 1 if two else j
                     read = []
-                    for hf in range(sh.tpb):
+                    for hf in range(0 if self.by_half else sh.tpb):
                         m = (u + i) * sh.tpb + hf
                         if not two or tile == 0:
                             yield from self.wait(self.k_full[m % sh.nsk], m // sh.nsk, "issuer K")
@@ -113,9 +134,12 @@ class Paged(Cta):
                     if s["unread"] or s["p_pending"]:
                         raise Violation("scores overwritten before they were used")
                     s.update(unread=WARPS, p_pending=True)
-                    self.mma.append(("read", read + [q]))
+                    if self.by_half:
+                        yield from halves("K", self.k_full, self.k_empty, sh.nsk, i, [q])
+                    else:
+                        self.mma.append(("read", read + [q]))
                     self.mma.append(("arrive", self.s_full[set_of(j)]))
-                    if not two or tile == 1:
+                    if not self.by_half and (not two or tile == 1):
                         for hf in range(sh.tpb):
                             self.mma.append(("arrive", self.k_empty[((u + i) * sh.tpb + hf) % sh.nsk]))
                     if j + 1 == steps:
@@ -133,10 +157,8 @@ class Paged(Cta):
                     for part in range(2 if self.halves else 1):
                         half = self.halves and part == 0
                         yield from self.wait((self.p_half if half else self.p_full)[the_set], phase, "issuer P")
-                        for hf in range(sh.tpb):
+                        for hf in range(0 if self.by_half else sh.tpb):
                             m = (u + i) * sh.tpb + hf
-                            if sh.tpb > 1:
-                                yield from self.wait(self.v_full[m % sh.nsv], m // sh.nsv, "issuer V")
                             read.append(self.reads("V", m % sh.nsv, (n, i, hf)))
                         o = self.o[tile]
                         if first and part == 0:
@@ -151,11 +173,14 @@ class Paged(Cta):
                         g[slot] += 1
                     self.scores[slot]["p_pending"] = False
                     self.pv_done += 1
-                    self.mma.append(("read", read))
+                    if self.by_half:
+                        yield from halves("V", self.v_full, self.v_empty, sh.nsv, i, [])
+                    else:
+                        self.mma.append(("read", read))
                     self.mma.append(("pv", tile))
                     o_set = self.o_turn * tile + count_of(j) % self.o_turn if three else slot
                     self.mma.append(("arrive", self.o_full[o_set]))
-                    if not two or tile == 1:
+                    if not self.by_half and (not two or tile == 1):
                         for hf in range(sh.tpb):
                             self.mma.append(("arrive", self.v_empty[((u + i) * sh.tpb + hf) % sh.nsv]))
 
@@ -203,8 +228,8 @@ class Paged(Cta):
                     slot = (us0 + (2 * i + t if two else i)) % 3 if three else g & 1
                     the_set = self.turn * t + g % self.turn if three else slot
                     yield from self.wait(self.s_full[the_set], g // self.turn if three else g >> 1, "softmax S")
-                    if i == it.n - 1 and it.tail and (t == 0 or split):
-                        if nt == 1 and g >= 1:
+                    if (i == self.tails[n - 1] if self.by_half else i == it.n - 1 and it.tail) and (t == 0 or split):
+                        if nt == 1 and g >= 1 and self.mistake != "zeros without waiting for the block before":
                             yield from wait_pv(g - 1, "softmax zeros")
                         for hf in range(sh.tpb):
                             m = (u0 + i) * sh.tpb + hf
@@ -270,13 +295,15 @@ def test_waits_take_no_longer_than_the_items_in_the_ring():
         assert cta.longest_wait <= RING * 30 + 6
 
 
-@pytest.mark.parametrize("mistake,found", [("two barriers in turn", "softmax S"), ("one barrier for O", "softmax")])
-def test_the_model_finds_mistakes(mistake, found):
+@pytest.mark.parametrize("d,mistake,found", [
+    (64, "two barriers in turn", "softmax S"), (64, "one barrier for O", "softmax"),
+    (256, "given back by the warp", "while in use"), (256, "zeros without waiting for the block before", "softmax V")])
+def test_the_model_finds_mistakes(d, mistake, found):
     rng = random.Random(7)
     seen = set()
     for _ in range(400):
         try:
-            Paged(FORMS[64], _items(rng, 2), rng, mistake=mistake).run()
+            Paged(FORMS[d], _items(rng, FORMS[d].shape.nt), rng, mistake=mistake).run()
         except Violation as e:
             seen.add(str(e))
     assert any(found in s for s in seen), seen
