@@ -305,6 +305,7 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
   m.G = G;
   m.kv_heads = r.kv_heads;
   m.tiles = r.tiles;
+  m.paged = paged != nullptr ? 1 : 0;
   // Of a paged call's few rows each gets a CTA (below), of more each a place among
   // its tile's.
   if (paged != nullptr && (!r.every_piece || rows > kMergeSharedRows)) {
@@ -315,7 +316,7 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
                                         : reinterpret_cast<const void*>(&gqa_tile_merge_kernel<256, false>))
                                  : (cut ? reinterpret_cast<const void*>(&gqa_tile_merge_kernel<128, true>)
                                         : reinterpret_cast<const void*>(&gqa_tile_merge_kernel<128, false>));
-    const int per_cta = kTileMergeThreads / 32 * (hd == 256 ? kTileMergeRows<256> : kTileMergeRows<128>);
+    const int per_cta = kTileMergeThreads / 32 * kTileMergeRows;
     const int per_triple = (m.s[0].split_keys ? 1 : m.tiles) * m.s[0].tokens * G;
     return launch_kernel(fn, dim3(static_cast<unsigned>(cut ? r.plan.num_ctas : r.s[0].triples),
                                   (per_triple + per_cta - 1) / per_cta), kTileMergeThreads, 0, &m, stream);

@@ -44,6 +44,7 @@ struct RowsMergeParams {
   int out_dtype;
   int batch, nq, Hq, G, kv_heads;
   int tiles;           // row tiles of a triple
+  int paged;           // a tile's partial rows lie 8 elements of all of them after another
 };
 
 namespace detail {
@@ -78,12 +79,11 @@ struct RowSum {
 };
 
 // Pieces first, first + step, ... of n (piece j begins at partial row at(j)) into R consecutive rows' sums, NB of
-// them in flight.
+// them in flight.  This lane's elements are `in_row` past a row's beginning.
 template <int HEAD_DIM, int R, int NB, typename At>
 __device__ __forceinline__ void add_pieces(RowSum<HEAD_DIM / 32> (&sum)[R], const RowsMergeParams& p, const At& at,
-                                           int n, int first, int step) {
+                                           int n, int first, int step, int in_row) {
   constexpr int VEC = HEAD_DIM / 32;
-  const int lane = threadIdx.x & 31;
   for (int j0 = first; j0 < n; j0 += NB * step) {
     float2 ml[NB][R];
     float v[NB][R][VEC];
@@ -94,7 +94,7 @@ __device__ __forceinline__ void add_pieces(RowSum<HEAD_DIM / 32> (&sum)[R], cons
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         ml[q][r] = p.ml_part[row + r];
-        load_vec<VEC>(p.o_part + (row + r) * HEAD_DIM + lane * VEC, v[q][r]);
+        load_vec<VEC>(p.o_part + (row + r) * HEAD_DIM + in_row, v[q][r]);
       }
     }
 #pragma unroll
@@ -104,6 +104,16 @@ __device__ __forceinline__ void add_pieces(RowSum<HEAD_DIM / 32> (&sum)[R], cons
       for (int r = 0; r < R; ++r) sum[r].add(ml[q][r], v[q][r]);
     }
   }
+}
+
+// Two elements of a 16-bit output.
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi, int out_dtype) {
+  if (out_dtype == kOutF16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <int HEAD_DIM>
@@ -129,15 +139,7 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
   } else {
     uint32_t w[VEC / 2];
 #pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      if (out_dtype == kOutF16) {
-        const __half2 h = __floats2half2_rn(acc[2 * i], acc[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
+    for (int i = 0; i < VEC / 2; ++i) w[i] = pack_out(acc[2 * i], acc[2 * i + 1], out_dtype);
     uint16_t* dst = static_cast<uint16_t*>(out) + row * HEAD_DIM + lane * VEC;
     if constexpr (VEC == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
@@ -180,7 +182,8 @@ gqa_rows_merge_kernel(const RowsMergeParams p) {
   detail::RowSum<HEAD_DIM / 32> sum[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) sum[r].clear();
-  detail::add_pieces<HEAD_DIM, R, 2>(sum, p, [&](int j) { return run.at(j); }, run.n, 0, 1);
+  detail::add_pieces<HEAD_DIM, R, 2>(sum, p, [&](int j) { return run.at(j); }, run.n, 0, 1,
+                                     static_cast<int>(threadIdx.x & 31) * (HEAD_DIM / 32));
   const int per_batch = p.kv_heads * s.groups;
   const int b = rec.x / per_batch, hg = rec.x - b * per_batch;
   const int h = hg / s.groups, grp = hg - h * s.groups;
@@ -214,6 +217,7 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
   const uint32_t bt = row / static_cast<uint32_t>(p.Hq);  // b * nq + t
   const int hq = static_cast<int>(row - bt * static_cast<uint32_t>(p.Hq)), h = hq / p.G;
   detail::PieceRun run[2];
+  int in_row = lane * VEC;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     run[i].n = 0;
@@ -231,12 +235,14 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
     run[i].next = run[i].first + run[i].stride;
     const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
     run[i].n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
+    if (p.paged != 0 && i == 0)
+      in_row = (in_row / 8 * static_cast<int>(tile_rows) + r) * 8 + in_row % 8 - r * HEAD_DIM;
   }
   detail::RowSum<VEC> sum[1];
   sum[0].clear();
   const int n0 = run[0].n;
   detail::add_pieces<HEAD_DIM, 1, NB>(sum, p, [&](int j) { return j < n0 ? run[0].at(j) : run[1].at(j - n0); },
-                                      n0 + run[1].n, WARPS > 1 ? warp : 0, WARPS);
+                                      n0 + run[1].n, WARPS > 1 ? warp : 0, WARPS, in_row);
   if constexpr (WARPS > 1) {
     __shared__ float s_acc[WARPS][HEAD_DIM], s_m[WARPS], s_w[WARPS];
 #pragma unroll
@@ -264,22 +270,21 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
   detail::write_row<HEAD_DIM>(sum[0], p.out, p.lse, p.out_dtype, row);
 }
 
-// The rows of a launch of one section whose triples hold many, a triple to
-// blockIdx.x (CUT: the cut triple, if any, that begins in that CTA of the launch)
-// and a group of its rows to blockIdx.y.  A warp takes R rows, whose pieces are the
-// same number of the same places, and has R x kBatch of them in flight: the two
-// kernels above have as many for one row or two, wait as long for each, and take
-// as many more waves of CTAs (whole calls over pages, us: 16 x 8 tiles of 104 rows of
-// 128 elements 63.7, not 65.6; 32 x 8 of 64 rows 41.8, not 43.7; 48 of 128 rows of 256
-// elements 58.9, not 60.3).
-constexpr int kTileMergeThreads = 128;
-template <int HEAD_DIM>
-constexpr int kTileMergeRows = HEAD_DIM == 256 ? 2 : 4;
+// The rows of a paged launch whose triples hold many, a triple to blockIdx.x
+// (CUT: the cut triple, if any, that begins in that CTA of the launch) and a group
+// of its rows to blockIdx.y.  A warp takes four rows, which lie side by side in
+// each piece: a lane has 8 elements at a time of one of them, and four lanes a line.
+// What the kernels above have in flight for a row or two is here for four, and a row's
+// weights are computed by 8 lanes, not 32 (whole calls over pages, us, of those kernels
+// and, rows lying one after another, of this one: 16 x 8 tiles of 104 rows of 128
+// elements 65.6, 63.7; 32 x 8 of 64 rows 43.7, 41.8; 48 of 128 rows of 256 elements
+// 60.3, 58.9).
+constexpr int kTileMergeThreads = 128, kTileMergeRows = 4;
 
 template <int HEAD_DIM, bool CUT>
 __global__ void __launch_bounds__(kTileMergeThreads)
 gqa_tile_merge_kernel(const RowsMergeParams p) {
-  constexpr int VEC = HEAD_DIM / 32, R = kTileMergeRows<HEAD_DIM>, kBatch = 2;
+  constexpr int UNITS = HEAD_DIM / 64, VEC = 8 * UNITS, kBatch = 2;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const RowsMergeSection& s = p.s[0];
@@ -288,61 +293,78 @@ gqa_tile_merge_kernel(const RowsMergeParams p) {
   const int tile_rows = s.tokens * p.G, own_tiles = s.split_keys ? 1 : p.tiles;  // tiles with rows of their own
   const long long piece_rows = static_cast<long long>(p.tiles) * tile_rows;
   int triple = static_cast<int>(blockIdx.x), n = 0;
-  long long first, next, stride;
+  detail::PieceRun run;
   if constexpr (CUT) {
     triple = rec.x;
     if (rec.x < 0 || rec.y <= 0 || 2 * (static_cast<int>(blockIdx.x) + rec.y) > s.pieces) return;
     n = rec.y;
-    first = (2ll * blockIdx.x + 1) * piece_rows;
-    next = 2ll * (blockIdx.x + 1) * piece_rows;
-    stride = 2ll * piece_rows;
+    run.first = (2ll * blockIdx.x + 1) * piece_rows;
+    run.next = 2ll * (blockIdx.x + 1) * piece_rows;
+    run.stride = 2ll * piece_rows;
   } else {
     const bool there = rec.x >= 0 && rec.y > 0 && rec.x <= s.pieces - rec.y;
     n = !there ? 0 : s.split_keys ? rec.y * p.tiles : rec.y;
-    first = s.part_row + rec.x * piece_rows;
-    stride = s.split_keys ? tile_rows : piece_rows;
-    next = first + stride;
+    run.first = s.part_row + rec.x * piece_rows;
+    run.stride = s.split_keys ? tile_rows : piece_rows;
+    run.next = run.first + run.stride;
   }
   const int rows = own_tiles * tile_rows;
-  const int i0 = (static_cast<int>(blockIdx.y) * (kTileMergeThreads / 32) + static_cast<int>(threadIdx.x >> 5)) * R;
+  const int i0 = (static_cast<int>(blockIdx.y) * (kTileMergeThreads / 32) + static_cast<int>(threadIdx.x >> 5)) *
+                 kTileMergeRows;
   if (i0 >= rows) return;
-  const int i = i0 + R <= rows ? i0 : (rows >= R ? rows - R : 0);  // (past the last row: the last again)
-  detail::RowSum<VEC> sum[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) sum[r].clear();
+  const int i = min(i0 + (lane & 3), rows - 1);  // (past the last row: the last again)
+  const int t = i / tile_rows, in_tile = i - t * tile_rows, unit0 = lane >> 2;
+  const float* o = p.o_part + static_cast<long long>(t) * tile_rows * HEAD_DIM + (unit0 * tile_rows + in_tile) * 8;
+  detail::RowSum<VEC> sum;
+  sum.clear();
   for (int j0 = 0; j0 < n; j0 += kBatch) {
-    float2 ml[kBatch][R];
-    float v[kBatch][R][VEC];
+    float2 ml[kBatch];
+    float v[kBatch][VEC];
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       if (j0 + q >= n) break;
-      const long long at = (j0 + q == 0 ? first : next + (j0 + q - 1) * stride) + i;
+      const long long at = run.at(j0 + q);
+      ml[q] = p.ml_part[at + i];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const long long row = at + (i + r < rows ? r : 0);
-        ml[q][r] = p.ml_part[row];
-        detail::load_vec<VEC>(p.o_part + row * HEAD_DIM + lane * VEC, v[q][r]);
+      for (int k = 0; k < UNITS; ++k) {
+        float x[8];
+        detail::load_vec<8>(o + at * HEAD_DIM + k * 64 * tile_rows, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[q][8 * k + e] = x[e];
       }
     }
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       if (j0 + q >= n) break;
-#pragma unroll
-      for (int r = 0; r < R; ++r) sum[r].add(ml[q][r], v[q][r]);
+      sum.add(ml[q], v[q]);
     }
   }
   const int per_batch = p.kv_heads * s.groups;
   const int b = triple / per_batch, hg = triple - b * per_batch;
   const int h = hg / s.groups, grp = hg - h * s.groups;
+  const int r_tok = in_tile / p.G, tok = (grp * own_tiles + t) * s.tokens + r_tok;
+  if (tok >= s.nq) return;
+  const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + (in_tile - r_tok * p.G);
+  const bool none = sum.W == 0.f;
+  const float inv = none ? 0.f : 1.0f / sum.W;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (i + r >= rows) break;
-    const int t = (i + r) / tile_rows, in_tile = i + r - t * tile_rows;
-    const int tok = (grp * own_tiles + t) * s.tokens + in_tile / p.G;
-    if (tok >= s.nq) continue;
-    const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + in_tile % p.G;
-    detail::write_row<HEAD_DIM>(sum[r], p.out, p.lse, p.out_dtype, row);
+  for (int k = 0; k < UNITS; ++k) {
+    const long long to = row * HEAD_DIM + (unit0 + 8 * k) * 8;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = none ? 0.f : sum.acc[8 * k + e] * inv;
+    if (p.out_dtype == kOutF32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
+      dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+      dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = detail::pack_out(y[2 * e], y[2 * e + 1], p.out_dtype);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
+  if (unit0 == 0 && p.lse != nullptr) p.lse[row] = none ? -INFINITY : 0.69314718055994531f * (sum.M + __log2f(sum.W));
 }
 
 }  // namespace gqa
