@@ -90,13 +90,16 @@ __device__ __forceinline__ void prefetch_table(const PagedKeys& k, int entries, 
   if (line < lines) ptx::prefetch_l2(k.table + line * 32);
 }
 
-// New tokens of entry b, which has L positions: at most nq, and at most L.
-__device__ __forceinline__ int live_tokens(const PagedKeys& k, unsigned int* err_word, int b, int L, int nq) {
+// New tokens of entry b as given (loaded together with its length, ahead of
+// what may flag either: a load does not move past an atomic).
+__device__ __forceinline__ int asked_tokens(const PagedKeys& k, int b, int nq) {
+  return k.news == nullptr ? nq : k.news[b];
+}
+// Those there are of an entry that has L positions: at most nq, and at most L.
+__device__ __forceinline__ int live_tokens(int asked, unsigned int* err_word, int L, int nq) {
   const int most = L < nq ? L : nq;
-  if (k.news == nullptr) return most;
-  const int n = k.news[b];
-  if (n < 0 || n > nq) atomicOr(err_word, kErrBadIndex);
-  return n < 0 ? 0 : (n > most ? most : n);
+  if (asked < 0 || asked > nq) atomicOr(err_word, kErrBadIndex);
+  return asked < 0 ? 0 : (asked > most ? most : asked);
 }
 
 // Bits [0, n) of 32 (n of any sign).

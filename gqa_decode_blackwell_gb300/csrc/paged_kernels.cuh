@@ -332,9 +332,11 @@ gqa_append_kernel(const RotaryParams p) {
     if (m.here) {
       const int e = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(p.nq));
       const int t = static_cast<int>(token) - e * p.nq;
-      const int raw = p.seqlens[e], L = clamp_len(raw, p.max_seqlen);
+      const int raw = p.seqlens[e], asked = detail::asked_tokens(p.pages, e, p.nq);
+      const int given = p.positions != nullptr ? p.positions[token] : 0;
+      const int L = clamp_len(raw, p.max_seqlen);
       if (raw != L && t == 0 && m.unit == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadSeqlen));
-      const int n = detail::live_tokens(p.pages, p.err_word, e, L, p.nq);
+      const int n = detail::live_tokens(asked, p.err_word, L, p.nq);
       there = t < n;
       place = L - n + t;
       if (there) {
@@ -345,7 +347,7 @@ gqa_append_kernel(const RotaryParams p) {
         b.load(from + at.y);
         page = p.pages.table[static_cast<long long>(e) * p.pages.cols + (place >> p.pages.page_shift)];
       }
-      if (m.unit == 0) positions[m.sub] = p.positions != nullptr && there ? p.positions[token] : place;
+      if (m.unit == 0) positions[m.sub] = p.positions != nullptr ? given : place;
     }
     __syncthreads();
     for (int j = static_cast<int>(threadIdx.x); j < m.count * p.pairs; j += kGroupThreads) {
@@ -377,12 +379,14 @@ gqa_append_kernel(const RotaryParams p) {
   const int b = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.nq));
   const int t = static_cast<int>(blockIdx.x) - b * p.nq;
   const uint64_t turns = tid < p.pairs ? p.turns[tid] : 0;
-  const int raw = p.seqlens[b], L = clamp_len(raw, p.max_seqlen);
+  const int raw = p.seqlens[b], asked = detail::asked_tokens(p.pages, b, p.nq);
+  const int given = p.positions != nullptr ? p.positions[token] : 0;
+  const int L = clamp_len(raw, p.max_seqlen);
   if (raw != L && t == 0 && tid == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadSeqlen));
-  const int n = detail::live_tokens(p.pages, p.err_word, b, L, p.nq);
+  const int n = detail::live_tokens(asked, p.err_word, L, p.nq);
   if (t >= n) return;
   const int place = L - n + t;
-  const int position = p.positions != nullptr ? p.positions[token] : place;
+  const int position = p.positions != nullptr ? given : place;
   const int page = p.pages.table[static_cast<long long>(b) * p.pages.cols + (place >> p.pages.page_shift)];
   const T* q = static_cast<const T*>(p.x.src) + token * p.x.src_stride;
   const T* k = static_cast<const T*>(p.k.src) + token * p.k.src_stride;
@@ -441,18 +445,16 @@ gqa_tree_kernel(const TreeParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int b = static_cast<int>(blockIdx.x), t = static_cast<int>(threadIdx.x);
-  const int raw = p.seqlens[b], L = clamp_len(raw, p.max_seqlen);
-  if (raw != L && t == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadSeqlen));
   PagedKeys k;
   k.news = p.news;
-  const int n = detail::live_tokens(k, p.err_word, b, L, p.nq);
-  int above = -1;
-  if (t < n) {
-    above = p.parents[static_cast<long long>(b) * p.nq + t];
-    if (above < -1 || above >= t) {
-      atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
-      above = -1;
-    }
+  const int raw = p.seqlens[b], asked = detail::asked_tokens(k, b, p.nq), L = clamp_len(raw, p.max_seqlen);
+  int above = t < p.nq ? p.parents[static_cast<long long>(b) * p.nq + t] : -1;
+  if (raw != L && t == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadSeqlen));
+  const int n = detail::live_tokens(asked, p.err_word, L, p.nq);
+  if (t >= n) above = -1;
+  if (above < -1 || above >= t) {
+    atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
+    above = -1;
   }
   uint32_t own[kMaxTreeWords];
 #pragma unroll
@@ -501,25 +503,43 @@ struct KeepParams {
 // for all of the branch.  Token path[i] moves to place i <= path[i], and the
 // tokens of a branch ascend, so nothing is overwritten that this thread or a later
 // batch of it still reads: a batch of rows is loaded whole, then stored.
+//
+// What bounds it is a chain of loads, so a token's are looked up by a thread of its
+// own, as soon as they can be: lengths and path, then the pages of a token and of its
+// place, then the rows.
 __global__ void __launch_bounds__(kKeepThreads)
 gqa_keep_kernel(const KeepParams p) {
   constexpr int kBatch = 8;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int b = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
-  const int raw = p.seqlens[b], L = clamp_len(raw, p.max_seqlen);
+  const int32_t* path = p.path + static_cast<long long>(b) * p.max_keep;
+  const int raw = p.seqlens[b], given = detail::asked_tokens(p.pages, b, p.nq), asked = p.keep_lens[b];
+  int at = -1, before = -1;  // of token tid of the branch, to begin with
+  auto load = [&](int i) {
+    at = i < p.max_keep ? path[i] : -1;
+    before = i > 0 && i < p.max_keep ? path[i - 1] : -1;
+  };
+  load(tid);
+  const int L = clamp_len(raw, p.max_seqlen);
   if (raw != L && tid == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadSeqlen));
-  const int n = detail::live_tokens(p.pages, p.err_word, b, L, p.nq), first = L - n;
-  const int asked = p.keep_lens[b];
+  const int n = detail::live_tokens(given, p.err_word, L, p.nq), first = L - n;
   const int most = asked < 0 ? 0 : (asked > p.max_keep ? p.max_keep : asked);
   if (asked != most && tid == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
-  const int32_t* path = p.path + static_cast<long long>(b) * p.max_keep;
-  // tokens of the branch that are in range and ascend
-  __shared__ int s_bad;
+  // the page of the token at `at`, and of place i (a token in range is not before its place)
+  const int32_t* table = p.pages.table + static_cast<long long>(b) * p.pages.cols;
+  int from = 0, to = 0;
+  auto look_up = [&](int i) {
+    if (i >= most || at < i || at >= n) return;
+    from = table[(first + at) >> p.pages.page_shift];
+    to = table[(first + i) >> p.pages.page_shift];
+  };
+  look_up(tid);
+  __shared__ int s_bad;  // the first token of the branch that is out of range or does not ascend
   if (tid == 0) s_bad = most;
   __syncthreads();
   for (int i = tid; i < most; i += kKeepThreads) {
-    const int at = path[i], before = i > 0 ? path[i - 1] : -1;
+    if (i != tid) load(i);
     if (at <= before || at >= n || at < 0) atomicMin(&s_bad, i);
   }
   __syncthreads();
@@ -528,32 +548,42 @@ gqa_keep_kernel(const KeepParams p) {
     if (keep != most) atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
     if (p.seqlens_out != nullptr) p.seqlens_out[b] = first + keep;
   }
+  __shared__ long long s_from[kKeepThreads], s_to[kKeepThreads];  // below 0: it stays, or is lost
   const int per_head = p.head_dim / 8, per_cache = p.kv_heads * per_head;
-  for (int c = tid; c < 2 * per_cache; c += kKeepThreads) {
-    const int in = c < per_cache ? c : c - per_cache, head = in / per_head;
-    uint16_t* base = static_cast<uint16_t*>(c < per_cache ? p.k_cache : p.v_cache) + head * p.head_stride +
-                     (in - head * per_head) * 8;
-    for (int i0 = 0; i0 < keep; i0 += kBatch) {
-      uint4 row[kBatch];
-      uint16_t* to[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        to[j] = nullptr;
-        const int i = i0 + j;
-        if (i >= keep) continue;
-        const int at = path[i];
-        if (at == i) continue;  // in its place
-        const int from_page = detail::page_of(p.pages, p.err_word, b, first + at);
-        const int to_page = detail::page_of(p.pages, p.err_word, b, first + i);
-        if (from_page >= p.pages.num_pages || to_page >= p.pages.num_pages) continue;
-        row[j] = *reinterpret_cast<const uint4*>(base + from_page * p.page_stride +
-                                                 ((first + at) & p.pages.page_mask) * p.pos_stride);
-        to[j] = base + to_page * p.page_stride + ((first + i) & p.pages.page_mask) * p.pos_stride;
+  for (int base = 0; base < keep; base += kKeepThreads) {
+    const int here = min(keep - base, kKeepThreads), i = base + tid;
+    if (i < keep) {
+      if (most > kKeepThreads) {
+        load(i);
+        look_up(i);
       }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (to[j] != nullptr) *reinterpret_cast<uint4*>(to[j]) = row[j];
+      s_from[tid] = -1;
+      if (at != i) {
+        const unsigned pages = static_cast<unsigned>(p.pages.num_pages);
+        if (static_cast<unsigned>(from) < pages && static_cast<unsigned>(to) < pages) {
+          s_from[tid] = from * p.page_stride + ((first + at) & p.pages.page_mask) * p.pos_stride;
+          s_to[tid] = to * p.page_stride + ((first + i) & p.pages.page_mask) * p.pos_stride;
+        } else {
+          atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
+        }
+      }
     }
+    __syncthreads();
+    for (int c = tid; c < 2 * per_cache; c += kKeepThreads) {
+      const int in = c < per_cache ? c : c - per_cache, head = in / per_head;
+      uint16_t* cache = static_cast<uint16_t*>(c < per_cache ? p.k_cache : p.v_cache) + head * p.head_stride +
+                        (in - head * per_head) * 8;
+      for (int i0 = 0; i0 < here; i0 += kBatch) {
+        uint4 row[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (i0 + j < here && s_from[i0 + j] >= 0) row[j] = *reinterpret_cast<const uint4*>(cache + s_from[i0 + j]);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (i0 + j < here && s_from[i0 + j] >= 0) *reinterpret_cast<uint4*>(cache + s_to[i0 + j]) = row[j];
+      }
+    }
+    __syncthreads();
   }
 }
 

@@ -583,9 +583,22 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       detail::prefetch_table(p.pages, n_entries, p.plan.num_ctas, lane);
       ptx::griddep_wait();
       ptx::griddep_launch_dependents();
-      stage_lengths(lane, 32);
-      for (int i = lane; i < n_entries; i += 32)
-        s_live[i] = static_cast<uint16_t>(detail::live_tokens(p.pages, p.err_word, i, s_len[i], section(0).nq));
+      constexpr int kEach = kMaxLoneEntries / 32;
+      int raw[kEach], asked[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = lane + 32 * j;
+        raw[j] = i < n_entries ? section(0).lens[i] : 0;
+        asked[j] = i < n_entries ? detail::asked_tokens(p.pages, i, section(0).nq) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = lane + 32 * j, L = clamp_len(raw[j], plan_section(0).max_len);
+        if (i >= n_entries) break;
+        s_len[i] = L;
+        s_live[i] = static_cast<uint16_t>(detail::live_tokens(asked[j], p.err_word, L, section(0).nq));
+        if (raw[j] != L && blockIdx.x == 0) detail::set_error(p.err_word, kErrBadSeqlen, nullptr);
+      }
       __syncwarp();
       ptx::named_barrier_sync(1, Cfg::kThreads);
     }
@@ -636,7 +649,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           it.L = w.L;
           it.live = !PAGED     ? s.nq
                     : one_warp ? static_cast<int>(s_live[w.b])
-                               : detail::live_tokens(p.pages, p.err_word, w.b, w.L, s.nq);
+                               : detail::live_tokens(detail::asked_tokens(p.pages, w.b, s.nq), p.err_word, w.L, s.nq);
           // A group behind the entry's last token has nothing to do but to leave
           // its rows empty: without keys, whole, wherever it was cut.
           if (PAGED && it.tok0 >= it.live) it.blk_end = it.blk_begin;

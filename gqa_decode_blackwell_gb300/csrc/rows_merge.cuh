@@ -284,7 +284,10 @@ constexpr int kTileMergeThreads = 128, kTileMergeRows = 4;
 template <int HEAD_DIM, bool CUT>
 __global__ void __launch_bounds__(kTileMergeThreads)
 gqa_tile_merge_kernel(const RowsMergeParams p) {
-  constexpr int UNITS = HEAD_DIM / 64, VEC = 8 * UNITS, kBatch = 2;
+  constexpr int UNITS = HEAD_DIM / 64, VEC = 8 * UNITS;
+  // pieces in flight: 4 against 2, 16 trees of 26 tokens 56.4 and 57.1 us (128), 42.0 and
+  // 42.7 (64), but of cut triples, 60 tokens, 75.3 and 72.8 (128)
+  constexpr int kBatch = CUT || HEAD_DIM == 256 ? 2 : 4;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const RowsMergeSection& s = p.s[0];

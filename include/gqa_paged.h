@@ -123,7 +123,7 @@ gqa_status_t gqa_rotary_apply(const gqa_rotary_t* rope, const uint64_t* turns, c
  *   new_lens    int32 [B]: n_b in [0, nq] (clamped and flagged); NULL: nq.  At most
  *               L_b of them are there (an unused slot of a batch has L_b = 0)
  * Token t < n_b goes to position L_b - n_b + t; of tokens behind the last nothing
- * is read or written.  A token whose page is out of range is not put anywhere.
+ * is used or written.  A token whose page is out of range is not put anywhere.
  * All of q, q_out, k, v and the caches are 16-byte aligned.
  */
 gqa_status_t gqa_paged_append(const gqa_desc_t* desc, const gqa_pages_t* pages, const gqa_rotary_t* rope,
@@ -136,7 +136,7 @@ gqa_status_t gqa_paged_append(const gqa_desc_t* desc, const gqa_pages_t* pages, 
  * The tree of each sequence's drafted tokens, as gqa_tree_attn reads it.
  *   parents    int32 [batch, q_tokens]: the parent of token t, an earlier token or
  *              -1 for the last position before them (anything else is flagged and
- *              taken for -1); of tokens behind the last not read
+ *              taken for -1); of tokens behind the last anything
  *   seqlens, max_seqlen, new_lens  as in gqa_paged_append
  *   tree       uint32 [batch, q_tokens, ceil(q_tokens / 32)], written in full: bit
  *              j % 32 of word j / 32 of token t's row says that j is t or one of
