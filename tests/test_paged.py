@@ -16,6 +16,7 @@ in all less than 2^-21 m (|a| + |b|); and half a step of the output's type.
 """
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -890,6 +891,33 @@ def test_keep_moves_the_branch(dev, K, d, page, dtype, heads_first):
     g.gqa_paged_keep(c.k, c.v, c.table, c.ln, path.to(dev), keep, c.ln, tokens=T, new_lens=c.new)   # lengths in place
     assert torch.equal(c.k, want[0]) and torch.equal(c.ln, ends)
     assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
+def test_keep_moves_long_branches(dev):
+    """More tokens than a CTA has threads; one branch ends at a bad token far along, of one a page is lost."""
+    T, lens = 900, [2000, 900, 1500]
+    c = Case(dev, lens, None, T, 2, 2, 64, 16, seed=17)
+    paths = [sorted(random.Random(b).sample(range(T), n)) for b, n in enumerate((700, 257, 513))]
+    path = torch.zeros(3, 700, dtype=torch.int32)
+    for b, p in enumerate(paths):
+        path[b, : len(p)] = torch.tensor(p, dtype=torch.int32)
+    path[0, 600] = path[0, 599]                                      # not past the one before it
+    paths[0] = paths[0][:600]
+    c.table[2, 1400 // 16] = -3                                      # positions 1392 to 1407
+    want = [c.k.clone(), c.v.clone()]
+    for cache in want:
+        old = cache.clone()
+        for b, p in enumerate(paths):
+            first = lens[b] - T
+            for i, at in enumerate(p):
+                if b != 2 or not (1392 <= first + at < 1408 or 1392 <= first + i < 1408):
+                    cache[c.places(b, first + i, first + i + 1)] = old[c.places(b, first + at, first + at + 1)]
+    ends = torch.empty(3, dtype=torch.int32, device=dev)
+    g.gqa_paged_keep(c.k, c.v, c.table, c.ln, path.to(dev), _ints(dev, [700, 257, 513]), ends, tokens=T)
+    assert g.gqa_decode_get_error() == g.GQA_ERR_BAD_INDEX
+    assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+    assert ends.tolist() == [L - T + len(p) for L, p in zip(lens, paths)]
 
 
 @gpu
