@@ -43,6 +43,13 @@ constexpr int kSplitUnits = 7, kSplitItemUnits = 16;
 // 65.0 / 65.6 / 66.0 us, 16 tokens 45.7 / 44.3 / 44.0 / 43.8 / 44.4, 1 token 23.4 / 23.2 /
 // 23.5 / 23.6 / 24.8.
 constexpr int kLoneItemUnits = 12;
+// Output elements from which on a merge of all rows costs more than it saves: whole
+// triples then write their own.  Measured on GB300 over pages of 500 keys, us a call (all
+// partials, whole ones written), 32 / 8 heads: 64 rows of 128 16 sequences 15.3 and
+// 16.4, 38 (2.5M elements) 25.4 and 25.0, 76 41.4 and 38.9; 104 rows 10 sequences 14.8
+// and 16.5, 19 (2.0M) 19.7 and 19.4, 76 47.3 and 40.4; 32 rows 38 22.5 and 24.0; 120 rows
+// of 256 10 (2.5M) 24.3 both ways, 76 90.6 and 68.3; 4 rows of 256 76 58.9 and 60.9.
+constexpr long long kWholeElements = 1 << 21;
 // Up to this many rows a merge gives each a CTA, whose warps share its pieces;
 // beyond, a warp to a row.  Measured on GB300, a whole call: 384 rows of 256
 // 28.2 us (33.3 with a warp each), 1024 rows of 128 the same both ways, 2048
@@ -98,8 +105,11 @@ RowsLaunch make_launch(const gqa_desc_t* d0, const gqa_desc_t* d1, int sm, bool 
   const int tiles = d0->head_dim == 256 || lone ? 1 : 2;
   r.tiles = tiles;
   // Triples of rows that fit one tile all leave partials, and so do all triples
-  // of a prefix's launch.
-  r.every_piece = r.n == 2 || r.d[0].q_tokens <= most_tokens;
+  // of a prefix's launch.  But over pages, from kWholeElements on, those that one CTA
+  // holds write their rows themselves (of split keys none can).
+  const long long elements = static_cast<long long>(d0->batch) * d0->q_tokens * d0->q_heads * d0->head_dim;
+  const bool whole = paged && elements >= kWholeElements && !split_keys(*d0, tiles);
+  r.every_piece = r.n == 2 || (r.d[0].q_tokens <= most_tokens && !whole);
   long long entries = 0, units = 0;
   for (int i = 0; i < r.n; ++i) {
     const gqa_desc_t& d = r.d[i];

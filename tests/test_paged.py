@@ -678,6 +678,12 @@ TREE = [  # lens, news, T, H, K, d, page, dtype, out dtype, heads first
     ([(i * 97) % 400 for i in range(150)], [i % 20 for i in range(150)], 19, 8, 1, 256, 16, BF16, None, False),
     ([(i * 29) % 150 for i in range(4100)], None, 20, 2, 2, 64, 16, BF16, None, False),      # more entries than are staged
     ([(i * 29) % 150 for i in range(4100)], [(i * 7) % 70 for i in range(4100)], 70, 4, 1, 64, 32, FP16, None, False),
+    # enough rows of one tile for whole triples to write their own: some cut, some without keys
+    ([(i * 331) % 900 for i in range(60)], [i % 13 for i in range(60)], 12, 32, 8, 128, 16, BF16, None, False),
+    ([5000, 0] + [(i * 97) % 300 for i in range(60)], None, 16, 28, 4, 128, 32, FP16, FP32, True),
+    ([4000] + [(i * 331) % 700 for i in range(40)], [9] + [i % 10 for i in range(40)], 9, 24, 8, 256, 64, BF16, None, False),
+    ([(i * 53) % 400 for i in range(140)], [i % 21 for i in range(140)], 20, 8, 2, 128, 32, BF16, None, False),
+    ([(i * 29) % 40 for i in range(4100)], None, 2, 2, 1, 256, 16, FP16, None, False),
 ]
 
 
