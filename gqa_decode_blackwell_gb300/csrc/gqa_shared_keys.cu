@@ -252,7 +252,18 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
     s.causal = d.causal != 0 ? 1 : 0;
   }
   p.plan = r.plan;
-  if (paged != nullptr) p.pages = paged->keys;
+  if (paged != nullptr) {
+    // Small pages are bound by the warp that issues their boxes.  Measured on GB300, us
+    // a call of 16 sequences with 134 MB of keys and of values (one loader, two): one token,
+    // heads of 64, pages of 16 152 and 103, of 32 107 and 104 (heads first 107 and 89), of 64
+    // 98 and 99 (95 and 89), of 128 97 and 99 (90 and 88); 64 tokens, two tiles that their
+    // own work bounds, pages of 32 157 and 165.  (One tile, which has no warp to spare: heads
+    // of 128, pages of 16 91 and 87, but 16 trees of 26 tokens in pages of 32 56.5 and 57.6,
+    // with either number of loaders, for the warp alone.)
+    const int page = paged->geometry->page_size;
+    p.pages = paged->keys;
+    p.two_loaders = page == 16 || (r.head_dim == 64 && r.s[0].split_keys != 0 && page <= 64) ? 1 : 0;
+  }
   const RowsWs w = rows_ws(r);
   if (w.total > 0) {
     p.o_part = reinterpret_cast<float*>(ws);

@@ -17,8 +17,8 @@ namespace {
 
 template <int TILES>
 KernelRef ref(bool f16) {
-  using Cfg = RowsCfg<GQA_INST_HD, TILES>;
   constexpr bool kPaged = GQA_INST_PAGED != 0;
+  using Cfg = RowsCfg<GQA_INST_HD, TILES>;
   const void* fn = f16 ? reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, TILES, true, kPaged>)
                        : reinterpret_cast<const void*>(&gqa_rows_kernel<GQA_INST_HD, TILES, false, kPaged>);
   return KernelRef{fn, Cfg::kSmemBytes, Cfg::kThreads, Cfg::kMoveRegs ? Cfg::kLaunchRegs : 0};

@@ -17,8 +17,8 @@
 // there before; a row of the MMA reaches no other row, and neither is ever
 // written out.
 //
-// Warps: 4 softmax warps per tile, then one TMA producer, one MMA issuer and
-// one that walks the plan and hands the others their items through a ring in
+// Warps: 4 softmax warps per tile, then one TMA producer (two tiles over small pages:
+// one for Q and K and one for V), one MMA issuer and one that walks the plan and hands the others their items through a ring in
 // shared memory (so that none of them keeps the plan's state in registers).
 // A row of S is one TMEM lane, so one softmax thread holds a whole row: its
 // max and sum need no exchange, P goes back into the TMEM columns of its S
@@ -125,6 +125,7 @@ struct RowsParams {
   // byte extents of the buffers the kernel writes, checked by -DGQA_DEBUG builds
   unsigned long long out_bytes, lse_bytes, o_part_bytes, ml_part_bytes, rec_bytes;
   PagedKeys pages;      // PAGED kernels
+  int two_loaders;      // PAGED, two tiles: a warp for Q and K, and one for V
 };
 
 // One item of a CTA: a range of key blocks of one triple.  (Copied to and from
@@ -217,6 +218,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // and 1.86 us a block; a tile alone, at HBM rate, 2.68 and 2.64)
   constexpr bool BY_HALF = PAGED && TPB == 2;
   constexpr int kProducerWarp = Cfg::kSoftmaxWarps, kMmaWarp = kProducerWarp + 1, kPlanWarp = kProducerWarp + 2;
+  // A box is ~100 cycles of a warp's time: p.two_loaders gives V's a warp of its own,
+  // the idle one of two tiles.
+  constexpr int kValueWarp = kProducerWarp + 3;
+  const bool two_loaders = PAGED && NT == 2 && p.two_loaders != 0;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -261,7 +266,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
     for (int i = lane; i < N_BARRIERS; i += 32) {
       uint32_t arrivals = 1;
       if (i >= P_HALF && i < O_FULL) arrivals = 4;             // the softmax warps of a tile
-      if (i >= ITEM_EMPTY) arrivals = Cfg::kSoftmaxWarps + 2;  // softmax warps, producer, issuer
+      if (i >= ITEM_EMPTY) arrivals = Cfg::kSoftmaxWarps + (two_loaders ? 3 : 2);  // softmax warps, producers, issuer
       ptx::mbar_init(BAR(i), arrivals);
     }
     if (lane == 0) *abort_flag = 0;
@@ -335,7 +340,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
 
   if (warp >= kProducerWarp) {
   if constexpr (Cfg::kMoveRegs) ptx::regs_dec<Cfg::kControlRegs>();
-  if (warp == kProducerWarp) {
+  if (warp == kProducerWarp || (two_loaders && warp == kValueWarp)) {
     // ============================================================= producer
     // One thread; or (PAGED) the whole warp, converged, whose lanes each look a
     // page up and of which one elected thread issues.
@@ -383,7 +388,7 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
       while (next_item(it, ok, PAGED)) {
         if (it.blk_begin >= it.blk_end) continue;
         const RowsSection& s = section(it.section);
-        const int nt = slots_of(it), n = it.blk_end - it.blk_begin;
+        const int nt = PAGED && warp == kValueWarp ? 0 : slots_of(it), n = it.blk_end - it.blk_begin;
         // (pages are looked up a block before they are asked for)
         int ids = PAGED ? look_up(it, it.block(0)) : 0, ids1 = PAGED && n > 1 ? look_up(it, it.block(1)) : 0;
         for (int t = 0; t < nt; ++t, ++tq) {
@@ -401,12 +406,13 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           }
           if (PAGED) __syncwarp();
         }
-        // K0, then K(i+1), V(i): at most one block of K ahead of its V
-        if (ok) ok = load_block(false, it, it.block(0), ids);
+        // K0, then K(i+1), V(i): at most one block of K ahead of its V (but with two loaders)
+        const bool loads_k = warp == kProducerWarp, loads_v = !two_loaders || !loads_k;
+        if (ok && loads_k) ok = load_block(false, it, it.block(0), ids);
         for (int i = 0; i < n && ok; ++i) {
           const int ids2 = PAGED && i + 2 < n ? look_up(it, it.block(i + 2)) : 0;
-          if (i + 1 < n) ok = load_block(false, it, it.block(i + 1), ids1);
-          if (ok) ok = load_block(true, it, it.block(i), ids);
+          if (loads_k && i + 1 < n) ok = load_block(false, it, it.block(i + 1), ids1);
+          if (ok && loads_v) ok = load_block(true, it, it.block(i), ids);
           ids = ids1;
           ids1 = ids2;
         }

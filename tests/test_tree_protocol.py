@@ -1,7 +1,7 @@
 """Host model of the rows kernel's mbarrier protocol over paged keys (csrc/rows_kernel.cuh).
 
-What differs from test_rows_protocol, whose checks these are: at head_dim 64 three
-S slots that the steps take in turn, with two QKs ahead of the PV at hand and the
+What differs from test_rows_protocol, whose checks these are: V may have a producer of
+its own; at head_dim 64 three S slots that the steps take in turn, with two QKs ahead of the PV at hand and the
 barriers of a tile's steps three in turn; at head_dim 128, where the rows fit one
 tile, one tile with two S slots, two Q slots and three stages of V; at head_dim 256
 halves of K's and V's blocks given back each after its own MMAs.  There the block that
@@ -19,7 +19,7 @@ FORMS = {64: Form(Shape(2, 1, 4, 4), 2, True), 128: Form(Shape(1, 1, 2, 3), 2, F
 
 
 class Paged(Cta):
-    def __init__(self, form, items, rng, give_up_at=None, mistake=None):
+    def __init__(self, form, items, rng, give_up_at=None, mistake=None, loaders=2):
         super().__init__(form.shape, items, rng, give_up_at, mistake)
         self.nq, self.three, self.by_half = form.nq, form.three, form.shape.tpb == 2
         self.tails = [rng.randrange(it.n) if it.n and it.tail else -1 for it in items]
@@ -28,6 +28,8 @@ class Paged(Cta):
         self.q_full, self.q_empty = [Bar() for _ in range(self.nq)], [Bar() for _ in range(self.nq)]
         self.stage["Q"] = [dict(holds=None, loading=False, readers=0, zeroed=True) for _ in range(self.nq)]
         self.halves = form.shape.tpb == 1 and not form.three
+        self.loaders = loaders
+        self.item_empty = [Bar(self.nt * WARPS + 1 + loaders) for _ in range(RING)]
         if self.three:
             n = self.turn * self.nt
             self.s_full, self.o_full = [Bar() for _ in range(n)], [Bar() for _ in range(self.o_turn * self.nt)]
@@ -41,17 +43,28 @@ class Paged(Cta):
         return super().reads(kind, slot, content)
 
     def producer(self):
-        sh, t = self.shape, dict(K=0, V=0, Q=0)
+        """One warp, or two, of Q and K and of V, in any order."""
+        warps = [self.loads("QK"), self.loads("V")] if self.loaders == 2 else [self.loads("QKV")]
+        while warps:
+            warp = self.rng.choice(warps)
+            try:
+                next(warp)
+            except StopIteration:
+                warps.remove(warp)
+            yield
 
-        def load_block(kind, n_item, blk):
-            full, empty, ns = ((self.k_full, self.k_empty, sh.nsk) if kind == "K" else
-                               (self.v_full, self.v_empty, sh.nsv))
-            for hf in range(sh.tpb):
-                n = t[kind]
-                if n >= ns:
-                    yield from self.wait(empty[n % ns], n // ns - 1, f"producer {kind}")
-                self.load(kind, n % ns, full[n % ns], (n_item, blk, hf))
-                t[kind] += 1
+    def loads(self, kinds):
+        sh, t = self.shape, dict(K=0, V=0, Q=0)
+        rings = dict(K=(self.k_full, self.k_empty, sh.nsk), V=(self.v_full, self.v_empty, sh.nsv),
+                     Q=(self.q_full, self.q_empty, self.nq))
+
+        def load(kind, content):
+            full, empty, ns = rings[kind]
+            n = t[kind]
+            if n >= ns:
+                yield from self.wait(empty[n % ns], n // ns - 1, f"producer {kind}")
+            self.load(kind, n % ns, full[n % ns], content)
+            t[kind] += 1
 
         try:
             n = 0
@@ -59,22 +72,18 @@ class Paged(Cta):
                 it = yield from self.next_item(n, "producer item")
                 if it is None:
                     break
-                if it.n > 0:
+                if it.n > 0 and "Q" in kinds:
                     for slot in range(self.slots_of(it)):
-                        s = t["Q"] % self.nq
-                        if t["Q"] >= self.nq:
-                            yield from self.wait(self.q_empty[s], t["Q"] // self.nq - 1, "producer Q")
-                        self.load("Q", s, self.q_full[s], (n, slot, 0))
-                        t["Q"] += 1
-                    yield from load_block("K", n, 0)
-                    for i in range(it.n):
-                        if i + 1 < it.n:
-                            yield from load_block("K", n, i + 1)
-                        yield from load_block("V", n, i)
+                        yield from load("Q", (n, slot, 0))
+                for i in range(-1, it.n):
+                    for kind, blk in (("K", i + 1), ("V", i)):
+                        for hf in range(sh.tpb if kind in kinds and 0 <= blk < it.n else 0):
+                            yield from load(kind, (n, blk, hf))
                 n += 1
         except GaveUp:
             self.abort = True
-        for kind, full, ns in (("K", self.k_full, sh.nsk), ("V", self.v_full, sh.nsv), ("Q", self.q_full, self.nq)):
+        for kind in kinds:
+            full, _, ns = rings[kind]
             for u in range(max(0, t[kind] - ns), t[kind]):
                 yield from self.wait(full[u % ns], u // ns, f"drain {kind}", bounded=False)
 
@@ -270,20 +279,22 @@ def _items(rng, nt, most=7):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_protocol_holds(d):
+@pytest.mark.parametrize("loaders", [1, 2])
+def test_protocol_holds(d, loaders):
     rng = random.Random(d)
     for _ in range(250):
-        Paged(FORMS[d], _items(rng, FORMS[d].shape.nt), rng).run()
+        Paged(FORMS[d], _items(rng, FORMS[d].shape.nt), rng, loaders=loaders).run()
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_a_wait_that_runs_out_ends_every_role(d):
+@pytest.mark.parametrize("loaders", [1, 2])
+def test_a_wait_that_runs_out_ends_every_role(d, loaders):
     rng = random.Random(2 * d)
     for _ in range(250):
         items = _items(rng, FORMS[d].shape.nt, 4)
-        whole = Paged(FORMS[d], items, rng)
+        whole = Paged(FORMS[d], items, rng, loaders=loaders)
         whole.run()
-        Paged(FORMS[d], items, rng, give_up_at=rng.randint(1, whole.waits)).run()
+        Paged(FORMS[d], items, rng, give_up_at=rng.randint(1, whole.waits), loaders=loaders).run()
 
 
 def test_waits_take_no_longer_than_the_items_in_the_ring():
