@@ -232,7 +232,7 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
         const gqa_pages_t& g = *paged->geometry;
         // A head's row of 64 elements is 128 bytes, and twice as many would bring
         // another head's, which may be gone before it is asked for (16 sequences of
-        // 32768 keys of 8 heads of 64: 248 us with 256-byte fetches, 207 with these).
+        // 32768 keys of 8 heads of 64, one loading warp: 248 us with 256-byte fetches, 207 so).
         ok = encode_heads_map(maps[m], d.in_dtype, bases[m], d.head_dim, d.kv_heads, g.page_size, g.num_pages,
                               g.head_stride, g.pos_stride, g.page_stride, 1, 1 << paged->keys.box_shift,
                               d.head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);

@@ -207,8 +207,8 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
   // head_dim 64 over pages: O takes a quarter of TMEM, so that there is room for a
   // third S slot.  Steps take the slots in turn, and two QKs run ahead of the PV at
   // hand, where a tile with one slot waits for its PV and its next QK after every
-  // block (16 sequences of 32768 keys, 32 / 8 heads, us a call with three slots and
-  // two: 64 tokens 305 and 334, 26 tokens, whose keys are split, 222 and 223).
+  // block (16 sequences of 32768 keys, 32 / 8 heads, one loading warp, us a call with three
+  // slots and two: 64 tokens 305 and 334, 26 tokens, whose keys are split, 222 and 223).
   constexpr bool THREE = PAGED && HEAD_DIM == 64;
   constexpr uint32_t OCOL = THREE ? 3 * kBlockN : Cfg::kOCol;
   static_assert(OCOL + NT * HEAD_DIM <= Cfg::kTmemCols, "TMEM column plan");
