@@ -1068,6 +1068,37 @@ def test_graph_of_a_step_follows_its_inputs(dev):
 
 
 @gpu
+@pytest.mark.parametrize("B,T,H,K,d,page", [(60, 16, 32, 8, 128, 32), (40, 9, 24, 8, 256, 16), (30, 5, 16, 2, 64, 16),
+                                            (3, 70, 16, 2, 64, 16)])
+def test_graph_over_a_workspace_of_anything(dev, B, T, H, K, d, page):
+    """Captured with one set of lengths, replayed with others, over a workspace that held NaNs before each."""
+    lens = [(i * 331) % 800 for i in range(B)]
+    c = Case(dev, lens, [i % (T + 1) for i in range(B)], T, H, K, d, page, seed=B)
+    ws = torch.empty(g.gqa_tree_workspace_size(c.q, c.k, c.table), dtype=torch.uint8, device=dev)
+    out, lse = torch.empty_like(c.q), torch.empty(B, T, H, device=dev)
+
+    def run():
+        g.gqa_tree_attn(c.q, c.k, c.v, c.table, c.ln, out, lse, ws, new_lens=c.new, causal=True)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for shift in (0, 1, 7):
+        now, news = [lens[i] if i % 7 < shift else lens[i] // (1 + shift) for i in range(B)], [(i * 5 + shift) % (T + 1) for i in range(B)]
+        c.lens, c.n = now, [min(n, L) for n, L in zip(news, now)]
+        c.ln.copy_(_ints(dev, now))
+        c.new.copy_(_ints(dev, news))
+        ws.fill_(255)
+        out.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        _compare("graph", out, lse, c.want(lambda b: torch.ones(c.n[b], c.n[b]).tril().bool()))
+    assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
 def test_tensors_that_do_not_fit_are_refused(dev):
     """Types, shapes, strides and devices, each wrong by itself; nothing is launched, and nothing changes."""
     c = Case(dev, [40, 90], None, 6, 8, 2, 64, 16, seed=98)
