@@ -13,7 +13,7 @@
 
 #include "plan.cuh"
 #ifdef __CUDACC__
-#include "sm103_ptx.cuh"
+#include "decode_kernel.cuh"
 #endif
 
 namespace gqa {
@@ -29,6 +29,12 @@ struct PagedKeys {
   int tree_words;
   int chain;
 };
+
+// The token whose bits a thread fetches for row rr of its tile, whose token is tok.
+// Threads whose rows hold none take token 0's, which are not used: rows behind the
+// entry's last token, and the lanes in front of a shifted tile's first row, where rr
+// (and with it tok) is below 0.
+GQA_HD int bits_token(int rr, int tok, int live) { return rr < 0 || tok >= live ? 0 : tok; }
 
 #ifdef __CUDACC__
 namespace detail {
@@ -110,9 +116,16 @@ __device__ __forceinline__ uint32_t seen_bits(int n) {
 // Words of bits that say which positions token t of entry b sees, of the 128
 // from `from` new tokens past the first new one on: bit i of them, shifted right
 // by from modulo 32.  Positions before the first are seen, those the tree has no
-// bits for are not (and without a tree all are).
-__device__ __forceinline__ void branch_words(uint32_t (&w)[5], const PagedKeys& k, int b, int nq, int t, int from) {
+// bits for are not (and without a tree all are).  -DGQA_DEBUG builds record a token
+// that has no row, and read none.
+__device__ __forceinline__ void branch_words(uint32_t (&w)[5], const PagedKeys& k, unsigned int* err_word, int b, int nq,
+                                             int t, int from) {
   const uint32_t* row = k.tree == nullptr ? nullptr : k.tree + (static_cast<long long>(b) * nq + t) * k.tree_words;
+  const bool in_tree = b >= 0 && static_cast<unsigned>(t) < static_cast<unsigned>(nq);
+  check_coord(err_word, in_tree);
+#ifdef GQA_DEBUG
+  if (!in_tree) row = nullptr;
+#endif
 #pragma unroll
   for (int i = 0; i < 5; ++i) {
     const int at = (from >> 5) + i;  // (an arithmetic shift: below 0 for what comes before)

@@ -760,8 +760,9 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         // PAGED: the words that hold the bits of this block's keys, fetched while its scores are computed
         const bool hides = PAGED && (blk + 1) * kBlockN > (p.pages.chain != 0 || p.pages.tree != nullptr ? drafts : it.L);
         uint32_t branch[5];
-        if (hides)
-          detail::branch_words(branch, p.pages, it.b, section(it.section).nq, dead ? 0 : tok_row, blk * kBlockN - drafts);
+        if (hides && active)
+          detail::branch_words(branch, p.pages, p.err_word, it.b, section(it.section).nq, bits_token(rr, tok_row, it.live),
+                               blk * kBlockN - drafts);
         if (!wait(S_FULL + set, THREE ? g / 3u : NT == 2 ? g : g >> 1)) break;
         const int tail = it.L - blk * kBlockN;  // keys of this block
         if (tail < kBlockN) {
