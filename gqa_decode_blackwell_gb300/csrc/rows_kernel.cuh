@@ -933,10 +933,11 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
         // are of whole lines (rows one after another: trees of 40 tokens, 256 wide,
         // 51.2 us a call and not 49.7, 26 tokens of 128 60.2 and 59.5).
         const long long tile0 = sec.part_row + (static_cast<long long>(it.piece) * NT + t) * rows, prow = tile0 + rr;
-        float* dst = p.o_part + (PAGED ? tile0 * HEAD_DIM + rr * 8 : prow * HEAD_DIM);
+        float* const tile = p.o_part + tile0 * HEAD_DIM;
+        float* dst = tile + rr * (PAGED ? 8 : HEAD_DIM);
+        const unsigned long long tile_bytes = static_cast<unsigned long long>(rows) * HEAD_DIM * 4ull;
         const bool store =
-            rr < rows && !empty &&
-            detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, p.o_part + prow * HEAD_DIM, HEAD_DIM * 4ull);
+            rr < rows && !empty && detail::write_ok(p.err_word, p.o_part, p.o_part_bytes, tile, tile_bytes);
         if (rr < rows && detail::write_ok(p.err_word, p.ml_part, p.ml_part_bytes, p.ml_part + prow, sizeof(float2)))
           p.ml_part[prow] = make_float2(-nm, l);
         if (empty) continue;
@@ -947,8 +948,10 @@ gqa_rows_kernel(const __grid_constant__ RowsParams p) {
           ptx::tmem_wait_ld();
           if (store) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              ptx::st_global_v8(dst + (PAGED ? (c / 8 + q) * rows * 8 : c + 8 * q), o[q]);
+            for (int q = 0; q < 4; ++q) {
+              float* to = dst + (PAGED ? (c / 8 + q) * rows * 8 : c + 8 * q);
+              if (detail::write_ok(p.err_word, tile, tile_bytes, to, 32ull)) ptx::st_global_v8(to, o[q]);
+            }
           }
           __syncwarp();  // the next TMEM load is the whole warp's
         }

@@ -135,3 +135,27 @@ def test_trees_inside_a_larger_tensor(dev, debug, lens, news, T, H, K, d, page, 
     out, lse = c.run(tree=tree)
     assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
     assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+PARTIALS = [  # lens, news, T, H, K, d, page, dtype, out dtype: pieces of each form
+    ([4000, 1], None, 1, 32, 8, 128, 16, BF16, None),
+    ([900, 65, 300], [64, 64, 10], 64, 64, 8, 128, 128, BF16, None),                # a dead second group
+    ([9000, 641, 130], [40, 7, 33], 40, 16, 2, 256, 64, FP16, torch.float32),       # three tiles of one head
+    ([3000, 2000, 1, 700], [70, 33, 1, 0], 70, 8, 2, 64, 32, BF16, None),           # a group of two tiles, then one alone
+    ([900, 257, 256], [256, 256, 200], 256, 4, 2, 64, 16, BF16, torch.float32),
+    ([5000, 0] + [(i * 97) % 300 for i in range(60)], None, 16, 28, 4, 128, 32, FP16, None),   # whole ones and cut ones
+    ([4000] + [(i * 331) % 700 for i in range(40)], [9] + [i % 10 for i in range(40)], 9, 24, 8, 256, 64, BF16, None),
+    ([700, 650], [3, 2], 3, 100, 1, 128, 1024, FP16, None),                         # G = 100: a token a tile
+]
+
+
+@gpu
+@pytest.mark.parametrize("lens,news,T,H,K,d,page,dtype,out_dtype", PARTIALS)
+@pytest.mark.parametrize("causal", [False, True])
+def test_partials_lie_in_their_tiles(dev, debug, lens, news, T, H, K, d, page, dtype, out_dtype, causal):
+    """Each store of a partial row inside its own tile's place in the workspace; the bits of the release build."""
+    c = Case(dev, lens, news, T, H, K, d, page, dtype, seed=T)
+    got = debug(lambda: c.run(causal=causal, out_dtype=out_dtype))
+    out, lse = c.run(causal=causal, out_dtype=out_dtype)
+    assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
+    _compare("partials", out, lse, c.want((lambda b: torch.ones(c.n[b], c.n[b]).tril().bool()) if causal else None, out_dtype))
