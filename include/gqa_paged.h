@@ -82,8 +82,11 @@ typedef enum {
 /*
  * The table that the kernels turn by, computed on the host into host memory:
  * turns[i] = f_i / (2 pi) as a fraction of a turn in units of 2^-64.  A position
- * times it, modulo 2^64, is the angle without its whole turns, exact to
- * position * 2^-54 turns at worst, however far the position.  Copy it to the device once.
+ * times it, modulo 2^64, is the angle without its whole turns: the product is exact,
+ * and the table, computed in fp64, is within 2^-54 of a turn, so that the angle is off
+ * by position * 2^-54 turns at most (position 10^9: 3.5e-7 radians).  With PARTS that
+ * holds where fast^2 <= original_length * (fast - slow) / 16; a steeper ramp loses bits
+ * of w.  Copy the table to the device once.
  * base > 1; original_length >= 1 and 0 <= slow < fast with PARTS (else ignored).
  */
 gqa_status_t gqa_rotary_turns(int dim, double base, int scaling, double factor, int original_length, double slow,
