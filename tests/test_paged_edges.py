@@ -1,0 +1,41 @@
+"""Calls over pages at the edges of what include/gqa_paged.h allows."""
+import math
+
+import pytest
+import torch
+
+import gqa_decode_blackwell_gb300 as g
+from gqa_decode_blackwell_gb300 import build as gbuild
+from tests.test_paged import BF16, Case, _ints, _randn, _words
+from tests.test_shared_keys import _compare
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    gbuild.build()
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g.gqa_decode_get_error(clear=True)
+    return torch.device("cuda:0")
+
+
+@gpu
+@pytest.mark.parametrize("d,T", [(64, 5), (64, 20), (128, 30), (128, 70), (256, 20)])
+def test_rows_whose_only_bits_are_of_missing_tokens(dev, d, T):
+    """An entry with nothing but T - 2 new tokens, whose rows have set no bits but those of the two that it lacks:
+    they see nothing.  Beside it one whose rows see their own token."""
+    see = torch.zeros(2, T, T, dtype=torch.bool)
+    see[0, :, T - 2:] = True
+    see[1] = torch.eye(T)
+    c = Case(dev, [T - 2, T], [T - 2, T], T, 8, 2, d, 16, seed=d + T)
+    c.poison()
+    out, lse = c.run(tree=_words(see).to(dev))
+    assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+    _compare("alone", out, lse, c.want(lambda b: see[b, : c.n[b], : c.n[b]]))
+    assert g.gqa_decode_get_error() == g.GQA_OK
