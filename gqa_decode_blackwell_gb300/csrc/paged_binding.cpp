@@ -128,6 +128,7 @@ int64_t token_stride(const Tensor& t, const char* what) {
   const int64_t heads = sizes[n - 2], d = sizes[n - 1];
   if ((d > 1 && strides[n - 1] != 1) || (heads > 1 && strides[n - 2] != d))
     refuse(std::string(what) + " must have dense heads");
+  if (t.numel() == 0) return heads * d;  // no token is reached by any
   int64_t stride = -1, run = 1;  // from the last token dimension outwards
   for (size_t i = n - 2; i-- > 0;) {
     if (sizes[i] == 1) continue;

@@ -39,3 +39,21 @@ def test_rows_whose_only_bits_are_of_missing_tokens(dev, d, T):
     assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
     _compare("alone", out, lse, c.want(lambda b: see[b, : c.n[b], : c.n[b]]))
     assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@pytest.mark.parametrize("t,stride", [
+    (torch.empty(2, 0, 8, 64), 512), (torch.empty(2, 0, 12, 64)[:, :, 4:8], 256), (torch.empty(3, 2, 0, 8, 64), 512),
+    (torch.empty(0, 3, 8, 64), 512), (torch.empty(0, 8, 64), 512)])
+def test_no_tokens_have_a_stride(t, stride):
+    """A tensor without tokens has one stride for all of them, wherever its empty dimension is."""
+    assert g._paged().stride_of(t) == stride
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(0, 8, 64), (2, 0, 8, 64), (0, 5, 8, 64), (3, 2, 0, 8, 64)])
+def test_rotation_of_no_tokens(dev, shape):
+    x, turns = torch.empty(shape, dtype=BF16, device=dev), g.rotary_turns(64, device=dev)
+    positions = torch.empty(shape[:-2], dtype=torch.int32, device=dev)
+    assert g.rotary(x, positions, turns).shape == shape
+    g.gqa_rotary_apply(x, positions, turns, x)
+    assert g.gqa_decode_get_error() == g.GQA_OK
