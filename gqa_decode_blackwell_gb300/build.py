@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -52,13 +53,26 @@ def binding_path() -> str:
     return os.path.join(PKG, f"_paged_binding-{sys.implementation.cache_tag}-torch{torch.__version__}.so")
 
 
-def _start_binding(out: str) -> subprocess.Popen:
+def _binding_includes():
+    """Include directories of the binding, or None where PyTorch, or its headers or
+    Python's, are not installed."""
+    try:
+        import torch
+    except (ImportError, OSError):
+        return None
+    base = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "include")
+    python = sysconfig.get_paths()["include"]
+    for header in (os.path.join(python, "Python.h"), os.path.join(base, "torch", "csrc", "autograd", "python_variable.h")):
+        if not os.path.exists(header):
+            return None
+    return [python, base, os.path.join(base, "torch", "csrc", "api", "include"),
+            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+
+
+def _start_binding(out: str, includes) -> subprocess.Popen:
     import torch
 
     base = os.path.dirname(os.path.abspath(torch.__file__))
-    includes = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
-                os.path.join(base, "include", "torch", "csrc", "api", "include"),
-                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
     return subprocess.Popen([
         shutil.which("g++") or "g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-w",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in includes),
@@ -103,20 +117,29 @@ def _units(build_dir: str):
 def build(force: bool = False, out: str = LIB, extra_flags=(), verbose: bool = False) -> str:
     """Compile the csrc translation units for sm_103a (in parallel) and link
     them into ``out``, and for the library itself the binding beside it (each
-    skipped if current)."""
-    binding = binding_path() if out == LIB else None
-    if binding is None or (not force and _binding_up_to_date(binding)):
+    skipped if current).  Without PyTorch or its headers or Python's the C library
+    is built alone, with a warning: the Python functions of
+    ``include/gqa_paged.h`` then raise."""
+    if out != LIB:
+        return _build_library(force, out, extra_flags, verbose)
+    includes = _binding_includes()
+    if includes is None:
+        warnings.warn("PyTorch, its headers or Python's are not installed: the binding of the paged calls is not built")
+        return _build_library(force, out, extra_flags, verbose)
+    binding = binding_path()
+    if not force and _binding_up_to_date(binding):
         return _build_library(force, out, extra_flags, verbose)
     os.makedirs(os.path.join(PKG, "_build"), exist_ok=True)
     temporary = os.path.join(PKG, "_build", f"{os.path.basename(binding)}.{os.getpid()}")
-    process = _start_binding(temporary)
+    process = _start_binding(temporary, includes)
     try:
-        return _build_library(force, out, extra_flags, verbose)
+        _build_library(force, out, extra_flags, verbose)
     finally:
-        if process.wait() == 0:
-            os.replace(temporary, binding)
-        else:
-            raise subprocess.CalledProcessError(process.returncode, "g++ (paged_binding.cpp)")
+        failed = process.wait() != 0  # waited for in either case
+    if failed:
+        raise subprocess.CalledProcessError(process.returncode, "g++ (paged_binding.cpp)")
+    os.replace(temporary, binding)
+    return out
 
 
 def _build_library(force: bool, out: str, extra_flags, verbose: bool) -> str:
