@@ -589,7 +589,8 @@ def _paged():
 def gqa_rotary_apply(x, positions, turns, out, *, interleaved: bool = False, inverse: bool = False,
                      magnitude: float = 0.0, stream=None) -> None:
     """Rotates x [..., heads, d] to positions int32 [...] into ``out`` (x itself, or
-    apart from it); see gqa_rotary_apply in ``include/gqa_paged.h``."""
+    apart from it); see gqa_rotary_apply in ``include/gqa_paged.h``.  No gradient is
+    recorded (``rotary`` records it)."""
     if stream is not None:
         stream = _raw_stream(stream, x.get_device())
     rc = _paged().rotary_apply(x, positions, turns, out, interleaved, inverse, magnitude, stream)
@@ -597,14 +598,51 @@ def gqa_rotary_apply(x, positions, turns, out, *, interleaved: bool = False, inv
         raise GQAError(rc, "gqa_rotary_apply")
 
 
+_rotation = None
+
+
+def _recorded_rotation():
+    """The rotation as autograd records it: linear, so that its gradient is the inverse
+    rotation of the incoming one (of the same magnitude)."""
+    global _rotation
+    if _rotation is None:
+        import torch
+
+        class Rotation(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, positions, turns, interleaved, inverse, magnitude):
+                ctx.save_for_backward(positions, turns)
+                ctx.how = interleaved, inverse, magnitude
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                gqa_rotary_apply(x, positions, turns, out, interleaved=interleaved, inverse=inverse, magnitude=magnitude)
+                return out
+
+            @staticmethod
+            def backward(ctx, grad):
+                positions, turns = ctx.saved_tensors
+                interleaved, inverse, magnitude = ctx.how
+                grad = rotary(grad.contiguous(), positions, turns, interleaved=interleaved, inverse=not inverse,
+                              magnitude=magnitude)
+                return grad, None, None, None, None, None
+
+        _rotation = Rotation
+    return _rotation
+
+
 def rotary(x, positions, turns, *, interleaved: bool = False, inverse: bool = False, magnitude: float = 0.0,
            stream=None):
-    """Allocates the result with torch and calls gqa_rotary_apply."""
+    """Allocates the result with torch and calls gqa_rotary_apply.  Differentiable in
+    x: the backward pass reads positions and turns again, which have to stay as they
+    are until then."""
     import torch
 
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
+    if stream is not None:
+        _raw_stream(stream, x.get_device())  # refuses another device's
     with torch.cuda.stream(_torch_stream(stream, x.device)):
+        if x.requires_grad and torch.is_grad_enabled():  # (recorded on the stream it runs on: the backward pass's too)
+            return _recorded_rotation().apply(x, positions, turns, interleaved, inverse, magnitude)
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     gqa_rotary_apply(x, positions, turns, out, interleaved=interleaved, inverse=inverse, magnitude=magnitude,
                      stream=stream)
