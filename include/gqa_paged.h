@@ -14,7 +14,8 @@
  *     gqa_paged_keep          the accepted branch moved together in the cache
  *
  * and a step of one token, or a chunk of a prompt, gqa_paged_append and
- * gqa_tree_attn.  gqa_rotary_apply rotates a tensor by itself.
+ * gqa_tree_attn (which takes up to GQA_MAX_TREE_TOKENS tokens of a sequence a call:
+ * longer chunks take several, see there).  gqa_rotary_apply rotates a tensor by itself.
  *
  * The conventions of gqa_decode.h hold: device pointers, caller-owned memory,
  * asynchronous on `stream`, checked before anything is launched, on the current
@@ -161,7 +162,12 @@ gqa_status_t gqa_tree_from_parents(int batch, int q_tokens, int max_seqlen, cons
  *   chunk of a prompt), or
  *   all of them (tree NULL, desc->causal 0).
  * A row that sees nothing, and every row behind the last token, is O = 0,
- * lse = -inf.  desc as in gqa_decode_attn, with q_tokens <= GQA_MAX_TREE_TOKENS,
+ * lse = -inf.
+ * A chain of n_b > GQA_MAX_TREE_TOKENS tokens, appended in one call, is seen in
+ * several, each over the positions up to its own last token: for tokens [i, i + m)
+ * of it, L_b - n_b + min(n_b, i + m) as the length and min(max(n_b - i, 0), m) as
+ * the number of new tokens.
+ * desc as in gqa_decode_attn, with q_tokens <= GQA_MAX_TREE_TOKENS,
  * at most 128 query heads to a KV head and max_seqlen <= max_pages * page_size;
  * reduction must be GQA_REDUCE_AUTO.
  *   q          in_dtype [B, nq, Hq, d], dense, 16-byte aligned

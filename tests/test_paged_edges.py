@@ -6,7 +6,7 @@ import torch
 
 import gqa_decode_blackwell_gb300 as g
 from gqa_decode_blackwell_gb300 import build as gbuild
-from tests.test_paged import BF16, Case, _ints, _randn, _words
+from tests.test_paged import BF16, Case, _randn, _words
 from tests.test_shared_keys import _compare
 
 gpu = pytest.mark.gpu
@@ -56,4 +56,27 @@ def test_rotation_of_no_tokens(dev, shape):
     positions = torch.empty(shape[:-2], dtype=torch.int32, device=dev)
     assert g.rotary(x, positions, turns).shape == shape
     g.gqa_rotary_apply(x, positions, turns, x)
+    assert g.gqa_decode_get_error() == g.GQA_OK
+
+
+@gpu
+@pytest.mark.parametrize("lens,news,H,K,d,page,m", [
+    ([1500, 700, 300, 0], [1000, 513, 256, 0], 8, 2, 128, 16, 256), ([900, 600], [600, 37], 8, 1, 64, 32, 256),
+    ([700], [700], 4, 2, 256, 16, 100)])
+def test_chunks_longer_than_a_call(dev, lens, news, H, K, d, page, m):
+    """A chunk of a prompt appended in one call and seen in several, with the lengths that the header gives: the rows
+    of one chain."""
+    T, B = max(news), len(lens)
+    c = Case(dev, lens, news, T, H, K, d, page, seed=d)
+    new = _randn(dev, B, T, H + 2 * K, d, seed=5)
+    turns = g.rotary_turns(d, device=dev)
+    g.gqa_paged_append(new[:, :, :H], new[:, :, H: H + K], new[:, :, H + K:], c.q, c.k, c.v, c.table, c.ln, new_lens=c.new,
+                       turns=turns)
+    out, lse = torch.full_like(c.q, math.nan), torch.full((B, T, H), math.nan, device=dev)
+    for i in range(0, T, m):
+        upto = c.ln - c.new + torch.clamp(c.new, max=i + m)
+        here = torch.clamp(c.new - i, 0, m)
+        o, l = g.tree_attention(c.q[:, i: i + m].contiguous(), c.k, c.v, c.table, upto, new_lens=here, causal=True)
+        out[:, i: i + m], lse[:, i: i + m] = o, l
+    _compare("chunk", out, lse, c.want(lambda b: torch.ones(c.n[b], c.n[b]).tril().bool()))
     assert g.gqa_decode_get_error() == g.GQA_OK
