@@ -198,8 +198,9 @@ gqa_status_t gqa_tree_attn(const gqa_desc_t* desc, const gqa_pages_t* pages, con
  *   path       int32 [B, max_keep]: new tokens, each in [0, n_b) and past the one
  *              before it; the branch ends (and is flagged) at one that is not
  *   keep_lens  int32 [B]: m_b in [0, max_keep] (clamped and flagged)
- *   seqlens_out  int32 [B] or NULL: L_b - n_b + the tokens moved; may be seqlens
- * A token whose page, or whose place's page, is out of range is not moved.
+ *   seqlens_out  int32 [B] or NULL: L_b - n_b + the branch's tokens; may be seqlens
+ * A token whose page, or whose place's page, is out of range is not moved (and is
+ * flagged); its place counts all the same.
  */
 gqa_status_t gqa_paged_keep(const gqa_desc_t* desc, const gqa_pages_t* pages, void* k_cache, void* v_cache,
                             const int32_t* page_table, const int32_t* seqlens, const int32_t* new_lens,
