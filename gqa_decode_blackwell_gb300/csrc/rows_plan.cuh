@@ -48,15 +48,20 @@ GQA_HD uint32_t div_by(uint32_t x, const RowsDivisor& by) {  // x below 2^31
   const uint32_t q = static_cast<uint32_t>((static_cast<uint64_t>(x) * by.m) >> 32);
   return q * by.d > x ? q - 1 : q;
 }
-// x / d for quotients below 2^20, in fp32: off by one at most, before it is put right.
-GQA_HD uint32_t div_small(uint32_t x, uint32_t d) {
-#ifdef __CUDA_ARCH__
-  uint32_t q = static_cast<uint32_t>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+// x / d from a quotient that is off by less than one.
+GQA_HD uint32_t div_corrected(float quotient, uint32_t x, uint32_t d) {
+  uint32_t q = static_cast<uint32_t>(quotient);
   if (q * d > x) --q;
   if (x - q * d >= d) ++q;
   return q;
+}
+// x / d for quotients below 2^20 and x, d below 2^31, in fp32: two operands rounded
+// and a division good to 2 ulp are off by less than 2^20 * 3 * 2^-23.
+GQA_HD uint32_t div_small(uint32_t x, uint32_t d) {
+#ifdef __CUDA_ARCH__
+  return div_corrected(__fdividef(static_cast<float>(x), static_cast<float>(d)), x, d);
 #else
-  return x / d;
+  return div_corrected(static_cast<float>(x) / static_cast<float>(d), x, d);
 #endif
 }
 
