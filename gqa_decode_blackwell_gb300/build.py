@@ -22,9 +22,10 @@ SHARED_KEYS_HEADER = os.path.join(ROOT, "include", "gqa_shared_keys.h")
 PAGED_HEADER = os.path.join(ROOT, "include", "gqa_paged.h")
 LIB = os.path.join(PKG, "libgqa_decode_sm103.so")
 # The same library with device-side bounds checks (-DGQA_DEBUG): every
-# global write of the decode kernel is checked against its buffer and
-# skipped if outside it, every TMA tile origin against its tensor; either
-# shows as GQA_ERR_BOUNDS from gqa_decode_get_error.  For testing only.
+# global write of the decode kernel, the rows kernel and its merges, and the
+# kernels around a paged cache is checked against its buffer and skipped if
+# outside it, every TMA tile origin against its tensor, reads of a page table
+# and of a tree's bits against their rows; each shows as GQA_ERR_BOUNDS from gqa_decode_get_error.  For testing only.
 DEBUG_LIB = os.path.join(PKG, "libgqa_decode_sm103_debug.so")
 # The same library with the decode kernel's clock64 event trace
 # (-DGQA_TRACE): gqa_trace_attach() names a device buffer that the following

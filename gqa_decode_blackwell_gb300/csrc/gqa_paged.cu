@@ -66,6 +66,12 @@ PagedKeys paged_keys(const gqa_pages_t& g, const int32_t* table, const int32_t* 
   return k;
 }
 
+// Bytes from a cache's first element to behind its last one.
+unsigned long long cache_bytes(const gqa_pages_t& g, int kv_heads, int head_dim) {
+  auto last = [](int n, int64_t stride) { return static_cast<unsigned long long>(n - 1) * static_cast<unsigned long long>(stride); };
+  return 2 * (last(g.num_pages, g.page_stride) + last(g.page_size, g.pos_stride) + last(kv_heads, g.head_stride) + head_dim);
+}
+
 // Elements of the runs that a number of pairs comes apart into.
 int run_of(bool interleaved, int pairs) {
   return interleaved || pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
@@ -198,6 +204,10 @@ gqa_status_t gqa_rotary_apply(const gqa_rotary_t* rope, const uint64_t* turns, c
   p.pairs = rope->dim / 2;
   p.inverse = rope->inverse != 0 ? 1 : 0;
   p.magnitude = rope->magnitude > 0.f ? rope->magnitude : 1.f;
+  p.x_bytes = static_cast<unsigned long long>((tokens - 1) * out_stride + dense) * (dtype == GQA_DTYPE_FP32 ? 4 : 2);
+#ifdef GQA_DEBUG
+  if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
+#endif
   return launch_rotary<false>(dtype, rope->interleaved != 0, p, tokens, heads, st->sm_count,
                               static_cast<cudaStream_t>(stream));
 }
@@ -250,6 +260,8 @@ gqa_status_t gqa_paged_append(const gqa_desc_t* desc, const gqa_pages_t* pages, 
   p.head_dim = desc->head_dim;
   p.pairs = rope != nullptr ? rope->dim / 2 : 0;
   p.magnitude = rope != nullptr && rope->magnitude > 0.f ? rope->magnitude : 1.f;
+  p.x_bytes = q != nullptr ? static_cast<unsigned long long>(tokens * dense_q) * 2 : 0;
+  p.cache_bytes = cache_bytes(*pages, desc->kv_heads, desc->head_dim);
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
   return launch_rotary<true>(desc->in_dtype, rope != nullptr && rope->interleaved != 0, p, tokens,
                              p.x.heads + 2 * desc->kv_heads, st->sm_count, static_cast<cudaStream_t>(stream));
@@ -277,6 +289,9 @@ gqa_status_t gqa_tree_from_parents(int batch, int q_tokens, int max_seqlen, cons
   p.nq = q_tokens;
   p.words = (q_tokens + 31) / 32;
   p.max_seqlen = max_seqlen;
+  const unsigned long long rows = static_cast<unsigned long long>(batch) * q_tokens;
+  p.tree_bytes = rows * p.words * 4;
+  p.positions_bytes = positions != nullptr ? rows * 4 : 0;
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
   return launch_kernel(reinterpret_cast<const void*>(&gqa_tree_kernel), dim3(static_cast<unsigned>(batch)),
                        32 * p.words, 0, &p, static_cast<cudaStream_t>(stream));
@@ -350,6 +365,8 @@ gqa_status_t gqa_paged_keep(const gqa_desc_t* desc, const gqa_pages_t* pages, vo
   p.max_keep = max_keep;
   p.kv_heads = desc->kv_heads;
   p.head_dim = desc->head_dim;
+  p.cache_bytes = cache_bytes(*pages, desc->kv_heads, desc->head_dim);
+  p.lens_bytes = seqlens_out != nullptr ? static_cast<unsigned long long>(desc->batch) * 4 : 0;
   if ((rc = error_word(st, &p.err_word)) != GQA_OK) return rc;
   return launch_kernel(reinterpret_cast<const void*>(&gqa_keep_kernel), dim3(static_cast<unsigned>(desc->batch)),
                        kKeepThreads, 0, &p, static_cast<cudaStream_t>(stream));

@@ -327,6 +327,9 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
   m.kv_heads = r.kv_heads;
   m.tiles = r.tiles;
   m.paged = paged != nullptr ? 1 : 0;
+  m.err_word = p.err_word;
+  m.out_bytes = p.out_bytes;
+  m.lse_bytes = p.lse_bytes;
   // Of a paged call's few rows each gets a CTA (below), of more each a place among
   // its tile's.
   if (paged != nullptr && (!r.every_piece || rows > kMergeSharedRows)) {

@@ -39,10 +39,24 @@ GQA_HD int bits_token(int rr, int tok, int live) { return rr < 0 || tok >= live 
 #ifdef __CUDACC__
 namespace detail {
 
+// The table's page number of position pos of entry b.  -DGQA_DEBUG builds record a
+// position that the entry's row does not reach, and read none.
+__device__ __forceinline__ int page_number(const PagedKeys& k, unsigned int* err_word, int b, int pos) {
+#ifdef GQA_DEBUG
+  if (b < 0 || pos < 0 || (pos >> k.page_shift) >= k.cols) {
+    atomicOr(err_word, kErrBounds);
+    return -1;
+  }
+#else
+  (void)err_word;
+#endif
+  return k.table[static_cast<long long>(b) * k.cols + (pos >> k.page_shift)];
+}
+
 // The page of position pos of entry b.  A number that names no page is flagged
 // and replaced by the one past the last, whose box TMA fills with zeros.
 __device__ __forceinline__ int page_of(const PagedKeys& k, unsigned int* err_word, int b, int pos) {
-  const int page = k.table[static_cast<long long>(b) * k.cols + (pos >> k.page_shift)];
+  const int page = page_number(k, err_word, b, pos);
   if (static_cast<unsigned>(page) < static_cast<unsigned>(k.num_pages)) return page;
   atomicOr(err_word, kErrBadIndex);
   return k.num_pages;

@@ -55,6 +55,8 @@ struct RotaryParams {
   int group;                 // tokens of a CTA (kernels of groups)
   long long tokens;
   unsigned int* err_word;
+  // byte extents of what is written (x.dst, each cache), checked by -DGQA_DEBUG builds
+  unsigned long long x_bytes, cache_bytes;
 };
 
 namespace detail {
@@ -193,13 +195,25 @@ __device__ __forceinline__ void turn_runs(Run<T, N>& a, Run<T, N>& b, const floa
   }
 }
 
+// Stores a run into the head at `to`, from element `at` on.
+template <typename T, int N>
+__device__ __forceinline__ void put_run(const RotaryParams& p, const Run<T, N>& run, T* to, int at) {
+  if (write_ok(p.err_word, to, p.head_dim * sizeof(T), to + at, N * sizeof(T))) run.store(to + at);
+}
+// `to`, if a head there lies inside the buffer it belongs to.
+template <typename T>
+__device__ __forceinline__ T* head_in(const RotaryParams& p, const void* base, unsigned long long bytes, T* to) {
+  return write_ok(p.err_word, base, bytes, to, p.head_dim * sizeof(T)) ? to : nullptr;
+}
+
 // The rows of one CTA: head r of them is at src(r) and goes to dst(r) (nowhere, if
 // that is null); those with rotated(r) are rotated by the table, which `ready`
 // fills while the first loads are under way.  (The next two runs loaded ahead cost
 // registers, and so CTAs: prompts 24.0 us, then 19.7 without.)
 template <typename T, bool INTERLEAVED, int N, typename Src, typename Dst, typename Rotated, typename Ready>
-__device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, const float4* table, const Src& src,
+__device__ __forceinline__ void turn_heads(const RotaryParams& p, int n_rows, const float4* table, const Src& src,
                                            const Dst& dst, const Rotated& rotated, const Ready& ready) {
+  const int head_dim = p.head_dim, pairs = p.pairs;
   // units of a row: a power of two, as head_dim and N are
   const int row_shift = 31 - __clz(head_dim / (2 * N)), n = n_rows << row_shift;
   const int step = static_cast<int>(gridDim.y * blockDim.x);
@@ -222,8 +236,8 @@ __device__ __forceinline__ void turn_heads(int n_rows, int head_dim, int pairs, 
     T* to = dst(r);
     if (to != nullptr) {
       const int2 at = runs_of<INTERLEAVED, N>(i, turns ? pairs : 0);
-      a.store(to + at.x);
-      b.store(to + at.y);
+      put_run(p, a, to, at.x);
+      put_run(p, b, to, at.y);
     }
     if ((u += step) < n) load();
   }
@@ -287,9 +301,10 @@ gqa_rotary_kernel(const RotaryParams p) {
     __syncthreads();
     if (!m.here) return;
     detail::turn_runs<T, INTERLEAVED, N>(a, b, table + m.sub * m.angles, i, p.pairs);
-    T* to = static_cast<T*>(p.x.dst) + token * p.x.dst_stride + in_token;
-    a.store(to + at.x);
-    b.store(to + at.y);
+    T* to = detail::head_in(p, p.x.dst, p.x_bytes, static_cast<T*>(p.x.dst) + token * p.x.dst_stride + in_token);
+    if (to == nullptr) return;
+    detail::put_run(p, a, to, at.x);
+    detail::put_run(p, b, to, at.y);
     return;
   }
   const long long token = blockIdx.x;
@@ -299,9 +314,9 @@ gqa_rotary_kernel(const RotaryParams p) {
   const T* src = static_cast<const T*>(p.x.src) + token * p.x.src_stride;
   T* dst = static_cast<T*>(p.x.dst) + token * p.x.dst_stride;
   detail::turn_heads<T, INTERLEAVED, N>(
-      p.x.heads, p.head_dim, p.pairs, table,
-      [&](int r) { return src + static_cast<long long>(r) * p.head_dim; },
-      [&](int r) { return dst + static_cast<long long>(r) * p.head_dim; }, [](int) { return true; },
+      p, p.x.heads, table, [&](int r) { return src + static_cast<long long>(r) * p.head_dim; },
+      [&](int r) { return detail::head_in(p, p.x.dst, p.x_bytes, dst + static_cast<long long>(r) * p.head_dim); },
+      [](int) { return true; },
       [&] {
         for (int i = tid; i < p.pairs; i += static_cast<int>(blockDim.x))
           detail::put_angle<N>(table, i, p.pairs,
@@ -345,7 +360,7 @@ gqa_append_kernel(const RotaryParams p) {
                                       : static_cast<const T*>(p.v.src) + token * p.v.src_stride + (r - hq - hk) * d;
         a.load(from + at.x);
         b.load(from + at.y);
-        page = p.pages.table[static_cast<long long>(e) * p.pages.cols + (place >> p.pages.page_shift)];
+        page = detail::page_number(p.pages, p.err_word, e, place);
       }
       if (m.unit == 0) positions[m.sub] = p.positions != nullptr ? given : place;
     }
@@ -360,18 +375,20 @@ gqa_append_kernel(const RotaryParams p) {
     if (pairs > 0) detail::turn_runs<T, INTERLEAVED, N>(a, b, table + m.sub * m.angles, i, pairs);
     T* to;
     if (r < hq) {
-      to = static_cast<T*>(p.x.dst) + token * p.x.dst_stride + r * d;
+      to = detail::head_in(p, p.x.dst, p.x_bytes, static_cast<T*>(p.x.dst) + token * p.x.dst_stride + r * d);
     } else {
       if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages.num_pages)) {
         atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
         return;
       }
       const int h = r < hq + hk ? r - hq : r - hq - hk;
-      to = static_cast<T*>(r < hq + hk ? p.k_cache : p.v_cache) + page * p.page_stride +
-           (place & p.pages.page_mask) * p.pos_stride + h * p.head_stride;
+      T* cache = static_cast<T*>(r < hq + hk ? p.k_cache : p.v_cache);
+      to = detail::head_in(p, cache, p.cache_bytes,
+                           cache + page * p.page_stride + (place & p.pages.page_mask) * p.pos_stride + h * p.head_stride);
     }
-    a.store(to + at.x);
-    b.store(to + at.y);
+    if (to == nullptr) return;
+    detail::put_run(p, a, to, at.x);
+    detail::put_run(p, b, to, at.y);
     return;
   }
   const long long token = blockIdx.x;
@@ -387,7 +404,7 @@ gqa_append_kernel(const RotaryParams p) {
   if (t >= n) return;
   const int place = L - n + t;
   const int position = p.positions != nullptr ? given : place;
-  const int page = p.pages.table[static_cast<long long>(b) * p.pages.cols + (place >> p.pages.page_shift)];
+  const int page = detail::page_number(p.pages, p.err_word, b, place);
   const T* q = static_cast<const T*>(p.x.src) + token * p.x.src_stride;
   const T* k = static_cast<const T*>(p.k.src) + token * p.k.src_stride;
   const T* v = static_cast<const T*>(p.v.src) + token * p.v.src_stride;
@@ -396,15 +413,16 @@ gqa_append_kernel(const RotaryParams p) {
   T *k_to = nullptr, *v_to = nullptr;
   const int hq = p.x.heads, hk = p.k.heads;
   detail::turn_heads<T, INTERLEAVED, N>(
-      hq + 2 * hk, p.head_dim, p.pairs, table,
+      p, hq + 2 * hk, table,
       [&](int r) {
         const long long d = p.head_dim;
         return r < hq ? q + r * d : r < hq + hk ? k + (r - hq) * d : v + (r - hq - hk) * d;
       },
       [&](int r) -> T* {
-        if (r < hq) return q_out + static_cast<long long>(r) * p.head_dim;
+        if (r < hq) return detail::head_in(p, p.x.dst, p.x_bytes, q_out + static_cast<long long>(r) * p.head_dim);
         if (k_to == nullptr) return nullptr;
-        return r < hq + hk ? k_to + (r - hq) * p.head_stride : v_to + (r - hq - hk) * p.head_stride;
+        return r < hq + hk ? detail::head_in(p, p.k_cache, p.cache_bytes, k_to + (r - hq) * p.head_stride)
+                           : detail::head_in(p, p.v_cache, p.cache_bytes, v_to + (r - hq - hk) * p.head_stride);
       },
       [&](int r) { return r < hq + hk && p.pairs > 0; },
       [&] {
@@ -432,6 +450,7 @@ struct TreeParams {
   int32_t* positions;       // [B, nq] or null
   int nq, words, max_seqlen;
   unsigned int* err_word;
+  unsigned long long tree_bytes, positions_bytes;  // byte extents, checked by -DGQA_DEBUG builds
 };
 
 // A CTA to a sequence, a thread to a token.  Each token holds the bits of the
@@ -479,9 +498,11 @@ gqa_tree_kernel(const TreeParams p) {
 #pragma unroll
   for (int w = 0; w < kMaxTreeWords; ++w) {
     depth += __popc(own[w]);
-    if (w < p.words) p.tree[row * p.words + w] = own[w];
+    uint32_t* to = p.tree + row * p.words + w;
+    if (w < p.words && detail::write_ok(p.err_word, p.tree, p.tree_bytes, to, 4)) *to = own[w];
   }
-  if (p.positions != nullptr) p.positions[row] = t < n ? L - n + depth : 0;
+  if (p.positions != nullptr && detail::write_ok(p.err_word, p.positions, p.positions_bytes, p.positions + row, 4))
+    p.positions[row] = t < n ? L - n + depth : 0;
 }
 
 constexpr int kKeepThreads = 256;
@@ -497,6 +518,7 @@ struct KeepParams {
   int32_t* seqlens_out;      // [B] or null; may be seqlens
   int nq, max_seqlen, max_keep, kv_heads, head_dim;
   unsigned int* err_word;
+  unsigned long long cache_bytes, lens_bytes;  // byte extents, checked by -DGQA_DEBUG builds
 };
 
 // A CTA to a sequence, 8 elements of K or of V to a thread, which moves them
@@ -527,12 +549,11 @@ gqa_keep_kernel(const KeepParams p) {
   const int most = asked < 0 ? 0 : (asked > p.max_keep ? p.max_keep : asked);
   if (asked != most && tid == 0) atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
   // the page of the token at `at`, and of place i (a token in range is not before its place)
-  const int32_t* table = p.pages.table + static_cast<long long>(b) * p.pages.cols;
   int from = 0, to = 0;
   auto look_up = [&](int i) {
     if (i >= most || at < i || at >= n) return;
-    from = table[(first + at) >> p.pages.page_shift];
-    to = table[(first + i) >> p.pages.page_shift];
+    from = detail::page_number(p.pages, p.err_word, b, first + at);
+    to = detail::page_number(p.pages, p.err_word, b, first + i);
   };
   look_up(tid);
   __shared__ int s_bad;  // the first token of the branch that is out of range or does not ascend
@@ -546,7 +567,8 @@ gqa_keep_kernel(const KeepParams p) {
   const int keep = s_bad;
   if (tid == 0) {
     if (keep != most) atomicOr(p.err_word, static_cast<unsigned>(kErrBadIndex));
-    if (p.seqlens_out != nullptr) p.seqlens_out[b] = first + keep;
+    if (p.seqlens_out != nullptr && detail::write_ok(p.err_word, p.seqlens_out, p.lens_bytes, p.seqlens_out + b, 4))
+      p.seqlens_out[b] = first + keep;
   }
   __shared__ long long s_from[kKeepThreads], s_to[kKeepThreads];  // below 0: it stays, or is lost
   const int per_head = p.head_dim / 8, per_cache = p.kv_heads * per_head;
@@ -571,8 +593,8 @@ gqa_keep_kernel(const KeepParams p) {
     __syncthreads();
     for (int c = tid; c < 2 * per_cache; c += kKeepThreads) {
       const int in = c < per_cache ? c : c - per_cache, head = in / per_head;
-      uint16_t* cache = static_cast<uint16_t*>(c < per_cache ? p.k_cache : p.v_cache) + head * p.head_stride +
-                        (in - head * per_head) * 8;
+      uint16_t* base_of = static_cast<uint16_t*>(c < per_cache ? p.k_cache : p.v_cache);
+      uint16_t* cache = base_of + head * p.head_stride + (in - head * per_head) * 8;
       for (int i0 = 0; i0 < here; i0 += kBatch) {
         uint4 row[kBatch];
 #pragma unroll
@@ -580,7 +602,9 @@ gqa_keep_kernel(const KeepParams p) {
           if (i0 + j < here && s_from[i0 + j] >= 0) row[j] = *reinterpret_cast<const uint4*>(cache + s_from[i0 + j]);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
-          if (i0 + j < here && s_from[i0 + j] >= 0) *reinterpret_cast<uint4*>(cache + s_to[i0 + j]) = row[j];
+          if (i0 + j < here && s_from[i0 + j] >= 0 &&
+              detail::write_ok(p.err_word, base_of, p.cache_bytes, cache + s_to[i0 + j], 16))
+            *reinterpret_cast<uint4*>(cache + s_to[i0 + j]) = row[j];
       }
     }
     __syncthreads();

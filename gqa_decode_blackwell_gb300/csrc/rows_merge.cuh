@@ -45,6 +45,8 @@ struct RowsMergeParams {
   int batch, nq, Hq, G, kv_heads;
   int tiles;           // row tiles of a triple
   int paged;           // a tile's partial rows lie 8 elements of all of them after another
+  unsigned int* err_word;
+  unsigned long long out_bytes, lse_bytes;  // byte extents, checked by -DGQA_DEBUG builds
 };
 
 namespace detail {
@@ -117,8 +119,7 @@ __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int out_dtype) 
 }
 
 template <int HEAD_DIM>
-__device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void* out, float* lse, int out_dtype,
-                                          long long row) {
+__device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, const RowsMergeParams& p, long long row) {
   constexpr int VEC = HEAD_DIM / 32;
   const int lane = threadIdx.x & 31;
   const bool none = sum.W == 0.f;
@@ -126,8 +127,9 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
   float acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = none ? 0.f : sum.acc[i] * inv;
-  if (out_dtype == kOutF32) {
-    float* dst = static_cast<float*>(out) + row * HEAD_DIM + lane * VEC;
+  if (p.out_dtype == kOutF32) {
+    float* dst = static_cast<float*>(p.out) + row * HEAD_DIM + lane * VEC;
+    if (!write_ok(p.err_word, p.out, p.out_bytes, dst, VEC * 4)) return;
     if constexpr (VEC == 8) {
       reinterpret_cast<float4*>(dst)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
       reinterpret_cast<float4*>(dst)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -139,13 +141,15 @@ __device__ __forceinline__ void write_row(const RowSum<HEAD_DIM / 32>& sum, void
   } else {
     uint32_t w[VEC / 2];
 #pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) w[i] = pack_out(acc[2 * i], acc[2 * i + 1], out_dtype);
-    uint16_t* dst = static_cast<uint16_t*>(out) + row * HEAD_DIM + lane * VEC;
+    for (int i = 0; i < VEC / 2; ++i) w[i] = pack_out(acc[2 * i], acc[2 * i + 1], p.out_dtype);
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + row * HEAD_DIM + lane * VEC;
+    if (!write_ok(p.err_word, p.out, p.out_bytes, dst, VEC * 2)) return;
     if constexpr (VEC == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }
-  if (lane == 0 && lse != nullptr) lse[row] = none ? -INFINITY : 0.69314718055994531f * (sum.M + __log2f(sum.W));
+  if (lane == 0 && p.lse != nullptr && write_ok(p.err_word, p.lse, p.lse_bytes, p.lse + row, 4))
+    p.lse[row] = none ? -INFINITY : 0.69314718055994531f * (sum.M + __log2f(sum.W));
 }
 
 }  // namespace detail
@@ -193,7 +197,7 @@ gqa_rows_merge_kernel(const RowsMergeParams p) {
     const int tok = (grp * p.tiles + t) * s.tokens + in_tile / p.G;
     if (tok >= s.nq) continue;
     const long long row = (static_cast<long long>(b) * s.nq + tok) * p.Hq + h * p.G + in_tile % p.G;
-    detail::write_row<HEAD_DIM>(sum[r], p.out, p.lse, p.out_dtype, row);
+    detail::write_row<HEAD_DIM>(sum[r], p, row);
   }
 }
 
@@ -267,7 +271,7 @@ gqa_pieces_merge_kernel(const RowsMergeParams p) {
       for (int e = 0; e < VEC; ++e) sum[0].acc[e] += w * s_acc[k][lane * VEC + e];
     }
   }
-  detail::write_row<HEAD_DIM>(sum[0], p.out, p.lse, p.out_dtype, row);
+  detail::write_row<HEAD_DIM>(sum[0], p, row);
 }
 
 // The rows of a paged launch whose triples hold many, a triple to blockIdx.x
@@ -358,16 +362,20 @@ gqa_tile_merge_kernel(const RowsMergeParams p) {
     for (int e = 0; e < 8; ++e) y[e] = none ? 0.f : sum.acc[8 * k + e] * inv;
     if (p.out_dtype == kOutF32) {
       float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
+      if (!detail::write_ok(p.err_word, p.out, p.out_bytes, dst, 32)) continue;
       dst[0] = make_float4(y[0], y[1], y[2], y[3]);
       dst[1] = make_float4(y[4], y[5], y[6], y[7]);
     } else {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = detail::pack_out(y[2 * e], y[2 * e + 1], p.out_dtype);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to) = make_uint4(w[0], w[1], w[2], w[3]);
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + to;
+      if (!detail::write_ok(p.err_word, p.out, p.out_bytes, dst, 16)) continue;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  if (unit0 == 0 && p.lse != nullptr) p.lse[row] = none ? -INFINITY : 0.69314718055994531f * (sum.M + __log2f(sum.W));
+  if (unit0 == 0 && p.lse != nullptr && detail::write_ok(p.err_word, p.lse, p.lse_bytes, p.lse + row, 4))
+    p.lse[row] = none ? -INFINITY : 0.69314718055994531f * (sum.M + __log2f(sum.W));
 }
 
 }  // namespace gqa

@@ -11,7 +11,7 @@ import torch
 
 import gqa_decode_blackwell_gb300 as g
 from gqa_decode_blackwell_gb300 import build as gbuild
-from tests.test_paged import BF16, FP16, Case, _branches, _parents, _words
+from tests.test_paged import (APPEND, BF16, FP16, FP32, STEPS, Case, Step, _branches, _ints, _parents, _randn, _words)
 from tests.test_shared_keys import _compare
 
 gpu = pytest.mark.gpu
@@ -159,3 +159,70 @@ def test_partials_lie_in_their_tiles(dev, debug, lens, news, T, H, K, d, page, d
     out, lse = c.run(causal=causal, out_dtype=out_dtype)
     assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
     _compare("partials", out, lse, c.want((lambda b: torch.ones(c.n[b], c.n[b]).tril().bool()) if causal else None, out_dtype))
+
+
+@gpu
+@pytest.mark.parametrize("i", range(len(STEPS)))
+def test_steps_write_inside_their_buffers(dev, debug, i):
+    """Tree, append, attention, merges and keep of a verification step: the bits of the release build."""
+    steps = [Step(dev, *STEPS[i], seed=70 + i) for _ in range(2)]
+    steps[0].run()
+    debug(steps[1].run)
+    a, b = ([s.tree, s.positions, s.q_out, s.out, s.lse, s.c.k, s.c.v, s.ends] for s in steps)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    steps[1].check()
+
+
+@gpu
+@pytest.mark.parametrize("lens,news,T,H,K,d,page,dtype,heads_first,dim,interleaved", APPEND)
+def test_appends_write_inside_their_buffers(dev, debug, lens, news, T, H, K, d, page, dtype, heads_first, dim, interleaved):
+    """Alone in a CTA and in groups, all runs, caches with heads first or last."""
+    c = Case(dev, lens, news, T, H, K, d, page, dtype, heads_first, seed=T)
+    new = _randn(dev, len(lens), T, H + 2 * K, d, dtype=dtype, seed=5)
+    turns = g.rotary_turns(dim, device=dev) if dim else None
+    k, v, results = c.k.clone(), c.v.clone(), []
+
+    def append():
+        out = torch.zeros_like(c.q)
+        c.k.copy_(k)
+        c.v.copy_(v)
+        g.gqa_paged_append(new[:, :, :H], new[:, :, H: H + K], new[:, :, H + K:], out, c.k, c.v, c.table, c.ln,
+                           new_lens=c.new, turns=turns, interleaved=interleaved)
+        results.append((out, c.k.clone(), c.v.clone()))
+
+    append()
+    debug(append)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@gpu
+@pytest.mark.parametrize("T,H,d,dim,interleaved,dtype", [
+    (9, 32, 128, 128, False, BF16), (2701, 3, 64, 20, False, FP16), (2703, 9, 64, 64, True, FP32),
+    (300, 65, 256, 254, False, BF16), (1, 1, 64, 2, False, FP32), (2709, 2, 64, 2, False, FP32)])
+def test_rotations_write_inside_their_buffers(dev, debug, T, H, d, dim, interleaved, dtype):
+    """Into part of a larger tensor."""
+    x, turns = _randn(dev, T, H, d, dtype=dtype, seed=T), g.rotary_turns(dim, device=dev)
+    positions = torch.arange(T, dtype=torch.int32, device=dev)
+    want = g.rotary(x, positions, turns, interleaved=interleaved)
+    into = torch.full((T, H + 1, d), 7.0, dtype=dtype, device=dev)
+    debug(lambda: g.gqa_rotary_apply(x, positions, turns, into[:, 1:], interleaved=interleaved))
+    assert torch.equal(into[:, 1:], want) and (into[:, 0] == 7).all()
+
+
+@gpu
+def test_bad_numbers_in_the_checked_build(dev):
+    """Pages, parents and branches out of range are flagged as what they are, as by the release build."""
+    gbuild.build_debug()
+    release, g._lib = g.lib(), g.load_library(gbuild.DEBUG_LIB)
+    try:
+        c = Case(dev, [300, 200], None, 20, 8, 2, 64, 16, seed=11)
+        c.table[1, 12] = -1                                            # positions 192 to 207
+        k = _randn(dev, 2, 20, 2, 64, seed=8)
+        for call in (lambda: g.gqa_paged_append(None, k, k, None, c.k, c.v, c.table, c.ln), c.run,
+                     lambda: g.gqa_paged_keep(c.k, c.v, c.table, c.ln, _ints(dev, [[1], [19]]), _ints(dev, [1, 1]), tokens=20),
+                     lambda: g.gqa_paged_keep(c.k, c.v, c.table, c.ln, _ints(dev, [[1], [20]]), _ints(dev, [1, 1]), tokens=20)):
+            call()
+            assert g.gqa_decode_get_error() == g.GQA_ERR_BAD_INDEX
+        assert g.gqa_decode_get_error() == g.GQA_OK
+    finally:
+        g._lib = release
