@@ -254,12 +254,18 @@ gqa_status_t run_rows(DeviceState* st, const RowsLaunch& r, const void* q, const
   p.plan = r.plan;
   if (paged != nullptr) {
     // Small pages are bound by the warp that issues their boxes.  Measured on GB300, us
-    // a call of 16 sequences with 134 MB of keys and of values (one loader, two): one token,
-    // heads of 64, pages of 16 152 and 103, of 32 107 and 104 (heads first 107 and 89), of 64
-    // 98 and 99 (95 and 89), of 128 97 and 99 (90 and 88); 64 tokens, two tiles that their
-    // own work bounds, pages of 32 157 and 165.  (One tile, which has no warp to spare: heads
-    // of 128, pages of 16 91 and 87, but 16 trees of 26 tokens in pages of 32 56.5 and 57.6,
-    // with either number of loaders, for the warp alone.)
+    // a call of 16 sequences of 8192 keys, 32 / 8 heads (one loader, two):
+    //   64, split keys, 1 token      pages of 16 83 and 56, of 32 60 and 51, of 64 54 and 50
+    //   64, split keys, 26 tokens    88 and 62, 64 and 55, 58 and 55
+    //   64, 64 tokens                95 and 88, 87 and 88, 87 and 88
+    //   128, 64 tokens               116 and 111, 112 and 111, 111 and 111
+    // and of 130 sequences of 1024 keys, which at 128 take two tiles however few their rows:
+    //   128, split keys, 9 tokens    112 and 112, 105 and 109, 104 and 108
+    //   128, 26 tokens               120 and 120, 119 and 120, 119 and 119
+    // With pages of 128 split keys of 64 take 97 and 99 (16 sequences of 16384 keys).
+    // (One tile has no warp to spare: heads of 128, pages of 16 91 and 87, but 16 trees
+    // of 26 tokens in pages of 32 56.5 and 57.6, with either number of loaders, for the
+    // warp alone.)
     const int page = paged->geometry->page_size;
     p.pages = paged->keys;
     p.two_loaders = page == 16 || (r.head_dim == 64 && r.s[0].split_keys != 0 && page <= 64) ? 1 : 0;
