@@ -611,10 +611,10 @@ def _recorded_rotation():
         class Rotation(torch.autograd.Function):
             @staticmethod
             def forward(ctx, x, positions, turns, interleaved, inverse, magnitude):
-                ctx.save_for_backward(positions, turns)
-                ctx.how = interleaved, inverse, magnitude
                 out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
                 gqa_rotary_apply(x, positions, turns, out, interleaved=interleaved, inverse=inverse, magnitude=magnitude)
+                ctx.save_for_backward(positions, turns)
+                ctx.how = interleaved, inverse, magnitude
                 return out
 
             @staticmethod

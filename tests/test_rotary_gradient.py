@@ -103,3 +103,17 @@ def test_gradient_in_a_graph(dev):
         assert torch.equal(y, g.rotary(x, positions, turns))
         assert torch.equal(grad, g.rotary(w, positions, turns, inverse=True))
     assert other.requires_grad
+
+
+@gpu
+def test_refusals_are_the_same_with_a_gradient(dev):
+    x, _, positions, turns = _inputs(dev, BF16)
+    for bad in (None, positions.long(), positions[:-1], positions.cpu(), "a tensor"):
+        errors = []
+        for t in (x, x.detach()):
+            with pytest.raises((TypeError, ValueError)) as e:
+                g.rotary(t, bad, turns)
+            errors.append((type(e.value), str(e.value)))
+        assert errors[0] == errors[1]
+    with pytest.raises(g.GQAError):
+        g.rotary(x, positions, turns, magnitude=-1.0)
